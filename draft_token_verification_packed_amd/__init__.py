@@ -13,6 +13,11 @@ Entry points mirror the C ABI in include/vspec_verify.h:
     verify_sampled(logits, row_offsets, row_owner, draft_tokens,
                    temperature, top_k, top_p, min_p, seed, offset=0)
     draft_confidence(draft_logits, selected=None)
+    sample_rows(logits, temperature, top_k, top_p, min_p, uniforms)
+    top_logits(logits, k, temperature=1.0)
+    distill_loss(student_logits, teacher_ids, teacher_logits, teacher_lse=None, temperature=1.0)   (autograd)
+    distill_loss_grad(student_logits, teacher_ids, teacher_logits, row_weight=None, teacher_lse=None, temperature=1.0)
+    distill_forward / distill_backward: the two halves of distill_loss
     allocate_verify(confidence, draft_tokens, num_requests, num_drafts, row_budget)
     Goodput(max_steps, window_size=20, update_interval=5, switch_min_gain=0.05)
         .observe(accepted_len, verify_len), .step(cost_ms, batch_size)   (host)
@@ -65,12 +70,23 @@ class Relax(ctypes.Structure):
                 ("num_protected", ctypes.c_int32)]
 
 
+class Distill(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("ld", ctypes.c_int64), ("num_rows", ctypes.c_int32), ("num_top", ctypes.c_int32),
+                ("ids", ctypes.c_void_p), ("top", ctypes.c_void_p), ("teacher_lse", ctypes.c_void_p),
+                ("temperature", ctypes.c_float)]
+
+
 MAX_PROTECTED = 256
+MAX_TOP = 256
+DISTILL_STATE = 5
 
 SYMBOLS = ("vsv_workspace_bytes", "vsv_workspace_init", "vsv_verify_greedy", "vsv_verify_greedy_relaxed",
            "vsv_verify_greedy_static",
            "vsv_verify_sampled",
-           "vsv_verify_probabilistic", "vsv_draft_confidence", "vsv_allocate_verify", "vsv_goodput_init", "vsv_goodput_observe",
+           "vsv_verify_probabilistic", "vsv_draft_confidence", "vsv_sample_rows", "vsv_top_logits",
+           "vsv_distill_workspace_bytes", "vsv_distill_forward", "vsv_distill_backward", "vsv_distill_grad",
+           "vsv_allocate_verify", "vsv_goodput_init", "vsv_goodput_observe",
            "vsv_goodput_step", "vsv_goodput_select", "vsv_status_string", "vsv_test_withhold_row_word", "vsv_version")
 
 GOODPUT_MAX_STEPS = 32
@@ -117,6 +133,19 @@ def lib():
     L.vsv_verify_probabilistic.restype = ctypes.c_int
     L.vsv_draft_confidence.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp]
     L.vsv_draft_confidence.restype = ctypes.c_int
+    L.vsv_sample_rows.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.vsv_sample_rows.restype = ctypes.c_int
+    L.vsv_top_logits.argtypes = [vp, i32, i32, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]
+    L.vsv_top_logits.restype = ctypes.c_int
+    dp = ctypes.POINTER(Distill)
+    L.vsv_distill_workspace_bytes.argtypes = [i32, i32, i32]
+    L.vsv_distill_workspace_bytes.restype = sz
+    L.vsv_distill_forward.argtypes = [dp, vp, vp, vp, vp, sz, vp]
+    L.vsv_distill_forward.restype = ctypes.c_int
+    L.vsv_distill_backward.argtypes = [dp, vp, vp, vp, i64, vp]
+    L.vsv_distill_backward.restype = ctypes.c_int
+    L.vsv_distill_grad.argtypes = [dp, vp, vp, vp, i64, vp, vp, sz, vp]
+    L.vsv_distill_grad.restype = ctypes.c_int
     L.vsv_allocate_verify.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     L.vsv_allocate_verify.restype = ctypes.c_int
     gp = ctypes.POINTER(GoodputState)
@@ -382,6 +411,228 @@ def draft_confidence(draft_logits, selected=None, vocab=None, stream=None):
     _check(lib().vsv_draft_confidence(_ptr(draft_logits), dtype, V, ld, D, _ptr(selected), _ptr(conf),
                                       _ptr(lse), _ptr(flag), _stream(stream)))
     return conf, lse, flag
+
+
+class _on:
+    """The device of a call's tensors as the current one, and the stream its
+    outputs are allocated and its kernels run on: `stream`, or the device's
+    current stream. Kernels launch on the current device, so a call on
+    another device's tensors switches to it."""
+
+    __slots__ = ("device", "stream", "other", "_back", "_swap")
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.other = stream is not None and stream != torch.cuda.current_stream(device)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        if self.stream.device != device:
+            raise ValueError("the stream belongs to %s, the tensors to %s" % (self.stream.device, device))
+
+    def __enter__(self):
+        self._swap = self._back = None
+        if self.other:
+            self._swap = torch.cuda.stream(self.stream)   # also switches the device
+            self._swap.__enter__()
+        elif self.device.index != torch.cuda.current_device():
+            self._back = torch.cuda.device(self.device)
+            self._back.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in (self._swap, self._back):
+            if c is not None:
+                c.__exit__(*exc)
+        return False
+
+    def keep(self, *tensors):
+        if self.other:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, the logits on %s" % (name, t.device, device))
+
+
+def _flag(error_flag, device):
+    """The caller's sticky error word, if given."""
+    if error_flag is not None:
+        _vec(error_flag, 1, torch.int32, "error_flag")
+        _same_device(device, error_flag=error_flag)
+    return error_flag
+
+
+def sample_rows(logits, temperature, top_k, top_p, min_p, uniforms, vocab=None, stream=None):
+    """One token per row of logits, drawn at the given numbers (vsv_sample_rows).
+
+    `temperature` (0: arg-max), `top_p`, `min_p` and `uniforms` (in [0, 1))
+    are float32 vectors with one value per row, `top_k` an int32 one. Returns
+    a dict of device vectors: token, logprob (under the filtered law the
+    token was drawn from), lse (of the row over its temperature) and
+    error_flag."""
+    dtype, V, ld = _logits(logits, vocab)
+    R, dev = logits.shape[0], logits.device
+    for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (uniforms, "uniforms")):
+        _vec(t, R, torch.float32, n)
+    _vec(top_k, R, torch.int32, "top_k")
+    _same_device(dev, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, uniforms=uniforms)
+    on = _on(dev, stream)
+    with on as s:
+        out = dict(token=torch.empty(R, dtype=torch.int32, device=dev),
+                   logprob=torch.empty(R, dtype=torch.float32, device=dev),
+                   lse=torch.empty(R, dtype=torch.float32, device=dev),
+                   error_flag=torch.zeros(1, dtype=torch.int32, device=dev))
+        on.keep(logits, temperature, top_k, top_p, min_p, uniforms)
+        _check(lib().vsv_sample_rows(_ptr(logits), dtype, V, ld, R, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                                     _ptr(min_p), _ptr(uniforms), _ptr(out["token"]), _ptr(out["logprob"]),
+                                     _ptr(out["lse"]), _ptr(out["error_flag"]), s))
+    return out
+
+
+def top_logits(logits, k, temperature=1.0, vocab=None, stream=None):
+    """The k first logits of every row (value descending, lowest token first;
+    vsv_top_logits). Returns a dict of device tensors: values [R, k] float32,
+    ids [R, k] int32, lse [R] of the rows over `temperature`, error_flag.
+    values, ids and lse are what distill_loss takes of a teacher."""
+    dtype, V, ld = _logits(logits, vocab)
+    R, dev, k = logits.shape[0], logits.device, int(k)
+    if not 1 <= k <= min(V, MAX_TOP):
+        raise ValueError("k must lie in 1 .. min(vocab, %d)" % MAX_TOP)
+    on = _on(dev, stream)
+    with on as s:
+        out = dict(values=torch.empty((R, k), dtype=torch.float32, device=dev),
+                   ids=torch.empty((R, k), dtype=torch.int32, device=dev),
+                   lse=torch.empty(R, dtype=torch.float32, device=dev),
+                   error_flag=torch.zeros(1, dtype=torch.int32, device=dev))
+        on.keep(logits)
+        _check(lib().vsv_top_logits(_ptr(logits), dtype, V, ld, R, k, float(temperature), _ptr(out["values"]),
+                                    _ptr(out["ids"]), _ptr(out["lse"]), _ptr(out["error_flag"]), s))
+    return out
+
+
+def _distill_args(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature):
+    dtype, V, ld = _logits(student_logits, None)
+    N, dev = student_logits.shape[0], student_logits.device
+    if teacher_ids.dim() != 2 or teacher_ids.shape[0] != N or not 1 <= teacher_ids.shape[1] <= MAX_TOP:
+        raise ValueError("teacher_ids must be [rows, 1 .. %d]" % MAX_TOP)
+    K = teacher_ids.shape[1]
+    for t, dt, n in ((teacher_ids, torch.int32, "teacher_ids"), (teacher_logits, torch.float32, "teacher_logits")):
+        if not t.is_cuda or t.dtype != dt or t.shape != (N, K) or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s CUDA matrix [%d, %d]" % (n, dt, N, K))
+    if teacher_lse is not None:
+        _vec(teacher_lse, N, torch.float32, "teacher_lse")
+    _same_device(dev, teacher_ids=teacher_ids, teacher_logits=teacher_logits, teacher_lse=teacher_lse)
+    return Distill(_ptr(student_logits), dtype, V, ld, N, K, _ptr(teacher_ids), _ptr(teacher_logits),
+                   _ptr(teacher_lse), float(temperature))
+
+
+def _distill_scratch(d, dev):
+    n = int(lib().vsv_distill_workspace_bytes(d.num_rows, d.vocab, d.dtype))
+    return torch.empty(n // 8, dtype=torch.float64, device=dev) if n else None, n
+
+
+def _row_weight(row_weight, d, dev):
+    if row_weight is not None:
+        _vec(row_weight, d.num_rows, torch.float32, "row_weight")
+        _same_device(dev, row_weight=row_weight)
+    return row_weight
+
+
+def distill_forward(student_logits, teacher_ids, teacher_logits, teacher_lse=None, temperature=1.0, error_flag=None,
+                    stream=None):
+    """(loss [N] float32, state [N, DISTILL_STATE] float64) of every student row
+    (vsv_distill_forward); `state` is what distill_backward takes. Device
+    conditions set bits in `error_flag` (int32 [1]) if given."""
+    d = _distill_args(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    dev = student_logits.device
+    _flag(error_flag, dev)
+    on = _on(dev, stream)
+    with on as s:
+        loss = torch.empty(d.num_rows, dtype=torch.float32, device=dev)
+        state = torch.empty((d.num_rows, DISTILL_STATE), dtype=torch.float64, device=dev)
+        ws, n = _distill_scratch(d, dev)
+        on.keep(student_logits, teacher_ids, teacher_logits, teacher_lse, error_flag)
+        _check(lib().vsv_distill_forward(ctypes.byref(d), _ptr(loss), _ptr(state), _ptr(error_flag), _ptr(ws), n, s))
+    return loss, state
+
+
+def distill_backward(row_weight, student_logits, teacher_ids, teacher_logits, state, teacher_lse=None,
+                     temperature=1.0, stream=None):
+    """Gradient [N, V] of sum(row_weight * loss) in the student's logits, in
+    their type (vsv_distill_backward)."""
+    d = _distill_args(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    dev = student_logits.device
+    _row_weight(row_weight, d, dev)
+    if (state.dtype != torch.float64 or state.shape != (d.num_rows, DISTILL_STATE) or not state.is_contiguous() or
+            state.device != dev):
+        raise ValueError("state must be the one distill_forward returned for these rows")
+    on = _on(dev, stream)
+    with on as s:
+        grad = torch.empty((d.num_rows, d.vocab), dtype=student_logits.dtype, device=dev)
+        on.keep(row_weight, student_logits, teacher_ids, teacher_logits, teacher_lse, state)
+        _check(lib().vsv_distill_backward(ctypes.byref(d), _ptr(state), _ptr(row_weight), _ptr(grad), d.vocab, s))
+    return grad
+
+
+def distill_loss_grad(student_logits, teacher_ids, teacher_logits, row_weight=None, teacher_lse=None,
+                      temperature=1.0, error_flag=None, stream=None):
+    """(loss [N], gradient [N, V] of sum(row_weight * loss)) in one call
+    (vsv_distill_grad); row_weight None counts 1 for every row."""
+    d = _distill_args(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    dev = student_logits.device
+    _row_weight(row_weight, d, dev)
+    _flag(error_flag, dev)
+    on = _on(dev, stream)
+    with on as s:
+        loss = torch.empty(d.num_rows, dtype=torch.float32, device=dev)
+        grad = torch.empty((d.num_rows, d.vocab), dtype=student_logits.dtype, device=dev)
+        ws, n = _distill_scratch(d, dev)
+        on.keep(student_logits, teacher_ids, teacher_logits, teacher_lse, row_weight, error_flag)
+        _check(lib().vsv_distill_grad(ctypes.byref(d), _ptr(row_weight), _ptr(loss), _ptr(grad), d.vocab,
+                                      _ptr(error_flag), _ptr(ws), n, s))
+    return loss, grad
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, student, ids, top, lse, temperature, error_flag):
+        loss, state = distill_forward(student, ids, top, lse, temperature, error_flag)
+        ctx.save_for_backward(student, ids, top, lse, state)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        student, ids, top, lse, state = ctx.saved_tensors
+        # a summed loss hands down one number for every row
+        grad = distill_backward(g.contiguous(), student, ids, top, state, lse, ctx.temperature)
+        return grad, None, None, None, None, None
+
+
+def distill_loss(student_logits, teacher_ids, teacher_logits, teacher_lse=None, temperature=1.0, vocab=None,
+                 error_flag=None):
+    """Distillation loss of every student row [N, V] (bfloat16 or float32)
+    against a teacher's top logits, differentiable in the student's logits.
+
+    `teacher_ids` (int32) and `teacher_logits` (float32) are [N, K], K at most
+    MAX_TOP, as top_logits returns them; a negative id marks an unused entry,
+    and a row without any has loss 0 and gradient 0. Without `teacher_lse` the
+    teacher is renormalised over its entries; with it (the teacher's
+    log-sum-exp at the same temperature) the rest of its mass is set against
+    the student's mass outside the row's ids. Losses are float32 [N]; runs on
+    the current stream, its backward on the same one. The teacher gets no
+    gradient. Columns at or beyond `vocab` are not part of the rows."""
+    if vocab is not None and int(vocab) != student_logits.shape[1]:
+        if not 1 <= int(vocab) <= student_logits.shape[1]:
+            raise ValueError("vocab exceeds the logits width")
+        student_logits = student_logits[:, :int(vocab)]
+    if student_logits.dim() == 2 and student_logits.shape[0] > 1 and student_logits.stride(0) < student_logits.shape[1]:
+        student_logits = student_logits.contiguous()   # one row standing for several
+    return _DistillLoss.apply(student_logits, teacher_ids, teacher_logits, teacher_lse, float(temperature), error_flag)
 
 
 def _alloc_outputs(B, K, G, dev, with_drafts):

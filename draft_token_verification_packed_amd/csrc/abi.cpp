@@ -9,6 +9,7 @@
 #include "allocate.hpp"
 #include "kernels.hpp"
 #include "probabilistic.hpp"
+#include "rows.hpp"
 
 using vsv::VerifyArgs;
 
@@ -87,6 +88,42 @@ vsv_status prepare(const vsv_batch* b, const vsv_outputs* o, void* ws, size_t ws
   v.ws_part = reinterpret_cast<uint64_t*>(w + vsv::kWsAlign + vsv::ws_row_bytes(b->num_rows));
   v.cus = device_cus();
   return VSV_OK;
+}
+
+// Checks of a matrix of logits given by itself.
+bool rows_ok(const void* p, int32_t dtype, int32_t vocab, int64_t ld, int32_t rows) {
+  if (!dtype_ok(dtype) || vocab < 1 || vocab > vsv::kMaxVocab || ld < vocab) return false;
+  if (static_cast<int64_t>(vocab) * static_cast<int64_t>(elem_size(dtype)) > vsv::kMaxRowBytes) return false;
+  return p && aligned(p, elem_size(dtype)) && ld <= (INT64_MAX / 4) / rows;
+}
+
+// Checks of a distillation's inputs; fills the shared launch args. The
+// caller has dealt with num_rows == 0.
+vsv_status prepare_distill(const vsv_distill* d, vsv::DistillArgs* a) {
+  if (d->num_top < 1 || d->num_top > VSV_MAX_TOP || !d->ids || !d->top) return VSV_EINVAL;
+  if (!(d->temperature > 0.f) || !(d->temperature < INFINITY)) return VSV_EINVAL;
+  if (!rows_ok(d->logits, d->dtype, d->vocab, d->ld, d->num_rows)) return VSV_EINVAL;
+  *a = vsv::DistillArgs{};
+  a->x = vsv::RowsIn{d->logits, d->ld, d->vocab, d->num_rows, d->dtype};
+  a->ids = d->ids;
+  a->top = d->top;
+  a->tlse = d->teacher_lse;
+  a->K = d->num_top;
+  a->c = static_cast<float>(1.44269504088896340736 / static_cast<double>(d->temperature));
+  a->inv_t = 1.0 / static_cast<double>(d->temperature);
+  a->parts = vsv::distill_parts(d->num_rows, d->vocab, d->dtype);
+  return VSV_OK;
+}
+
+vsv_status distill_scratch(vsv::DistillArgs* a, void* ws, size_t bytes) {
+  if (a->parts < 2) return VSV_OK;
+  if (!ws || !aligned(ws, 8) || bytes < vsv_distill_workspace_bytes(a->x.N, a->x.V, a->x.dtype)) return VSV_EWORKSPACE;
+  a->part = static_cast<double*>(ws);
+  return VSV_OK;
+}
+
+bool distill_grad_ok(const vsv::DistillArgs& a, const void* grad, int64_t grad_ld) {
+  return grad && aligned(grad, elem_size(a.x.dtype)) && grad_ld >= a.x.V && grad_ld <= (INT64_MAX / 4) / a.x.N;
 }
 
 }  // namespace
@@ -194,6 +231,90 @@ vsv_status vsv_draft_confidence(const void* draft_logits, int32_t dtype, int32_t
   return vsv::launch_confidence(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 
+vsv_status vsv_sample_rows(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows,
+                           const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                           const float* uniform, int32_t* token, float* logprob, float* lse, int32_t* error_flag,
+                           hipStream_t stream) {
+  if (num_rows < 0) return VSV_EINVAL;
+  if (num_rows == 0) return VSV_OK;
+  if (!rows_ok(logits, dtype, vocab, ld, num_rows)) return VSV_EINVAL;
+  if (!temperature || !top_k || !top_p || !min_p || !uniform || !token) return VSV_EINVAL;
+  const vsv::DrawArgs a{{logits, ld, vocab, num_rows, dtype}, temperature, top_k, top_p, min_p, uniform,
+                        token, logprob, lse, error_flag};
+  return vsv::launch_draw(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
+vsv_status vsv_top_logits(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows, int32_t k,
+                          float temperature, float* values, int32_t* ids, float* lse, int32_t* error_flag,
+                          hipStream_t stream) {
+  if (num_rows < 0) return VSV_EINVAL;
+  if (num_rows == 0) return VSV_OK;
+  if (!rows_ok(logits, dtype, vocab, ld, num_rows) || !values || !ids) return VSV_EINVAL;
+  if (k < 1 || k > VSV_MAX_TOP || k > vocab) return VSV_EINVAL;
+  if (!(temperature > 0.f) || !(temperature < INFINITY)) return VSV_EINVAL;
+  const vsv::TopArgs a{{logits, ld, vocab, num_rows, dtype}, k,
+                       static_cast<float>(1.44269504088896340736 / static_cast<double>(temperature)),
+                       values, ids, lse, error_flag};
+  return vsv::launch_top(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
+size_t vsv_distill_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtype) {
+  if (num_rows < 1 || vocab < 1 || !dtype_ok(dtype)) return 0;
+  const size_t parts = static_cast<size_t>(vsv::distill_parts(num_rows, vocab, dtype));
+  return parts < 2 ? 0 : static_cast<size_t>(num_rows) * (parts * vsv::kPartDoubles + vsv::kStateWords) * sizeof(double);
+}
+
+vsv_status vsv_distill_forward(const vsv_distill* d, float* loss, double* state, int32_t* error_flag, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+  if (!d || d->num_rows < 0) return VSV_EINVAL;
+  if (d->num_rows == 0) return VSV_OK;
+  vsv::DistillArgs a;
+  vsv_status st = prepare_distill(d, &a);
+  if (st != VSV_OK) return st;
+  if (!loss) return VSV_EINVAL;
+  st = distill_scratch(&a, workspace, workspace_bytes);
+  if (st != VSV_OK) return st;
+  a.loss = loss;
+  a.state = state;
+  a.error_flag = error_flag;
+  return vsv::launch_distill_forward(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
+vsv_status vsv_distill_backward(const vsv_distill* d, const double* state, const float* weight, void* grad,
+                                int64_t grad_ld, hipStream_t stream) {
+  if (!d || d->num_rows < 0) return VSV_EINVAL;
+  if (d->num_rows == 0) return VSV_OK;
+  vsv::DistillArgs a;
+  const vsv_status st = prepare_distill(d, &a);
+  if (st != VSV_OK) return st;
+  if (!state || !distill_grad_ok(a, grad, grad_ld)) return VSV_EINVAL;
+  a.state = const_cast<double*>(state);
+  a.weight = weight;
+  a.grad = grad;
+  a.grad_ld = grad_ld;
+  return vsv::launch_distill_backward(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
+vsv_status vsv_distill_grad(const vsv_distill* d, const float* weight, float* loss, void* grad, int64_t grad_ld,
+                            int32_t* error_flag, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!d || d->num_rows < 0) return VSV_EINVAL;
+  if (d->num_rows == 0) return VSV_OK;
+  vsv::DistillArgs a;
+  vsv_status st = prepare_distill(d, &a);
+  if (st != VSV_OK) return st;
+  if (!loss || !distill_grad_ok(a, grad, grad_ld)) return VSV_EINVAL;
+  st = distill_scratch(&a, workspace, workspace_bytes);
+  if (st != VSV_OK) return st;
+  a.loss = loss;
+  a.weight = weight;
+  a.grad = grad;
+  a.grad_ld = grad_ld;
+  a.error_flag = error_flag;
+  // with parts the rows' states pass through the scratch, behind the sums
+  if (a.parts > 1) a.state = a.part + static_cast<size_t>(a.x.N) * a.parts * vsv::kPartDoubles;
+  return vsv::launch_distill_grad(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
 vsv_status vsv_allocate_verify(const float* confidence, const int32_t* draft_tokens, int32_t num_requests,
                                int32_t num_drafts, int32_t row_budget, int32_t* verify_len, int32_t* row_offsets,
                                int32_t* row_owner, int32_t* row_source, int32_t* packed_drafts, float* prefix,
@@ -229,6 +350,6 @@ vsv_status vsv_test_withhold_row_word(int32_t row) {
   return VSV_OK;
 }
 
-int32_t vsv_version(void) { return 103; }
+int32_t vsv_version(void) { return 104; }
 
 }  // extern "C"

@@ -1,0 +1,78 @@
+// Interface between the C ABI (abi.cpp) and the logit-row operators next to
+// verification: drawing tokens, a teacher's top logits, distillation.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "vspec_verify.h"
+
+namespace vsv {
+
+// A packed matrix of logits.
+struct RowsIn {
+  const void* p;
+  int64_t ld;
+  int32_t V, N, dtype;
+};
+
+struct DistillArgs {
+  RowsIn x;                // the student's rows
+  const int32_t* ids;      // [N, K]
+  const float* top;        // [N, K]
+  const float* tlse;       // [N] or NULL: renormalise over the entries
+  int32_t K;
+  float c;                 // log2(e) / T
+  double inv_t;            // 1 / T
+  const float* weight;     // [N] upstream gradient of the losses
+  float* loss;             // [N]
+  double* state;           // [N, kStateWords]
+  void* grad;              // [N, grad_ld], the student's type
+  int64_t grad_ld;
+  int32_t* error_flag;
+  double* part;            // [N, parts, kPartDoubles] when parts > 1
+  int32_t parts;
+};
+
+// What the backward pass needs of a row: the student's exponent reference and
+// one over its sum relative to that, the scale of the unnamed tokens, the
+// teacher's total, and the teacher's log-sum-exp (over the entries where none
+// was given).
+constexpr int kStateWords = VSV_DISTILL_STATE;
+constexpr int kPartDoubles = 3;   // exponent reference, sum outside the ids, sum over the ids
+
+// Parts a row is cut into, so that a call of few rows still gives every CU
+// something to stream; a function of the call's sizes alone, because the
+// workspace size depends on it.
+int32_t distill_parts(int32_t num_rows, int32_t vocab, int32_t dtype);
+
+hipError_t launch_distill_forward(const DistillArgs& a, hipStream_t s);
+hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s);
+hipError_t launch_distill_grad(const DistillArgs& a, hipStream_t s);
+
+struct TopArgs {
+  RowsIn x;
+  int32_t k;
+  float c;                 // log2(e) / T
+  float* values;           // [N, k]
+  int32_t* ids;            // [N, k]
+  float* lse;              // [N] or NULL
+  int32_t* error_flag;
+};
+hipError_t launch_top(const TopArgs& a, hipStream_t s);
+
+struct DrawArgs {
+  RowsIn x;
+  const float* temperature;   // [N] each
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* uniform;
+  int32_t* token;
+  float* logprob;
+  float* lse;
+  int32_t* error_flag;
+};
+hipError_t launch_draw(const DrawArgs& a, hipStream_t s);
+
+}  // namespace vsv

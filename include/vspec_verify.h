@@ -251,6 +251,105 @@ vsv_status vsv_draft_confidence(const void* draft_logits, int32_t dtype,
                                 float* lse, int32_t* error_flag,
                                 hipStream_t stream);
 
+/* One token per row of logits, drawn with a given random number: the draft
+ * side's draw (and any other row's, such as the first token after a prompt).
+ * Row r of `num_rows` rows [num_rows, ld] has its own temperature[r] (0 = the
+ * lowest-index arg-max), top_k[r], top_p[r] and min_p[r], and the draw is the
+ * inverse CDF at uniform[r] in [0, 1): filters, order and draw are those of
+ * vsv_verify_sampled, so the same number gives the same token. The sums that
+ * decide a cut or a draw hold to about 1e-11 of the row's total.
+ *   token [num_rows]    the drawn token
+ *   logprob [num_rows]  log-probability of the token under the law it was
+ *                       drawn from (after temperature and filters; 0 when
+ *                       the temperature is 0), or NULL
+ *   lse [num_rows]      log-sum-exp of x / T over the whole row (of x when
+ *                       the temperature is 0), or NULL: x[t] / T - lse is the
+ *                       log-probability without the filters
+ * Needs no workspace; calls are independent of each other. VSV_FLAG_LOGITS:
+ * a NaN or +inf logit or no finite one (token 0); VSV_FLAG_PARAMS: a
+ * parameter or number outside its range (temperature counts as 0, a filter
+ * as off, the number as 0).
+ * Errors: VSV_EINVAL (num_rows < 0, NULL logits, parameters, uniform or
+ * token, vocab outside 1 .. 2^30 - 1 or a row of 2 GiB, ld < vocab,
+ * misaligned logits, unknown dtype), VSV_EHIP. */
+vsv_status vsv_sample_rows(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows,
+                           const float* temperature, const int32_t* top_k, const float* top_p,
+                           const float* min_p, const float* uniform, int32_t* token, float* logprob,
+                           float* lse, int32_t* error_flag, hipStream_t stream);
+
+/* The first k logits of every row in the order (value desc, index asc), with
+ * the row's log-sum-exp: what vsv_distill reads of a teacher, taken from the
+ * target rows that verification has just read.
+ *   values [num_rows, k]  the logits, widened to float
+ *   ids [num_rows, k]     their tokens
+ *   lse [num_rows]        log-sum-exp of x / temperature, or NULL
+ * -inf logits count as the last. A NaN or +inf logit, or a row whose largest
+ * x / temperature is beyond float range, sets VSV_FLAG_LOGITS (ids stay
+ * inside the row). Needs no workspace.
+ * Errors: VSV_EINVAL (num_rows < 0, NULL logits, values or ids, k outside
+ * 1 .. min(vocab, VSV_MAX_TOP), temperature not positive and finite, vocab,
+ * ld, alignment and dtype as above), VSV_EHIP. */
+#define VSV_MAX_TOP 256
+vsv_status vsv_top_logits(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows,
+                          int32_t k, float temperature, float* values, int32_t* ids, float* lse,
+                          int32_t* error_flag, hipStream_t stream);
+
+/* Distillation of a draft head from the target's top logits. With y a
+ * student row, q = softmax(y / T), and a row's used entries (ids[r, k] >= 0;
+ * the same id may appear more than once):
+ *   teacher_lse NULL:  t = softmax(top / T) over the row's entries,
+ *                      loss = sum_k t_k (ln t_k - ln q_k)
+ *   teacher_lse given: t_k = exp(top_k / T - teacher_lse), what they leave of
+ *                      one, t_r = max(0, 1 - sum t), stands against the
+ *                      student's mass q_r outside the row's ids:
+ *                      loss = sum_k t_k (ln t_k - ln q_k) + t_r (ln t_r - ln q_r)
+ * (the Kullback-Leibler divergence, no factor T^2). Entries of weight 0 add
+ * nothing. A row without a used entry has loss 0 and gradient 0 and its
+ * logits are not read. */
+typedef struct {
+  const void* logits;       /* [num_rows, ld] the student's rows                */
+  int32_t dtype;            /* vsv_dtype                                        */
+  int32_t vocab;            /* as in vsv_batch                                  */
+  int64_t ld;
+  int32_t num_rows;         /* >= 0                                             */
+  int32_t num_top;          /* entries per row, 1 .. VSV_MAX_TOP                */
+  const int32_t* ids;       /* [num_rows, num_top] teacher's tokens; < 0: unused */
+  const float* top;         /* [num_rows, num_top] teacher's logits             */
+  const float* teacher_lse; /* [num_rows] log-sum-exp of the teacher's whole    */
+                            /* row / T, or NULL                                 */
+  float temperature;        /* T, positive and finite                           */
+} vsv_distill;
+
+/* Bytes of scratch that vsv_distill_forward and vsv_distill_grad need (0 for
+ * batches of many rows). It needs no initial value and nothing in it outlives
+ * the call. */
+size_t vsv_distill_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtype);
+
+/* Loss of every row, and the state vsv_distill_backward takes (doubles
+ * [num_rows, VSV_DISTILL_STATE], or NULL). VSV_FLAG_LOGITS: a NaN or +inf
+ * logit in a row that has entries, or none finite; VSV_FLAG_TOKEN: an id at
+ * or beyond vocab (counts as unused).
+ * Errors: VSV_EINVAL (NULL student, ids, top or loss; sizes, alignment,
+ * dtype, temperature), VSV_EWORKSPACE, VSV_EHIP. */
+#define VSV_DISTILL_STATE 5
+vsv_status vsv_distill_forward(const vsv_distill* d, float* loss, double* state, int32_t* error_flag,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of sum_r weight[r] loss[r] in the student's logits, in their type,
+ * rows grad_ld apart (columns beyond vocab are left as they are); weight NULL
+ * counts 1 for every row. A row of weight 0 gets zeros and is not read. `d`
+ * and `state` as in the forward call; grad may not overlap the logits.
+ * Errors: VSV_EINVAL (as vsv_distill_forward, NULL state or grad,
+ * grad_ld < vocab, misaligned grad), VSV_EHIP. */
+vsv_status vsv_distill_backward(const vsv_distill* d, const double* state, const float* weight, void* grad,
+                                int64_t grad_ld, hipStream_t stream);
+
+/* Both in one call, for a step whose row weights are known beforehand: the
+ * same results, and a large batch's rows cross HBM once each way.
+ * Errors: as the two above. */
+vsv_status vsv_distill_grad(const vsv_distill* d, const float* weight, float* loss, void* grad, int64_t grad_ld,
+                            int32_t* error_flag, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Adaptive target-verify allocation: how many leading drafts of each request
  * the target verifies under a padded row budget, and the packed layout of
  * those verify rows (xLLM docs, "Adaptive speculative inference": the
