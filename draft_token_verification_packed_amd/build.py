@@ -27,7 +27,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
 # probabilistic one spills 23 VGPRs (48 instead of 144 bytes of scratch per
 # lane without it; 581 instead of 609 us on the mixed B=512, K=7 batch).
 _NO_LICM = ["-mllvm", "-disable-machine-licm"]
-SOURCE_FLAGS = {"sampled.hip": _NO_LICM, "probabilistic.hip": _NO_LICM}
+SOURCE_FLAGS = {"sampled.hip": _NO_LICM, "probabilistic.hip": _NO_LICM, "draw.hip": _NO_LICM}
 
 
 def hipcc():

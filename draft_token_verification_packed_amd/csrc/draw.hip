@@ -6,14 +6,25 @@
 // survivors are a prefix of that order (the first top_k; of those the
 // shortest prefix whose weight reaches top_p of theirs; of those the tokens
 // with (x - m) / T >= ln min_p), and the token is the first whose cumulative
-// weight exceeds u times the survivors' total.
+// weight exceeds u times the survivors' total. T = 0 is the first token.
 //
 // Every cut is a comparison of sums over up to the whole row, so the sums
 // have to be better than the float sums of a softmax: a relative error of
 // 1e-7 decides the wrong token in about one row of a hundred where the law is
-// broad. Weights are 64-bit integers, rint(w 2^s) with the largest s whose
-// total cannot overflow, so sums are exact in any order and the same on every
-// run; a row of 152064 logits has s = 44 and sums within about 1e-11.
+// broad. So weights are summed as 64-bit integers, exact in any order:
+//
+// The row is streamed once. With y = 32 x / T, an element falls into bin
+// rint(y), and its weight relative to the bin's centre, exp((y - rint(y)) /
+// 32) by a polynomial in float64, is added to the bin as an integer (2^44 to
+// one for a vocabulary up to 2^18) by one LDS atomic. Bins reach from 48 T below the first group's
+// maximum to 80 T above it; lower elements weigh less than e^-48 and move no
+// cut, and a row that rises beyond is streamed again from its true maximum.
+// A scan over the 48 T below the maximum then turns bins into cumulative
+// weights, and each cut and the draw are known to within a bin or two (a cut
+// inside a bin leaves the total of what follows it known to within that
+// bin). One more pass, mostly served by the caches, gathers the elements of
+// those bins, and the exact order among them decides. Bins too full for the
+// gathered list fall back to a radix search over the whole row.
 #include "row_visit.hpp"
 #include "rows.hpp"
 
@@ -23,6 +34,22 @@ namespace {
 
 constexpr int kDrawThreads = 512;
 constexpr int kDrawUnroll = 2;
+constexpr int kBins = 4096;
+constexpr int kReach = 1536;       // bins below the maximum that count (48 T)
+constexpr double kPerT = 32.0;     // bins per T
+constexpr int kList = 4096;        // elements the gathered list holds
+constexpr int kFew = 128;          // lists decided by direct comparison
+// Beyond this |32 x / T| bins are too coarse in float64 to trust.
+constexpr double kFarBin = 4194304.0;
+
+// Sums hold to about 1e-13 of the row's weight (a weight's integer is off by
+// up to half a unit, 2^-45 of it for a vocabulary up to 2^18; the polynomial
+// by 2e-14), so two that differ by less than this share are taken as equal:
+// where weights are equal and a border falls exactly between tokens, it is
+// decided as exact sums would.
+constexpr double kEqual = 1.0 / 4398046511104.0;   // 2^-42
+
+typedef unsigned long long ull;
 
 __device__ __forceinline__ uint32_t up_key(float x) {
   const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
@@ -34,21 +61,96 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ uint64_t rank_key(float x, int e) {
   return (static_cast<uint64_t>(up_key(x)) << 32) | static_cast<uint32_t>(~e);
 }
+__device__ __forceinline__ float key_x(uint64_t k) { return key_value(static_cast<uint32_t>(k >> 32)); }
 
 template <int NT> struct DrawLds {
   static constexpr int NW = NT / kWave;
-  unsigned long long mass[256];
-  uint32_t cnt[256];
-  unsigned long long total;
-  uint64_t best;
-  int digit, bad;
-  uint64_t red[NW];
+  ull bin[kBins];              // weights; then, as doubles, cumulative weights
+  union {
+    uint32_t cnt[kBins];       // counts (top-k rows), until the cuts are located
+    uint64_t list[kList];      // rank keys of the gathered elements
+  } u;
+  ull mass[256];               // radix search
+  uint32_t num[256];
+  double w[kFew];
+  int at[kFew];
+  uint32_t mark[kReach / 32];  // bins to gather
+  ull red_u[NW];
+  double red_d[NW];
+  float red_f[NW];
+  int red_i[NW];
+  ull key[2];
+  ull kept;
+  double cut;
+  int n, before, j[8], digit[2];
 };
 
+// ---------------------------------------------------------------- bins
+
+// Position of an element among the bins: t = fma(x, s, k) with k = 1.5 2^52
+// minus an integer rounds to the bin's number in the low bits of t.
+constexpr double kMagic = 6755399441055744.0;         // 1.5 * 2^52
+constexpr uint32_t kMagicHi = 0x43380000u;
+struct Grid {
+  double s, k;
+  __device__ __forceinline__ double t(float x) const { return fma(static_cast<double>(x), s, k); }
+  // bin number, or -1 where the element lies outside the bins
+  static __device__ __forceinline__ int slot(double t) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, t);
+    const uint32_t lo = static_cast<uint32_t>(b);
+    return (static_cast<uint32_t>(b >> 32) == kMagicHi && lo < static_cast<uint32_t>(kBins)) ? static_cast<int>(lo) : -1;
+  }
+};
+
+template <typename E, int NT, int U, bool kCount>
+struct BinVisit {
+  Grid g;
+  ull* bin;
+  uint32_t* cnt;
+  double c[6];   // the polynomial's coefficients, in weight units
+  float top;     // IEEE maximum: a NaN stays
+
+  __device__ __forceinline__ void put(float x) {
+    const double t = g.t(x);
+    const uint64_t b = __builtin_bit_cast(uint64_t, t);
+    const uint32_t lo = static_cast<uint32_t>(b);
+    if (static_cast<uint32_t>(b >> 32) == kMagicHi && lo < static_cast<uint32_t>(kBins)) {
+      // r in [-1/2, 1/2]; exp(r / 32) in weight units, the integer in the low
+      // bits of a double between 2^52 and 2^53
+      const double r = fma(static_cast<double>(x), g.s, -(t - g.k));
+      double h = fma(r, c[5], c[4]);
+      h = fma(r, h, c[3]);
+      h = fma(r, h, c[2]);
+      h = fma(r, h, c[1]);
+      h = fma(r, h, c[0]);
+      atomicAdd(&bin[lo], __builtin_bit_cast(uint64_t, h) - 0x4330000000000000ull);
+      if (kCount) atomicAdd(&cnt[lo], 1u);
+    }
+  }
+  template <bool kPartial>
+  __device__ __forceinline__ void group(const u32x4* w, int v, int nvec) {
+    constexpr int N = Elem<E>::kVec;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kPartial && v + u * NT >= nvec) continue;
+      float f[N];
+      top = __builtin_elementwise_maximum(top, vec_max<E, true>(w[u], f));
+#pragma unroll
+      for (int k = 0; k < N; ++k) put(f[k]);
+    }
+  }
+  __device__ __forceinline__ void one(float x, int) {
+    top = __builtin_elementwise_maximum(top, x);
+    put(x);
+  }
+};
+
+// Elements at or above `low`, a vector at a time.
 template <typename E, int NT, int U, typename F>
-struct EachElem {
+struct EachAbove {
   F& f;
   int head;
+  float low;
   template <bool kPartial>
   __device__ __forceinline__ void group(const u32x4* w, int v, int nvec) {
     constexpr int N = Elem<E>::kVec;
@@ -56,157 +158,511 @@ struct EachElem {
     for (int u = 0; u < U; ++u) {
       if (kPartial && v + u * NT >= nvec) continue;
       float x[N];
-      Elem<E>::decode(w[u], x);
+      if (vec_max<E, true>(w[u], x) >= low) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) f(x[k], head + (v + u * NT) * N + k);
+        for (int k = 0; k < N; ++k)
+          if (x[k] >= low) f(x[k], head + (v + u * NT) * N + k);
+      }
     }
   }
-  __device__ __forceinline__ void one(float x, int e) { f(x, e); }
+  __device__ __forceinline__ void one(float x, int e) {
+    if (x >= low) f(x, e);
+  }
 };
-template <typename E, int NT, int U, typename F>
-__device__ __forceinline__ void each_elem(const E* row, int V, F&& f) {
-  EachElem<E, NT, U, F> v{f, row_head(row, V)};
-  visit_row<E, NT, U, kLoadNormal>(row, V, v);
-}
+
+// ---------------------------------------------------------------- radix search
 
 struct Weigh {
   double m, T, one;   // row maximum, temperature, 2^s
   __device__ __forceinline__ double z(float x) const { return (static_cast<double>(x) - m) / T; }
-  __device__ __forceinline__ unsigned long long operator()(float x) const {
-    return static_cast<unsigned long long>(rint(exp(z(x)) * one));
-  }
+  __device__ __forceinline__ double exact(float x) const { return exp(z(x)); }
+  __device__ __forceinline__ ull operator()(float x) const { return static_cast<ull>(rint(exact(x) * one)); }
 };
 
-// The first element in rank order with `count` elements, or a weight of
-// `target` (or more than it: strict), through it; `through` receives the
-// weight through it. A byte of the rank key at a time, the row read once per
-// byte.
-template <typename E, int NT, int U>
-__device__ uint64_t find_cut(const E* row, int V, const Weigh& w, bool by_count, int count, double target, bool strict,
-                             unsigned long long& through, DrawLds<NT>& L) {
+// A cumulative weight reaches t / exceeds t exactly where it is at least /
+// more than these.
+__device__ __forceinline__ double reach(double t) { return t - t * kEqual; }
+__device__ __forceinline__ double exceed(double t) { return t + t * kEqual; }
+
+// A cut: the first element in rank order with `count` elements through it
+// (count > 0), or a cumulative weight of `target` (strict: more than it).
+struct Cut {
+  int count;
+  bool strict;
+  double target;
+};
+
+// The cut's element among those that each(f) visits with f(x, e), all of them
+// behind elements of weight w0 and number n0; `through` receives the weight
+// through it. A byte of the rank key at a time, one visit of the elements per
+// byte; the last element is taken if none reaches the target.
+template <int NT, typename Each>
+__device__ __forceinline__ uint64_t find_cut(const Each& each, const Weigh& w, const Cut& c, double w0, int n0,
+                                             double& through, DrawLds<NT>& L) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  constexpr int kDigits = 256, DW = kDigits / kWave;
+  static_assert(NT >= kDigits, "one digit per thread");
+  // bytes that all keys share need no search
+  ull all = ~0ull, any = 0ull;
+  each([&](float x, int e) {
+    const ull key = rank_key(x, e);
+    all &= key;
+    any |= key;
+  });
+  all = wave_all(all, [](ull p, ull q) { return p & q; });
+  any = wave_all(any, [](ull p, ull q) { return p | q; });
+  lds_barrier();
+  if (tid == 0) {
+    L.mass[0] = ~0ull;
+    L.mass[1] = 0ull;
+  }
+  lds_barrier();
+  if (lane == 0) {
+    atomicAnd(&L.mass[0], all);
+    atomicOr(&L.mass[1], any);
+  }
+  lds_barrier();
+  any = L.mass[1];
+  const ull differ = L.mass[0] ^ any;
   uint64_t prefix = 0;
-  unsigned long long mass = 0;
-  unsigned long long cnt = 0;
+  ull mass = 0;
+  int num = n0;
+#pragma unroll 1
   for (int shift = 56; shift >= 0; shift -= 8) {
-    for (int b = threadIdx.x; b < 256; b += NT) {
-      L.cnt[b] = 0;
-      L.mass[b] = 0;
+    if (shift > 0 && (differ >> shift & 255) == 0) {
+      prefix |= static_cast<uint64_t>(any >> shift & 255) << shift;
+      continue;
     }
     lds_barrier();
-    each_elem<E, NT, U>(row, V, [&](float x, int e) {
+    if (tid < kDigits) {
+      L.num[tid] = 0;
+      L.mass[tid] = 0;
+    }
+    if (tid == 0) {
+      L.digit[0] = kDigits;
+      L.digit[1] = -1;
+    }
+    lds_barrier();
+    each([&](float x, int e) {
       const uint64_t key = rank_key(x, e);
       if (shift == 56 || (key >> (shift + 8)) == (prefix >> (shift + 8))) {
         const int d = static_cast<int>(key >> shift) & 255;
-        atomicAdd(&L.cnt[d], 1u);
+        atomicAdd(&L.num[d], 1u);
         atomicAdd(&L.mass[d], w(x));
       }
     });
     lds_barrier();
-    // every thread walks the digits alike; the last one that holds anything
-    // is taken if none reaches the target
-    int d = 255, hit = -1;
-    unsigned long long bm = mass, bc = cnt;
-    for (; d >= 0; --d) {
-      if (L.cnt[d] == 0) continue;
-      hit = d;
-      bm = mass;
-      bc = cnt;
-      const unsigned long long nm = mass + L.mass[d], nc = cnt + L.cnt[d];
-      const bool done = by_count ? nc >= static_cast<unsigned long long>(count)
-                                 : (strict ? static_cast<double>(nm) > target : static_cast<double>(nm) >= target);
-      if (done) break;
-      mass = nm;
-      cnt = nc;
+    // thread t holds digit 255 - t; the first that reaches the cut is taken
+    ull dm = 0, im = 0;
+    int dn = 0, in = 0;
+    if (wave < DW) {
+      dm = L.mass[kDigits - 1 - tid];
+      dn = static_cast<int>(L.num[kDigits - 1 - tid]);
+      im = wave_scan_incl(dm);
+      in = wave_scan_incl(dn);
+      if (lane == kWave - 1) {
+        L.red_u[wave] = im;
+        L.red_i[wave] = in;
+      }
     }
-    through = bm + L.mass[hit < 0 ? 0 : hit];
-    mass = bm;
-    cnt = bc;
-    prefix |= static_cast<uint64_t>(hit < 0 ? 0 : hit) << shift;
     lds_barrier();
+    if (wave < DW) {
+#pragma unroll
+      for (int k = 0; k < DW; ++k) {
+        im += k < wave ? L.red_u[k] : 0ull;
+        in += k < wave ? L.red_i[k] : 0;
+      }
+      im += mass;
+      in += num;
+      const double cum = w0 + static_cast<double>(im) / w.one;
+      const bool done = dn > 0 && (c.count > 0 ? in >= c.count : (c.strict ? cum > c.target : cum >= c.target));
+      if (done) atomicMin(&L.digit[0], tid);
+      if (dn > 0) atomicMax(&L.digit[1], tid);
+    }
+    lds_barrier();
+    const int hit = L.digit[0] < kDigits ? L.digit[0] : L.digit[1];
+    if (hit < 0) return 0;   // nothing to search (every thread returns)
+    if (tid == hit) {
+      L.red_u[0] = im;
+      L.red_u[1] = im - dm;
+      L.red_i[0] = in - dn;
+    }
+    lds_barrier();
+    through = w0 + static_cast<double>(L.red_u[0]) / w.one;
+    mass = L.red_u[1];
+    num = L.red_i[0];
+    prefix |= static_cast<uint64_t>(kDigits - 1 - hit) << shift;
   }
+  lds_barrier();
   return prefix;
 }
 
-// Sum of a 64-bit integer over the workgroup.
+struct Draw {
+  float T, top_p, min_p, u;
+  int top_k;
+};
+
 template <int NT>
-__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, DrawLds<NT>& L) {
-  if (threadIdx.x == 0) L.total = 0;
+__device__ __forceinline__ ull block_sum(ull v, DrawLds<NT>& L) {
+  v = wave_all(v, SumOp());
   lds_barrier();
-  atomicAdd(&L.total, v);
+  if ((threadIdx.x & (kWave - 1)) == 0) L.red_u[threadIdx.x / kWave] = v;
   lds_barrier();
-  const unsigned long long t = L.total;
-  lds_barrier();
+  ull t = 0;
+#pragma unroll
+  for (int w = 0; w < NT / kWave; ++w) t += L.red_u[w];
   return t;
 }
 
 template <typename E, int NT, int U>
-__global__ __launch_bounds__(NT) void draw_kernel(DrawArgs a) {
+__global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
   __shared__ DrawLds<NT> L;
+  constexpr int NW = NT / kWave;
+  constexpr int PER = kReach / NT;
+  static_assert(kReach % NT == 0 && kFew <= NT, "bins per thread");
   const int64_t r = blockIdx.x;
   const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
   const int V = a.x.V;
-  const int tid = threadIdx.x;
-  float T = a.temperature[r], top_p = a.top_p[r], min_p = a.min_p[r], u = a.uniform[r];
-  const int top_k = a.top_k[r];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  Draw d{a.temperature[r], a.top_p[r], a.min_p[r], a.uniform[r], a.top_k[r]};
   int bits = 0;
-  if (!(T >= 0.f && T < INFINITY) || !(top_p > 0.f && top_p <= 1.f) || !(min_p >= 0.f && min_p <= 1.f) ||
-      !(u >= 0.f && u < 1.f)) {
+  if (!(d.T >= 0.f && d.T < INFINITY) || !(d.top_p > 0.f && d.top_p <= 1.f) || !(d.min_p >= 0.f && d.min_p <= 1.f) ||
+      !(d.u >= 0.f && d.u < 1.f)) {
     bits |= VSV_FLAG_PARAMS;
-    T = (T >= 0.f && T < INFINITY) ? T : 0.f;
-    top_p = (top_p > 0.f && top_p <= 1.f) ? top_p : 1.f;
-    min_p = (min_p >= 0.f && min_p <= 1.f) ? min_p : 0.f;
-    u = (u >= 0.f && u < 1.f) ? u : 0.f;
+    d.T = (d.T >= 0.f && d.T < INFINITY) ? d.T : 0.f;
+    d.top_p = (d.top_p > 0.f && d.top_p <= 1.f) ? d.top_p : 1.f;
+    d.min_p = (d.min_p >= 0.f && d.min_p <= 1.f) ? d.min_p : 0.f;
+    d.u = (d.u >= 0.f && d.u < 1.f) ? d.u : 0.f;
   }
-  // the first element of the rank order
-  uint64_t best = 0;
-  int bad = 0;
-  each_elem<E, NT, U>(row, V, [&](float x, int e) {
-    bad |= !(x < INFINITY);
-    const uint64_t key = rank_key(x, e);
-    best = key > best ? key : best;
-  });
-  best = wave_all(best, MaxOp());
-  if ((tid & (kWave - 1)) == 0) L.red[tid / kWave] = best;
-  bad = __syncthreads_or(bad);
-  for (int w = 0; w < NT / kWave; ++w) best = L.red[w] > best ? L.red[w] : best;
-  const float m = key_value(static_cast<uint32_t>(best >> 32));
-  if (bad || !(m > -INFINITY)) {
-    if (tid == 0) {
-      a.token[r] = 0;
-      if (a.logprob) a.logprob[r] = 0.f;
-      if (a.lse) a.lse[r] = m;
-      if (a.error_flag) atomicOr(a.error_flag, bits | VSV_FLAG_LOGITS);
+  // the arg-max is the first token of the order at any temperature
+  const bool greedy = d.T == 0.f;
+  if (greedy) d = Draw{1.f, 1.f, 0.f, 0.f, 0};
+  const bool count = d.top_k > 0 && d.top_k < V;
+  const double T = static_cast<double>(d.T);
+
+  // weights are integers in units of 1 / one: V of them stay below 2^63, and
+  // one below 2^52
+  const double one = ldexp(1.0, min(50, 62 - (32 - __clz(V))));
+
+  // ---- the row into bins
+  Grid g{kPerT / T, 0.0};
+  float m = -INFINITY;
+  bool far = false;
+  auto bins = [&](auto& f, bool known) {
+    f.g = g;
+    f.bin = L.bin;
+    f.cnt = L.u.cnt;
+    f.top = -INFINITY;
+    f.c[0] = one;
+#pragma unroll
+    for (int k = 1; k < 6; ++k) f.c[k] = f.c[k - 1] * (1.0 / (kPerT * k));
+    f.c[0] += 4503599627370496.0;
+    for (int b = tid; b < kBins; b += NT) L.bin[b] = 0;
+    if (count)
+      for (int b = tid; b < kBins; b += NT) L.u.cnt[b] = 0;
+    auto place = [&](float ref) {
+      const double y = static_cast<double>(ref) * f.g.s;
+      far = !(fabs(y) < kFarBin);
+      f.g.k = kMagic - (far ? 0.0 : rint(y)) + static_cast<double>(kReach);
+    };
+    visit_row<E, NT, U, kLoadNormal>(row, V, f, [&](const u32x4* w, int nvec) {
+      float t = m;
+      if (!known) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[Elem<E>::kVec];
+          if (tid + u * NT < nvec) t = fmaxf(t, vec_max<E>(w[u], x));
+        }
+        const int head = row_head(row, V);
+        if (tid < head) t = fmaxf(t, Elem<E>::at(row, tid));
+        if (tid < V - head - nvec * Elem<E>::kVec) t = fmaxf(t, Elem<E>::at(row, V - 1 - tid));
+        t = wave_all(t, MaxOp());
+        if (lane == 0) L.red_f[wave] = t;
+      }
+      lds_barrier();
+      if (!known) {
+        t = L.red_f[0];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) t = fmaxf(t, L.red_f[k]);
+      }
+      place(t);
+    });
+    g = f.g;
+    const float t = wave_all(f.top, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
+    lds_barrier();
+    if (lane == 0) L.red_f[wave] = t;
+    lds_barrier();
+    m = L.red_f[0];
+#pragma unroll
+    for (int k = 1; k < NW; ++k) m = __builtin_elementwise_maximum(m, L.red_f[k]);
+  };
+  auto pass = [&](bool known) {
+    if (count) {
+      BinVisit<E, NT, U, true> f;
+      bins(f, known);
+    } else {
+      BinVisit<E, NT, U, false> f;
+      bins(f, known);
     }
-    return;
+  };
+  // again where the first group held nothing to go by, or the row rises far
+  // beyond it
+  for (bool known = false;; known = true) {
+    pass(known);
+    if (!(m > -INFINITY && m < INFINITY)) {
+      if (tid == 0) {
+        a.token[r] = 0;
+        if (a.logprob) a.logprob[r] = 0.f;
+        if (a.lse) a.lse[r] = m;
+        if (a.error_flag) atomicOr(a.error_flag, bits | VSV_FLAG_LOGITS);
+      }
+      return;
+    }
+    if (known || !(far || Grid::slot(g.t(m)) < 0)) break;
+    lds_barrier();
   }
-  const int s = 62 - (32 - __clz(V));
-  const Weigh w{static_cast<double>(m), T > 0.f ? static_cast<double>(T) : 1.0, ldexp(1.0, s)};
-  unsigned long long mine = 0, above = 0;
-  const double zmin = min_p > 0.f ? log(static_cast<double>(min_p)) : -INFINITY;
-  each_elem<E, NT, U>(row, V, [&](float x, int) {
-    const unsigned long long f = w(x);
-    mine += f;
-    if (w.z(x) >= zmin) above += f;
-  });
-  const unsigned long long total = block_sum<NT>(mine, L);
-  const unsigned long long kept = block_sum<NT>(above, L);
-  const double lse = w.m / w.T + log(static_cast<double>(total) / w.one);
-  uint64_t at = best;
-  double logprob = 0.0;
-  if (T > 0.f) {
-    unsigned long long left = total;
-    if (top_k > 0 && top_k < V) find_cut<E, NT, U>(row, V, w, true, top_k, 0.0, false, left, L);
-    if (top_p < 1.f)
-      find_cut<E, NT, U>(row, V, w, false, 0, static_cast<double>(top_p) * static_cast<double>(left), false, left, L);
-    left = kept < left ? kept : left;
-    unsigned long long through;
-    at = find_cut<E, NT, U>(row, V, w, false, 0, static_cast<double>(u) * static_cast<double>(left), true, through, L);
-    logprob = w.z(key_value(static_cast<uint32_t>(at >> 32))) - log(static_cast<double>(left) / w.one);
+  const Weigh w{static_cast<double>(m), T, one};
+  const double top_p = static_cast<double>(d.top_p), u = static_cast<double>(d.u);
+  const double zmin = d.min_p > 0.f ? log(static_cast<double>(d.min_p)) : -INFINITY;
+  uint64_t key = 0;                  // rank key of the token
+  double total = 0.0, left = 0.0;    // weight of the row, of the survivors
+
+  // what the search below goes by: the gathered list (bins), or the row
+  int n = V, top_k = 0, jk = -1, jm = -1, top = 0;
+  const double* cum = nullptr;
+  double through[PER];
+  int seen[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    through[k] = 0.0;
+    seen[k] = 0;
+  }
+  // weight through the j-th bin downwards
+  auto upto = [&](int j) { return j < 0 ? 0.0 : cum[-j]; };
+  auto bin_of = [&](float x) {
+    const int b = Grid::slot(g.t(x));
+    return b < 0 ? -1 : top - b;
+  };
+  // the first bin whose k-th slot of its thread satisfies pred, into L.j[q]
+  // (the last one if none does)
+  auto first_bin = [&](int q, auto pred) {
+    int mine = kReach;
+#pragma unroll
+    for (int k = PER - 1; k >= 0; --k) mine = pred(k) ? tid * PER + k : mine;
+    mine = wave_all(mine, MinOp());
+    if (lane == 0 && mine < kReach) atomicMin(&L.j[q], mine);
+  };
+  auto at_least = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] >= t; }); };
+  auto more_than = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] > t; }); };
+
+  if (!far) {
+    // ---- cumulative weights, downwards from the maximum's bin
+    top = Grid::slot(g.t(m));
+    const double mpos = fma(static_cast<double>(m), g.s, g.k - kMagic);   // the maximum among the bins' numbers
+    double sum = 0.0;
+    int num = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int b = top - (tid * PER + k);
+      sum += static_cast<double>(L.bin[b]) / one * exp((static_cast<double>(b) - mpos) / kPerT);
+      through[k] = sum;
+      num += count ? static_cast<int>(L.u.cnt[b]) : 0;
+      seen[k] = num;
+    }
+    double wb = wave_scan_incl(sum);
+    int nb = wave_scan_incl(num);
+    if (lane == kWave - 1) {
+      L.red_d[wave] = wb;
+      L.red_i[wave] = nb;
+    }
+    if (tid < 8) L.j[tid] = kReach - 1;
+    if (tid < kReach / 32) L.mark[tid] = 0;
+    if (tid == 0) {
+      L.n = 0;
+      L.before = 0;
+    }
+    lds_barrier();
+    wb -= sum;
+    nb -= num;
+    int number = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      wb += k < wave ? L.red_d[k] : 0.0;
+      nb += k < wave ? L.red_i[k] : 0;
+      total += L.red_d[k];
+      number += L.red_i[k];
+    }
+    double* out = reinterpret_cast<double*>(L.bin) + top;
+    cum = out;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      through[k] += wb;
+      seen[k] += nb;
+      out[-(tid * PER + k)] = through[k];
+    }
+
+    // ---- where each cut lies: a range of bins, and bounds of the weight
+    // it leaves
+    top_k = (count && number >= d.top_k) ? d.top_k : 0;
+    lds_barrier();
+    double lo = total, hi = total;
+    if (top_k) {
+      first_bin(0, [&](int k) { return seen[k] >= top_k; });
+      lds_barrier();
+      jk = L.j[0];
+      lo = upto(jk - 1);
+      hi = upto(jk);
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        if (tid * PER + k == jk) L.before = k ? seen[k - 1] : nb;
+    }
+    int p0 = kReach, p1 = -1;
+    if (d.top_p < 1.f) {
+      at_least(1, reach(top_p * lo));
+      at_least(2, reach(top_p * hi));
+      lds_barrier();
+      p0 = L.j[1];
+      p1 = L.j[2];
+      lo = fmin(lo, upto(p0 - 1));
+      hi = fmin(hi, upto(p1));
+    }
+    if (d.min_p > 0.f) {
+      const double jz = static_cast<double>(top) - rint(mpos + kPerT * zmin);
+      if (jz < static_cast<double>(kReach)) {
+        jm = jz > 0.0 ? static_cast<int>(jz) : 0;
+        lo = fmin(lo, upto(jm - 1));
+        hi = fmin(hi, upto(jm));
+      }
+    }
+    more_than(3, exceed(u * lo));
+    more_than(4, exceed(u * hi));
+    lds_barrier();
+    const int d0 = L.j[3], d1 = L.j[4];
+    const int last = max(max(jk, jm), max(p1, d1));
+    for (int j = tid; j <= last; j += NT)
+      if (j == jk || j == jm || (j >= p0 && j <= p1) || (j >= d0 && j <= d1)) atomicOr(&L.mark[j >> 5], 1u << (j & 31));
+    lds_barrier();
+
+    // ---- the elements of those bins
+    {
+      const double edge = (static_cast<double>(top - last) - 0.5 - (g.k - kMagic)) / g.s;
+      const float low = static_cast<float>(edge - fabs(edge) * (1.0 / 1048576.0) - 1e-30);
+      auto take = [&](float x, int e) {
+        const int j = bin_of(x);
+        if (j >= 0 && j <= last && (L.mark[j >> 5] >> (j & 31) & 1u)) {
+          const int n = atomicAdd(&L.n, 1);
+          if (n < kList) L.u.list[n] = rank_key(x, e);
+        }
+      };
+      EachAbove<E, NT, U, decltype(take)> v{take, row_head(row, V), low};
+      visit_row<E, NT, U, kLoadNormal>(row, V, v);
+    }
+    lds_barrier();
+    n = L.n;
+    left = total;
+    if (n <= kFew) {
+      // ---- few: each element's cumulative weight from the others of its bin
+      uint64_t mine = 0;
+      int j = -1;
+      if (tid < n) {
+        mine = L.u.list[tid];
+        j = bin_of(key_x(mine));
+        L.w[tid] = w.exact(key_x(mine));
+        L.at[tid] = j;
+      }
+      if (tid < 2) L.key[tid] = 0;
+      if (tid == 0) L.kept = __builtin_bit_cast(ull, upto(jm - 1));
+      lds_barrier();
+      double c = 0.0;
+      if (tid < n) {
+        int before = 0;
+        for (int i = 0; i < n; ++i) {
+          const bool in = L.at[i] == j && L.u.list[i] >= mine;
+          c += in ? L.w[i] : 0.0;
+          before += in ? 1 : 0;
+        }
+        c += upto(j - 1);
+        if (j == jk && L.before + before == top_k) L.cut = c;
+      }
+      if (top_k) {
+        lds_barrier();
+        left = L.cut;
+      }
+      // the first in rank order, whatever rounding does to light tokens' sums
+      if (tid < n) {
+        if (d.top_p < 1.f && c >= reach(top_p * left)) atomicMax(&L.key[0], static_cast<ull>(mine));
+        // (positive doubles order like their bits)
+        if (jm >= 0 && w.z(key_x(mine)) >= zmin) atomicMax(&L.kept, __builtin_bit_cast(ull, c));
+      }
+      lds_barrier();
+      if (d.top_p < 1.f) {
+        if (mine != 0 && mine == L.key[0]) L.cut = c;
+        lds_barrier();
+        if (L.key[0] != 0) left = fmin(left, L.cut);
+      }
+      if (jm >= 0) left = fmin(left, __builtin_bit_cast(double, L.kept));
+      if (tid < n && c > exceed(u * left)) atomicMax(&L.key[1], static_cast<ull>(mine));
+      lds_barrier();
+      key = L.key[1];
+    }
+  }
+  if (key == 0) {
+    // ---- more: each cut by a radix search, over its own bin's elements or,
+    // where the bins hold too many or cannot place them (or rounding hides a
+    // border from the list), over the row
+    bool list = !far && n > kFew && n <= kList;
+    int j = -1;
+    auto each = [&](auto&& f) {
+      if (list) {
+        for (int i = tid; i < n; i += NT) {
+          const uint64_t k = L.u.list[i];
+          if (bin_of(key_x(k)) == j) f(key_x(k), static_cast<int>(~static_cast<uint32_t>(k)));
+        }
+      } else {
+        for (int e = tid; e < V; e += NT) f(Elem<E>::at(row, e), e);
+      }
+    };
+#pragma unroll 1
+    for (;; list = false) {
+      if (!list) {
+        top_k = count ? d.top_k : 0;
+        ull mine = 0;
+        each([&](float x, int) { mine += w(x); });
+        total = static_cast<double>(block_sum<NT>(mine, L)) / w.one;
+        left = total;
+      }
+#pragma unroll 1
+      for (int c = 0; c < 3; ++c) {
+        if (c == 2 && d.min_p > 0.f && (!list || jm >= 0)) {
+          j = jm;
+          ull kept = 0;
+          each([&](float x, int) { kept += w.z(x) >= zmin ? w(x) : 0ull; });
+          left = fmin(left, (list ? upto(jm - 1) : 0.0) + static_cast<double>(block_sum<NT>(kept, L)) / w.one);
+        }
+        if ((c == 0 && !top_k) || (c == 1 && !(d.top_p < 1.f))) continue;
+        const double t = c == 1 ? reach(top_p * left) : exceed(u * left);
+        if (list) {
+          if (c == 0) {
+            j = jk;
+          } else {
+            if (c == 1) at_least(5, t);
+            else more_than(6, t);
+            lds_barrier();
+            j = L.j[4 + c];
+          }
+        }
+        double to;
+        key = find_cut<NT>(each, w, Cut{c == 0 ? top_k : 0, c == 2, t}, list ? upto(j - 1) : 0.0, list ? L.before : 0, to, L);
+        if (c < 2) left = to;
+      }
+      if (key != 0 || !list) break;
+    }
   }
   if (tid == 0) {
-    a.token[r] = static_cast<int>(~static_cast<uint32_t>(at));
-    if (a.logprob) a.logprob[r] = static_cast<float>(logprob);
-    if (a.lse) a.lse[r] = static_cast<float>(lse);
+    const float x = key_x(key);
+    a.token[r] = static_cast<int>(~static_cast<uint32_t>(key));
+    if (a.logprob) a.logprob[r] = greedy ? 0.f : static_cast<float>(w.z(x) - log(left));
+    if (a.lse) a.lse[r] = static_cast<float>(w.m / T + log(total));
     if (bits && a.error_flag) atomicOr(a.error_flag, bits);
   }
 }

@@ -69,9 +69,14 @@ __device__ __forceinline__ void add_term(ExpSum& p, float x, float c) { add_term
 
 // f.template group<kPartial>(w, v, nvec): vectors v, v + NT, .. of one thread
 // (kPartial: those at or beyond nvec hold zeros and are to be left out);
-// f.one(x, e): element e. `hook` runs once after the first loads are issued.
-template <typename E, int NT, int U, int kAux, typename F, typename Hook = NoHook>
-__device__ __forceinline__ void visit_row(const E* __restrict__ row, int V, F& f, Hook hook = Hook()) {
+// f.one(x, e): element e. `first` sees each thread's first group, w[u] the
+// vector tid + u NT where that is below nvec, before any of it is visited;
+// every thread calls it, so it may hold barriers.
+struct NoFirst {
+  __device__ __forceinline__ void operator()(const u32x4*, int) const {}
+};
+template <typename E, int NT, int U, int kAux, typename F, typename First = NoFirst>
+__device__ __forceinline__ void visit_row(const E* __restrict__ row, int V, F& f, First first = First()) {
   constexpr int N = Elem<E>::kVec;
   const int tid = threadIdx.x;
   const int head = row_head(row, V);
@@ -83,7 +88,7 @@ __device__ __forceinline__ void visit_row(const E* __restrict__ row, int V, F& f
     const __amdgpu_buffer_rsrc_t rsrc = vec_rsrc(row + head, nvec);
     u32x4 a[U], b[U];
     load_group_rsrc<NT, U, kAux>(a, rsrc, 0);
-    hook();
+    first(a, nvec);
     int g = 0;
     for (; g + 2 <= nfull; g += 2) {
       load_group_rsrc<NT, U, kAux>(b, rsrc, g + 1);
@@ -99,7 +104,8 @@ __device__ __forceinline__ void visit_row(const E* __restrict__ row, int V, F& f
       f.template group<true>(a, nfull * G + tid, nvec);
     }
   } else {
-    hook();
+    u32x4 none[U];
+    first(none, 0);
   }
   if (tid < head) f.one(Elem<E>::at(row, tid), tid);
   const int tail = V - body_end;
