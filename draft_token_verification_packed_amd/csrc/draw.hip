@@ -50,6 +50,9 @@ constexpr double kFarBin = 4194304.0;
 constexpr double kEqual = 1.0 / 4398046511104.0;   // 2^-42
 
 typedef unsigned long long ull;
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ bool any_lane(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
 
 __device__ __forceinline__ uint32_t up_key(float x) {
   const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
@@ -145,28 +148,77 @@ struct BinVisit {
   }
 };
 
-// Elements at or above `low`, a vector at a time.
-template <typename E, int NT, int U, typename F>
-struct EachAbove {
-  F& f;
+// ---------------------------------------------------------------- gathering
+
+// The wanted elements of a range of the row: want(w, mask) sets a bit per
+// wanted element of a vector, want.one(x) decides one element, and
+// put(position, element) stores it. Positions come from one LDS atomic per
+// wave and group.
+template <typename E, int NT, int U, typename Want, typename Put>
+struct GatherVisit {
+  Want& want;
+  Put& put;
+  int* n;
   int head;
-  float low;
   template <bool kPartial>
   __device__ __forceinline__ void group(const u32x4* w, int v, int nvec) {
     constexpr int N = Elem<E>::kVec;
+    uint32_t mask = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (kPartial && v + u * NT >= nvec) continue;
-      float x[N];
-      if (vec_max<E, true>(w[u], x) >= low) {
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (x[k] >= low) f(x[k], head + (v + u * NT) * N + k);
+      const uint32_t m = want(w[u]);
+      mask |= (kPartial && v + u * NT >= nvec) ? 0u : m << (u * N);
+    }
+    if (any_lane(mask != 0)) {
+      const int c = __popc(mask);
+      const int incl = wave_scan_incl(c);
+      int at = 0;
+      if ((threadIdx.x & (kWave - 1)) == kWave - 1) at = atomicAdd(n, incl);
+      at = read_lane(at, kWave - 1) + incl - c;
+      while (mask) {
+        const int b = __ffs(mask) - 1;
+        mask &= mask - 1;
+        put(at++, head + (v + b / N * NT) * N + b % N);
       }
     }
   }
   __device__ __forceinline__ void one(float x, int e) {
-    if (x >= low) f(x, e);
+    if (want.one(x)) put(atomicAdd(n, 1), e);
+  }
+};
+
+// Elements between two bounds whose bin is marked (bin(x): whether it is).
+template <typename E, typename Bin> struct WantBetween {
+  Bin& bin;
+  float low, high;
+  __device__ __forceinline__ bool in(float x) const { return __builtin_amdgcn_fmed3f(x, low, high) == x; }
+  __device__ __forceinline__ bool one(float x) const { return in(x) && bin(x); }
+  __device__ __forceinline__ uint32_t operator()(const u32x4& w) const {
+    constexpr int N = Elem<E>::kVec;
+    float x[N];
+    Elem<E>::decode(w, x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) m |= in(x[k]) ? 1u << k : 0u;
+    if (m) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (m >> k & 1) m &= bin(x[k]) ? ~0u : ~(1u << k);
+    }
+    return m;
+  }
+};
+
+// bfloat16 elements with one bit pattern.
+struct WantCode {
+  uint32_t code;   // in both halves
+  __device__ __forceinline__ bool one(float x) const { return __float_as_uint(x) >> 16 == (code & 0xFFFFu); }
+  __device__ __forceinline__ uint32_t operator()(const u32x4& w) const {
+    const uint32_t d[4] = {w.x ^ code, w.y ^ code, w.z ^ code, w.w ^ code};
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m |= ((d[k] & 0xFFFFu) == 0 ? 1u << (2 * k) : 0u) | (d[k] < 0x10000u ? 2u << (2 * k) : 0u);
+    return m;
   }
 };
 
@@ -314,18 +366,9 @@ __device__ __forceinline__ ull block_sum(ull v, DrawLds<NT>& L) {
   return t;
 }
 
-template <typename E, int NT, int U>
-__global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
-  __shared__ DrawLds<NT> L;
-  constexpr int NW = NT / kWave;
-  constexpr int PER = kReach / NT;
-  static_assert(kReach % NT == 0 && kFew <= NT, "bins per thread");
-  const int64_t r = blockIdx.x;
-  const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
-  const int V = a.x.V;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+// A row's parameters; those outside their ranges are flagged and replaced.
+__device__ __forceinline__ Draw load_draw(const DrawArgs& a, int64_t r, int& bits, bool& greedy) {
   Draw d{a.temperature[r], a.top_p[r], a.min_p[r], a.uniform[r], a.top_k[r]};
-  int bits = 0;
   if (!(d.T >= 0.f && d.T < INFINITY) || !(d.top_p > 0.f && d.top_p <= 1.f) || !(d.min_p >= 0.f && d.min_p <= 1.f) ||
       !(d.u >= 0.f && d.u < 1.f)) {
     bits |= VSV_FLAG_PARAMS;
@@ -335,14 +378,29 @@ __global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
     d.u = (d.u >= 0.f && d.u < 1.f) ? d.u : 0.f;
   }
   // the arg-max is the first token of the order at any temperature
-  const bool greedy = d.T == 0.f;
+  greedy = d.T == 0.f;
   if (greedy) d = Draw{1.f, 1.f, 0.f, 0.f, 0};
+  return d;
+}
+// Weights are integers in units of one over this: V of them stay below 2^63,
+// and one below 2^52.
+__device__ __forceinline__ double weight_units(int V) { return ldexp(1.0, min(50, 62 - (32 - __clz(V)))); }
+
+// Row r by linear bins, by the whole workgroup.
+template <typename E, int NT, int U>
+__device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<NT>& L) {
+  constexpr int NW = NT / kWave;
+  constexpr int PER = kReach / NT;
+  static_assert(kReach % NT == 0 && kFew <= NT, "bins per thread");
+  const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
+  const int V = a.x.V;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  int bits = 0;
+  bool greedy;
+  const Draw d = load_draw(a, r, bits, greedy);
   const bool count = d.top_k > 0 && d.top_k < V;
   const double T = static_cast<double>(d.T);
-
-  // weights are integers in units of 1 / one: V of them stay below 2^63, and
-  // one below 2^52
-  const double one = ldexp(1.0, min(50, 62 - (32 - __clz(V))));
+  const double one = weight_units(V);
 
   // ---- the row into bins
   Grid g{kPerT / T, 0.0};
@@ -539,22 +597,27 @@ __global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
     lds_barrier();
     const int d0 = L.j[3], d1 = L.j[4];
     const int last = max(max(jk, jm), max(p1, d1));
+    const int first = min(min(jk < 0 ? d0 : jk, jm < 0 ? d0 : jm), min(p0, d0));
     for (int j = tid; j <= last; j += NT)
       if (j == jk || j == jm || (j >= p0 && j <= p1) || (j >= d0 && j <= d1)) atomicOr(&L.mark[j >> 5], 1u << (j & 31));
     lds_barrier();
 
     // ---- the elements of those bins
     {
-      const double edge = (static_cast<double>(top - last) - 0.5 - (g.k - kMagic)) / g.s;
-      const float low = static_cast<float>(edge - fabs(edge) * (1.0 / 1048576.0) - 1e-30);
-      auto take = [&](float x, int e) {
+      // a little outside the outermost bins' borders; bin_of decides
+      const double at = static_cast<double>(top) - (g.k - kMagic);
+      const double to = (at - first + 0.5) / g.s, from = (at - last - 0.5) / g.s;
+      const float high = static_cast<float>(to + fabs(to) * (1.0 / 1048576.0) + 1e-30);
+      const float low = static_cast<float>(from - fabs(from) * (1.0 / 1048576.0) - 1e-30);
+      auto marked = [&](float x) {
         const int j = bin_of(x);
-        if (j >= 0 && j <= last && (L.mark[j >> 5] >> (j & 31) & 1u)) {
-          const int n = atomicAdd(&L.n, 1);
-          if (n < kList) L.u.list[n] = rank_key(x, e);
-        }
+        return j >= first && j <= last && (L.mark[j >> 5] >> (j & 31) & 1u) != 0;
       };
-      EachAbove<E, NT, U, decltype(take)> v{take, row_head(row, V), low};
+      auto put = [&](int at, int e) {
+        if (at < kList) L.u.list[at] = rank_key(Elem<E>::at(row, e), e);
+      };
+      WantBetween<E, decltype(marked)> want{marked, low, high};
+      GatherVisit<E, NT, U, decltype(want), decltype(put)> v{want, put, &L.n, row_head(row, V)};
       visit_row<E, NT, U, kLoadNormal>(row, V, v);
     }
     lds_barrier();
@@ -664,6 +727,353 @@ __global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
     if (a.logprob) a.logprob[r] = greedy ? 0.f : static_cast<float>(w.z(x) - log(left));
     if (a.lse) a.lse[r] = static_cast<float>(w.m / T + log(total));
     if (bits && a.error_flag) atomicOr(a.error_flag, bits);
+  }
+}
+
+// ---------------------------------------------------------------- bfloat16 codes
+
+// A bfloat16 row holds few distinct values: a count per 16-bit code says all
+// of its weights exactly, so its stream needs no exponentials, and a cut
+// inside a code is arithmetic. The table covers 2^-16 <= |x| < 2^8, 24
+// binades of 128 codes of either sign; smaller |x| (zeros among them) are one
+// cell between the signs, with their weight, and rows with other values that
+// matter are left to draw_row.
+constexpr uint32_t kCodeLow = 0x3780u;     // 2^-16
+constexpr int kCodes = 0xC00;              // codes of a sign
+constexpr int kTab = 8192;                 // sign << 12 | code - kCodeLow
+constexpr int kCells = 2 * kCodes + 1;     // in rank order: positive, tiny, negative
+constexpr int kCodeList = 4096;
+constexpr double kTinyT = 1.0 / 1024.0;    // below this T the tiny cell is no point
+
+template <int NT> struct CodeLds {
+  static constexpr int NW = NT / kWave;
+  uint32_t tab[kTab];
+  uint32_t list[kCodeList];
+  uint32_t hist[256];
+  ull tiny;          // weight of the tiny cell relative to x = 0
+  uint32_t tiny_n;
+  int bad;           // a value of 2^8 or more, or a NaN
+  uint32_t low;      // key of the largest finite value at or below -2^8
+  int n, j[6];
+  double red_d[NW];
+  int red_i[NW];
+  double cut_w;
+  int cut_j, cut_r, cut_n, digit, before;
+  int token;
+};
+
+template <int NT, int U>
+struct CodeVisit {
+  CodeLds<NT>& L;
+  double inv_t, units;
+
+  __device__ __forceinline__ void rare(uint32_t h) {
+    const uint32_t mag = h & 0x7FFFu;
+    const uint32_t q = mag - kCodeLow;
+    if (q < static_cast<uint32_t>(kCodes)) {
+      atomicAdd(&L.tab[(h >> 15 << 12) | q], 1u);
+    } else if (mag < kCodeLow) {
+      const float x = __uint_as_float(h << 16);
+      atomicAdd(&L.tiny, static_cast<ull>(rint(exp(static_cast<double>(x) * inv_t) * units)));
+      atomicAdd(&L.tiny_n, 1u);
+    } else if (h == 0xFF80u) {
+      // -inf weighs nothing
+    } else if ((h & 0x8000u) && mag < 0x7F80u) {
+      atomicMax(&L.low, up_key(__uint_as_float(h << 16)));
+    } else {
+      L.bad = 1;
+    }
+  }
+  template <bool kPartial>
+  __device__ __forceinline__ void group(const u32x4* w, int v, int nvec) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kPartial && v + u * NT >= nvec) continue;
+      const uint32_t d[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      u16x2 q[4], m = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const u16x2 base = {static_cast<uint16_t>(kCodeLow), static_cast<uint16_t>(kCodeLow)};
+        q[k] = __builtin_bit_cast(u16x2, d[k] & 0x7FFF7FFFu) - base;
+        m = __builtin_elementwise_max(m, q[k]);
+      }
+      if (m.x < kCodes && m.y < kCodes) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t a = __builtin_bit_cast(uint32_t, q[k]) | (d[k] >> 3 & 0x10001000u);
+          atomicAdd(&L.tab[a & 0xFFFFu], 1u);
+          atomicAdd(&L.tab[a >> 16], 1u);
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t h = k == 0 ? w[u].x : k == 1 ? w[u].y : k == 2 ? w[u].z : w[u].w;
+          rare(h & 0xFFFFu);
+          rare(h >> 16);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void one(float x, int) { rare(__float_as_uint(x) >> 16); }
+};
+
+// The r-th (1, 2, ..) element of [e0, e1) that holds `code`, by index, or -1
+// where there are more than the list holds.
+template <int NT, int U>
+__device__ __forceinline__ int nth_code(const uint16_t* row, int e0, int e1, uint32_t code, int r, CodeLds<NT>& L) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  if (tid == 0) L.n = 0;
+  lds_barrier();
+  WantCode want{code | code << 16};
+  auto put = [&](int at, int e) {
+    if (at < kCodeList) L.list[at] = static_cast<uint32_t>(e);
+  };
+  GatherVisit<uint16_t, NT, U, WantCode, decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
+  visit_row<uint16_t, NT, U, kLoadNormal>(row + e0, e1 - e0, v);
+  lds_barrier();
+  const int n = L.n;
+  if (n > kCodeList || r > n) return -1;
+  if (n <= NT) {
+    if (tid < n) {
+      const uint32_t mine = L.list[tid];
+      int before = 0;
+      for (int i = 0; i < n; ++i) before += L.list[i] < mine ? 1 : 0;
+      if (before == r - 1) L.token = static_cast<int>(mine);
+    }
+    lds_barrier();
+    return e0 + L.token;
+  }
+  // a byte of the index at a time
+  uint32_t prefix = 0;
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (shift > 0 && (static_cast<uint32_t>(e1 - e0) >> shift) == 0) continue;
+    lds_barrier();
+    for (int b = tid; b < 256; b += NT) L.hist[b] = 0;
+    lds_barrier();
+    for (int i = tid; i < n; i += NT) {
+      const uint32_t e = L.list[i];
+      if (shift == 24 || (e >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&L.hist[e >> shift & 255], 1u);
+    }
+    lds_barrier();
+    if (tid < kWave) {
+      // four digits a lane, upwards
+      int c[4], sum = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum += c[k] = static_cast<int>(L.hist[lane * 4 + k]);
+      int at = wave_scan_incl(sum) - sum;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (at < r && r <= at + c[k]) {
+          L.digit = lane * 4 + k;
+          L.before = at;
+        }
+        at += c[k];
+      }
+    }
+    lds_barrier();
+    prefix |= static_cast<uint32_t>(L.digit) << shift;
+    r -= L.before;
+  }
+  lds_barrier();
+  return e0 + static_cast<int>(prefix);
+}
+
+__device__ __forceinline__ uint32_t cell_code(int j) {
+  return j < kCodes ? kCodeLow + static_cast<uint32_t>(kCodes - 1 - j) : (0x8000u | kCodeLow) + static_cast<uint32_t>(j - kCodes - 1);
+}
+
+template <int NT>
+__device__ __forceinline__ void clear_codes(CodeLds<NT>& L) {
+  for (int b = threadIdx.x; b < kTab; b += NT) L.tab[b] = 0;
+  if (threadIdx.x == 0) {
+    L.tiny = 0;
+    L.tiny_n = 0;
+    L.bad = 0;
+    L.low = 0;
+  }
+  lds_barrier();
+}
+
+// The draw from a row's counts: L's tiny cell and flags, and cnt[k], the
+// count of cell PER * thread + k. nth(code, r) finds the r-th element that
+// holds a code. False where the row is left to draw_row (nothing is written).
+template <int NT, int PER, typename Nth>
+__device__ __forceinline__ bool draw_codes(const DrawArgs& a, int64_t r, const Draw& d, bool greedy, int bits,
+                                           const int (&cnt)[PER], CodeLds<NT>& L, Nth nth) {
+  constexpr int NW = NT / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const double T = static_cast<double>(d.T);
+  if (tid < 6) L.j[tid] = kCells;
+  lds_barrier();
+  auto first_cell = [&](int q, auto pred) {
+    int mine = kCells;
+#pragma unroll
+    for (int k = PER - 1; k >= 0; --k) mine = (cnt[k] > 0 && pred(k)) ? tid * PER + k : mine;
+    mine = wave_all(mine, MinOp());
+    if (lane == 0 && mine < kCells) atomicMin(&L.j[q], mine);
+  };
+  first_cell(0, [](int) { return true; });
+  lds_barrier();
+  const int jmax = L.j[0];
+  if (L.bad || jmax >= kCells || jmax == kCodes || !(T >= kTinyT)) return false;
+  const Weigh w{static_cast<double>(__uint_as_float(cell_code(jmax) << 16)), T, weight_units(a.x.V)};
+  // a value below the table within reach of the maximum
+  if (L.low != 0 && static_cast<double>(key_value(L.low)) > w.m - 48.0 * T) return false;
+
+  // ---- cumulative weights and counts
+  auto z_of = [&](int j) { return j == kCodes ? -w.m / T : w.z(__uint_as_float(cell_code(j) << 16)); };
+  double through[PER], sum = 0.0;
+  int seen[PER], num = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int j = tid * PER + k;
+    if (cnt[k] > 0) {
+      const double z = z_of(j);
+      if (z > -48.0) sum += exp(z) * (j == kCodes ? static_cast<double>(L.tiny) / w.one : static_cast<double>(cnt[k]));
+    }
+    through[k] = sum;
+    num += cnt[k];
+    seen[k] = num;
+  }
+  double wb = wave_scan_incl(sum);
+  int nb = wave_scan_incl(num);
+  if (lane == kWave - 1) {
+    L.red_d[wave] = wb;
+    L.red_i[wave] = nb;
+  }
+  lds_barrier();
+  wb -= sum;
+  nb -= num;
+  double total = 0.0;
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    wb += k < wave ? L.red_d[k] : 0.0;
+    nb += k < wave ? L.red_i[k] : 0;
+    total += L.red_d[k];
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    through[k] += wb;
+    seen[k] += nb;
+  }
+  // ---- cuts: the cell, and how many of its tokens are through
+  enum { kByCount, kReach_, kExceed };
+  auto cut = [&](int q, int how, int count, double t) {
+    if (how == kByCount) first_cell(q, [&](int k) { return seen[k] >= count; });
+    if (how == kReach_) first_cell(q, [&](int k) { return through[k] >= t; });
+    if (how == kExceed) first_cell(q, [&](int k) { return through[k] > t; });
+    lds_barrier();
+    const int j = L.j[q];
+    if (j >= kCells || j == kCodes) return false;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      if (tid * PER + k == j) {
+        const double before = k ? through[k > 0 ? k - 1 : 0] : wb;
+        const double one = exp(z_of(j));
+        int c;
+        if (how == kByCount) {
+          c = count - (k ? seen[k > 0 ? k - 1 : 0] : nb);
+        } else {
+          // the least c with before + c one at least (more than) t
+          const double f = one > 0.0 ? fmin((t - before) / one, static_cast<double>(cnt[k])) : 1.0;
+          c = how == kReach_ ? static_cast<int>(ceil(f)) : static_cast<int>(floor(f)) + 1;
+          c = max(1, min(c, cnt[k]));
+          auto past = [&](int q2) {
+            const double s = before + static_cast<double>(q2) * one;
+            return how == kReach_ ? s >= t : s > t;
+          };
+          if (c > 1 && past(c - 1)) --c;
+          else if (c < cnt[k] && !past(c)) ++c;
+        }
+        L.cut_w = before + static_cast<double>(c) * one;
+        L.cut_r = c;
+      }
+    }
+    lds_barrier();
+    return true;
+  };
+  double left = total;
+  if (d.top_k > 0 && d.top_k < a.x.V) {
+    // (-inf tokens are in no cell: a cut among them leaves everything)
+    first_cell(1, [&](int k) { return seen[k] >= d.top_k; });
+    lds_barrier();
+    if (L.j[1] < kCells) {
+      if (!cut(1, kByCount, d.top_k, 0.0)) return false;
+      left = L.cut_w;
+    }
+  }
+  if (d.top_p < 1.f) {
+    if (!cut(2, kReach_, 0, reach(static_cast<double>(d.top_p) * left))) return false;
+    left = fmin(left, L.cut_w);
+  }
+  if (d.min_p > 0.f) {
+    const double zmin = log(static_cast<double>(d.min_p));
+    // the tiny cell spans a few 2^-16 / T of z
+    if (fabs(zmin + w.m / T) * T < 1.0 / 16384.0) return false;
+    first_cell(3, [&](int k) { return z_of(tid * PER + k) < zmin; });
+    lds_barrier();
+    const int j = L.j[3];
+    if (j < kCells) {
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        if (tid * PER + k == j) L.cut_w = k ? through[k > 0 ? k - 1 : 0] : wb;
+      lds_barrier();
+      left = fmin(left, L.cut_w);
+    }
+  }
+  if (!cut(4, kExceed, 0, exceed(static_cast<double>(d.u) * left))) return false;
+  const int j = L.j[4];
+  const int token = nth(cell_code(j), L.cut_r);
+  if (token < 0) return false;
+  if (tid == 0) {
+    a.token[r] = token;
+    if (a.logprob) a.logprob[r] = greedy ? 0.f : static_cast<float>(z_of(j) - log(left));
+    if (a.lse) a.lse[r] = static_cast<float>(w.m / T + log(total));
+    if (bits && a.error_flag) atomicOr(a.error_flag, bits);
+  }
+  return true;
+}
+
+template <int NT> constexpr int cells_per() { return (kCells + NT - 1) / NT; }
+
+// The count of a cell of the table.
+template <int NT>
+__device__ __forceinline__ int cell_count(const CodeLds<NT>& L, int j) {
+  if (j < kCodes) return static_cast<int>(L.tab[kCodes - 1 - j]);
+  if (j == kCodes) return static_cast<int>(L.tiny_n);
+  return j < kCells ? static_cast<int>(L.tab[4096 + j - kCodes - 1]) : 0;
+}
+
+template <typename E, int NT, int U>
+__global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
+  const int64_t r = blockIdx.x;
+  if constexpr (sizeof(E) == 2) {
+    __shared__ union {
+      DrawLds<NT> row;
+      CodeLds<NT> code;
+    } L;
+    constexpr int PER = cells_per<NT>();
+    int bits = 0;
+    bool greedy;
+    const Draw d = load_draw(a, r, bits, greedy);
+    const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
+    clear_codes(L.code);
+    CodeVisit<NT, U> f{L.code, 1.0 / static_cast<double>(d.T), weight_units(a.x.V)};
+    visit_row<E, NT, U, kLoadNormal>(row, a.x.V, f);
+    lds_barrier();
+    int cnt[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) cnt[k] = cell_count(L.code, static_cast<int>(threadIdx.x) * PER + k);
+    const bool done = draw_codes<NT, PER>(a, r, d, greedy, bits, cnt, L.code, [&](uint32_t code, int q) {
+      return nth_code<NT, U>(row, 0, a.x.V, code, q, L.code);
+    });
+    if (done) return;
+    lds_barrier();
+    draw_row<E, NT, U>(a, r, L.row);
+  } else {
+    __shared__ DrawLds<NT> L;
+    draw_row<E, NT, U>(a, r, L);
   }
 }
 
