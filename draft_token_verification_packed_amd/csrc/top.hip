@@ -1,5 +1,16 @@
 // The k first logits of every row in the order (value desc, index asc), with
 // the row's log-sum-exp of x / T: what a distillation loss reads of a teacher.
+//
+// One pass over the row. The k-th largest of the threads' own maxima bounds
+// the row's k-th largest element from below (k different elements are at
+// least that large), and it is close: with 512 threads and k = 64 about 70
+// elements of a shuffled row lie above it. So the first group of every thread
+// gives a bound, the stream keeps the indices of the elements at or above it
+// while it sums the exponentials, and the bound is raised after 2, 4, 8, ..
+// groups; at the end the kept elements above the last bound are ranked
+// against each other. Rows whose order defeats this (more kept than the list
+// holds, as in a rising row) are read once more with the last bound, and rows
+// of too many ties are searched a byte of the rank key at a time.
 #include "row_visit.hpp"
 #include "rows.hpp"
 
@@ -9,7 +20,7 @@ namespace {
 
 constexpr int kTopThreads = 512;
 constexpr int kTopUnroll = 2;
-constexpr int kTopList = 4096;    // elements a row may keep as candidates
+constexpr int kTopList = 4096;    // elements a row may keep
 
 // Order-preserving unsigned key of a float (-0 mapped to +0).
 __device__ __forceinline__ uint32_t up_key(float x) {
@@ -24,75 +35,125 @@ __device__ __forceinline__ uint64_t rank_key(float x, int e) {
   return (static_cast<uint64_t>(up_key(x)) << 32) | static_cast<uint32_t>(~e);
 }
 
+constexpr int kTopKeys = 1024;    // of them, those that are ranked
+
 template <int NT> struct TopLds {
   static constexpr int NW = NT / kWave;
-  uint64_t list[kTopList];
+  uint32_t list[kTopList];
+  uint64_t keys[kTopKeys];
+  float most[NT];                 // each thread's maximum
   uint32_t hist[256];
-  int n, digit, below;
+  int n, m, digit, below;
   float mc[NW];
   double s[NW];
-  int scan[NW];
 };
 
+// A lower bound of the k-th largest of the NT maxima in `most`: their keys'
+// leading kBits are searched, by every wave for itself.
+template <int NT, int kBits>
+__device__ __forceinline__ float kth_bound(const float* most, int k) {
+  constexpr int PER = NT / kWave;
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = up_key(most[(threadIdx.x & (kWave - 1)) + i * kWave]);
+  uint32_t p = 0;
+#pragma unroll 1
+  for (int b = 31; b >= 32 - kBits; --b) {
+    const uint32_t t = p | 1u << b;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n += __popcll(__builtin_amdgcn_ballot_w64(key[i] >= t));
+    p = n >= k ? t : p;
+  }
+  // keys below that of -inf are no values
+  return p < 0x00800000u ? -INFINITY : key_value(p);
+}
+
 template <typename E, int NT, int U>
-struct SumAll {
+struct TopVisit {
+  TopLds<NT>& L;
   ExpSum p;
-  float c;
+  float c, most, bound;
+  int k, head, at;   // at: groups seen
+
+  __device__ __forceinline__ void raise() {
+    lds_barrier();
+    L.most[threadIdx.x] = most;
+    lds_barrier();
+    bound = kth_bound<NT, sizeof(E) == 2 ? 16 : 20>(L.most, k);
+  }
+  __device__ __forceinline__ void keep(uint32_t mask, int v) {
+    constexpr int N = Elem<E>::kVec;
+    const int c = __popc(mask);
+    const int incl = wave_scan_incl(c);
+    int to = 0;
+    if ((threadIdx.x & (kWave - 1)) == kWave - 1) to = atomicAdd(&L.n, incl);
+    to = read_lane(to, kWave - 1) + incl - c;
+    while (mask) {
+      const int b = __ffs(mask) - 1;
+      mask &= mask - 1;
+      if (to < kTopList) L.list[to] = static_cast<uint32_t>(head + (v + b / N * NT) * N + b % N);
+      ++to;
+    }
+  }
   template <bool kPartial>
   __device__ __forceinline__ void group(const u32x4* w, int v, int nvec) {
     constexpr int N = Elem<E>::kVec;
+    if (at > 1 && (at & (at - 1)) == 0) raise();
+    ++at;
     float f[U * N];
     float gmax = -INFINITY;
+    uint32_t in = 0;   // the vectors that are there
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       Elem<E>::decode(w[u], f + u * N);
-      if (kPartial && v + u * NT >= nvec) {
+      const bool out = kPartial && v + u * NT >= nvec;
+      in |= out ? 0u : ((1u << N) - 1) << (u * N);
+      if (out) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) f[u * N + k] = -INFINITY;
+        for (int q = 0; q < N; ++q) f[u * N + q] = -INFINITY;
       }
 #pragma unroll
-      for (int k = 0; k < N; ++k) gmax = fmaxf(gmax, f[u * N + k]);
+      for (int q = 0; q < N; ++q) gmax = fmaxf(gmax, f[u * N + q]);
+    }
+    most = fmaxf(most, gmax);
+    if (__builtin_amdgcn_ballot_w64(gmax >= bound) != 0) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int q = 0; q < U * N; ++q) mask |= f[q] >= bound ? 1u << q : 0u;
+      keep(mask & in, v);
     }
     add_terms<U * N>(p, f, gmax, c);
   }
-  __device__ __forceinline__ void one(float x, int) { add_term(p, x, c); }
+  __device__ __forceinline__ void one(float x, int e) {
+    if (x >= bound) {
+      const int to = atomicAdd(&L.n, 1);
+      if (to < kTopList) L.list[to] = static_cast<uint32_t>(e);
+    }
+    most = fmaxf(most, x);
+    add_term(p, x, c);
+  }
 };
 
-// Calls f(key) for every element's rank key.
-template <typename E, int NT, int U, typename F>
-struct EachKey {
-  F& f;
-  int head;
-  template <bool kPartial>
-  __device__ __forceinline__ void group(const u32x4* w, int v, int nvec) {
-    constexpr int N = Elem<E>::kVec;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (kPartial && v + u * NT >= nvec) continue;
-      float x[N];
-      Elem<E>::decode(w[u], x);
-#pragma unroll
-      for (int k = 0; k < N; ++k) f(rank_key(x[k], head + (v + u * NT) * N + k));
-    }
-  }
-  __device__ __forceinline__ void one(float x, int e) { f(rank_key(x, e)); }
-};
-template <typename E, int NT, int U, typename F>
-__device__ __forceinline__ void each_key(const E* row, int V, F&& f) {
-  EachKey<E, NT, U, F> v{f, row_head(row, V)};
-  visit_row<E, NT, U, kLoadNormal>(row, V, v);
+// Whole rows element by element, for the rare paths.
+template <typename E, int NT, typename F>
+__device__ __forceinline__ void each_elem(const E* row, int V, F&& f) {
+#pragma unroll 1
+  for (int e = threadIdx.x; e < V; e += NT) f(Elem<E>::at(row, e), e);
 }
 
 // The key of the k-th element in rank order (k >= 1), a byte at a time from
 // the highest: the row is read once per byte.
-template <typename E, int NT, int U>
-__device__ uint64_t nth_key(const E* row, int V, int k, TopLds<NT>& L) {
+template <typename E, int NT>
+__device__ __forceinline__ uint64_t nth_key(const E* row, int V, int k, TopLds<NT>& L) {
   uint64_t prefix = 0;
   int left = k;
+#pragma unroll 1
   for (int shift = 56; shift >= 0; shift -= 8) {
     for (int b = threadIdx.x; b < 256; b += NT) L.hist[b] = 0;
     lds_barrier();
-    each_key<E, NT, U>(row, V, [&](uint64_t key) {
+    each_elem<E, NT>(row, V, [&](float x, int e) {
+      const uint64_t key = rank_key(x, e);
       if (shift == 56 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&L.hist[(key >> shift) & 255], 1u);
     });
     lds_barrier();
@@ -111,50 +172,81 @@ __device__ uint64_t nth_key(const E* row, int V, int k, TopLds<NT>& L) {
 }
 
 template <typename E, int NT, int U>
-__global__ __launch_bounds__(NT) void top_kernel(TopArgs a) {
+__global__ __launch_bounds__(NT, 6) void top_kernel(TopArgs a) {
   __shared__ TopLds<NT> L;
   constexpr int NW = NT / kWave;
   const int64_t r = blockIdx.x;
   const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
+  const int V = a.x.V;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  SumAll<E, NT, U> f;
-  f.p = ExpSum{-FLT_MAX, 0.0};
-  f.c = a.c;
-  visit_row<E, NT, U, kLoadNormal>(row, a.x.V, f);
+  if (tid == 0) L.n = L.m = 0;
+  TopVisit<E, NT, U> f{L, ExpSum{-FLT_MAX, 0.0}, a.c, -INFINITY, -INFINITY, a.k, row_head(row, V), 0};
+  visit_row<E, NT, U, kLoadStream>(row, V, f, [&](const u32x4* w, int nvec) {
+    float t = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[Elem<E>::kVec];
+      if (tid + u * NT < nvec) t = fmaxf(t, vec_max<E>(w[u], x));
+    }
+    f.most = t;
+    f.raise();
+  });
   const float mw = wave_all(f.p.mc, MaxOp());
   if (lane == 0) L.mc[wave] = mw;
-  lds_barrier();
+  f.raise();
   float mc = L.mc[0];
 #pragma unroll
   for (int w = 1; w < NW; ++w) mc = fmaxf(mc, L.mc[w]);
   const double sw = wave_sum_f64(sum_at(f.p.s, f.p.mc, mc));
   if (lane == 0) L.s[wave] = sw;
-  lds_barrier();
-  double total = 0.0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) total += L.s[w];
 
-  const uint64_t last = nth_key<E, NT, U>(row, a.x.V, a.k, L);
-  if (tid == 0) L.n = 0;
-  lds_barrier();
-  each_key<E, NT, U>(row, a.x.V, [&](uint64_t key) {
-    if (key >= last) {
-      const int at = atomicAdd(&L.n, 1);
-      if (at < kTopList) L.list[at] = key;
+  // ---- the kept elements at or above the last bound
+  const int n = L.n;
+  auto take = [&](float x, int e) {
+    if (x >= f.bound) {
+      const int to = atomicAdd(&L.m, 1);
+      if (to < kTopKeys) L.keys[to] = rank_key(x, e);
     }
-  });
+  };
+  if (n <= kTopList) {
+    for (int i = tid; i < n; i += NT) {
+      const int e = static_cast<int>(L.list[i]);
+      take(Elem<E>::at(row, e), e);
+    }
+  } else {
+    each_elem<E, NT>(row, V, take);
+  }
   lds_barrier();
-  const int n = min(L.n, kTopList);
-  for (int i = tid; i < n; i += NT) {
-    const uint64_t key = L.list[i];
+  int m = L.m;
+  if (m > kTopKeys || m < a.k) {
+    // too many ties at the bound (or NaN elements, which no bound keeps)
+    const uint64_t last = nth_key<E, NT>(row, V, a.k, L);
+    if (tid == 0) L.m = 0;
+    lds_barrier();
+    each_elem<E, NT>(row, V, [&](float x, int e) {
+      const uint64_t key = rank_key(x, e);
+      if (key >= last) {
+        const int to = atomicAdd(&L.m, 1);
+        if (to < kTopKeys) L.keys[to] = key;
+      }
+    });
+    lds_barrier();
+    m = min(L.m, kTopKeys);
+  }
+  for (int i = tid; i < m; i += NT) {
+    const uint64_t key = L.keys[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += L.list[j] > key ? 1 : 0;
+#pragma unroll 4
+    for (int j = 0; j < m; ++j) rank += L.keys[j] > key ? 1 : 0;
     if (rank < a.k) {
       a.values[r * a.k + rank] = key_value(static_cast<uint32_t>(key >> 32));
       a.ids[r * a.k + rank] = static_cast<int>(~static_cast<uint32_t>(key));
     }
   }
   if (tid == 0) {
+    double total = 0.0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) total += L.s[w];
     const bool ok = total > 0.0 && total < INFINITY;
     if (a.lse) a.lse[r] = static_cast<float>(0.69314718055994530942 * (static_cast<double>(mc) + log2(total)));
     if (!ok && a.error_flag) atomicOr(a.error_flag, VSV_FLAG_LOGITS);
