@@ -6,7 +6,7 @@
 // least that large), and it is close: with 512 threads and k = 64 about 70
 // elements of a shuffled row lie above it. So the first group of every thread
 // gives a bound, the stream keeps the indices of the elements at or above it
-// while it sums the exponentials, and the bound is raised after 2, 4, 8, ..
+// while it sums the exponentials, and the bound is raised after 4, 16 and 64
 // groups; at the end the kept elements above the last bound are ranked
 // against each other. Rows whose order defeats this (more kept than the list
 // holds, as in a rising row) are read once more with the last bound, and rows
@@ -18,8 +18,14 @@ namespace vsv {
 
 namespace {
 
-constexpr int kTopThreads = 512;
-constexpr int kTopUnroll = 2;
+// A wave has to see k of the workgroup's maxima: up to kFewTop of them 256
+// threads serve, with fewer maxima to search and a list more workgroups can
+// hold per CU; beyond it 512. The top 64 of 640 bf16 rows of 152064 take 50
+// us with 256 threads against 54, the top 256 of them 73 us with 512 and 2.4
+// ms with 256 (the bound is the least maximum there and keeps too much).
+// Vectors per group: four, for bf16 rows of 512 threads two (73 us; 77 with
+// four, whose registers leave room for fewer workgroups).
+constexpr int kFewTop = 64;
 constexpr int kTopList = 4096;    // elements a row may keep
 
 // Order-preserving unsigned key of a float (-0 mapped to +0).
@@ -56,9 +62,19 @@ __device__ __forceinline__ float kth_bound(const float* most, int k) {
   uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) key[i] = up_key(most[(threadIdx.x & (kWave - 1)) + i * kWave]);
-  uint32_t p = 0;
+  // leading bits that all of them share are no question
+  uint32_t all = ~0u, any = 0u;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    all &= key[i];
+    any |= key[i];
+  }
+  all = wave_all(all, [](uint32_t x, uint32_t y) { return x & y; });
+  any = wave_all(any, [](uint32_t x, uint32_t y) { return x | y; });
+  const int same = __clz(all ^ any);   // 32 where all are equal
+  uint32_t p = same >= 32 ? any : any & ~(0xFFFFFFFFu >> same);
 #pragma unroll 1
-  for (int b = 31; b >= 32 - kBits; --b) {
+  for (int b = 31 - same; b >= 32 - kBits; --b) {
     const uint32_t t = p | 1u << b;
     int n = 0;
 #pragma unroll
@@ -99,7 +115,7 @@ struct TopVisit {
   template <bool kPartial>
   __device__ __forceinline__ void group(const u32x4* w, int v, int nvec) {
     constexpr int N = Elem<E>::kVec;
-    if (at > 1 && (at & (at - 1)) == 0) raise();
+    if (at == 4 || at == 16 || at == 64) raise();
     ++at;
     float f[U * N];
     float gmax = -INFINITY;
@@ -171,8 +187,8 @@ __device__ __forceinline__ uint64_t nth_key(const E* row, int V, int k, TopLds<N
   return prefix;
 }
 
-template <typename E, int NT, int U>
-__global__ __launch_bounds__(NT, 6) void top_kernel(TopArgs a) {
+template <typename E, int NT, int U, int kWaves>
+__global__ __launch_bounds__(NT, kWaves) void top_kernel(TopArgs a) {
   __shared__ TopLds<NT> L;
   constexpr int NW = NT / kWave;
   const int64_t r = blockIdx.x;
@@ -255,7 +271,12 @@ __global__ __launch_bounds__(NT, 6) void top_kernel(TopArgs a) {
 
 template <typename E>
 hipError_t top_t(const TopArgs& a, hipStream_t s) {
-  top_kernel<E, kTopThreads, kTopUnroll><<<dim3(a.x.N), dim3(kTopThreads), 0, s>>>(a);
+  constexpr bool kTwo = sizeof(E) == 2;
+  if (a.k <= kFewTop) {
+    top_kernel<E, 256, 4, 4><<<dim3(a.x.N), dim3(256), 0, s>>>(a);
+  } else {
+    top_kernel<E, 512, kTwo ? 2 : 4, kTwo ? 6 : 4><<<dim3(a.x.N), dim3(512), 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
