@@ -457,6 +457,23 @@ def _same_device(device, **tensors):
             raise ValueError("%s is on %s, the logits on %s" % (name, t.device, device))
 
 
+_flag_words = {}
+
+
+def _new_flag(device, stream):
+    """A zeroed int32 [1] error word of its own: cut from a block that is
+    zero-filled on the call's stream once in a thousand calls, or filled by
+    the call itself where it is captured (so that a replay starts from 0)."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    words = _flag_words.setdefault((device.index, stream.cuda_stream), [])
+    try:
+        return words.pop()
+    except IndexError:
+        words.extend(torch.zeros((1024, 1), dtype=torch.int32, device=device).unbind(0))
+        return words.pop()
+
+
 def _flag(error_flag, device):
     """The caller's sticky error word, if given."""
     if error_flag is not None:
@@ -484,7 +501,7 @@ def sample_rows(logits, temperature, top_k, top_p, min_p, uniforms, vocab=None, 
         out = dict(token=torch.empty(R, dtype=torch.int32, device=dev),
                    logprob=torch.empty(R, dtype=torch.float32, device=dev),
                    lse=torch.empty(R, dtype=torch.float32, device=dev),
-                   error_flag=torch.zeros(1, dtype=torch.int32, device=dev))
+                   error_flag=_new_flag(dev, on.stream))
         on.keep(logits, temperature, top_k, top_p, min_p, uniforms)
         _check(lib().vsv_sample_rows(_ptr(logits), dtype, V, ld, R, _ptr(temperature), _ptr(top_k), _ptr(top_p),
                                      _ptr(min_p), _ptr(uniforms), _ptr(out["token"]), _ptr(out["logprob"]),
@@ -506,7 +523,7 @@ def top_logits(logits, k, temperature=1.0, vocab=None, stream=None):
         out = dict(values=torch.empty((R, k), dtype=torch.float32, device=dev),
                    ids=torch.empty((R, k), dtype=torch.int32, device=dev),
                    lse=torch.empty(R, dtype=torch.float32, device=dev),
-                   error_flag=torch.zeros(1, dtype=torch.int32, device=dev))
+                   error_flag=_new_flag(dev, on.stream))
         on.keep(logits)
         _check(lib().vsv_top_logits(_ptr(logits), dtype, V, ld, R, k, float(temperature), _ptr(out["values"]),
                                     _ptr(out["ids"]), _ptr(out["lse"]), _ptr(out["error_flag"]), s))

@@ -26,8 +26,14 @@ namespace vsv {
 
 namespace {
 
+// Vectors per thread and group: two in the forward pass (22.7 us for 300
+// bf16 rows of 152064, 25.8 with three; the same for 640 and 2048), three
+// where the gradient follows in the same launch (2048 rows: 290 us, 298 with
+// two), four for the gradient's own pass (2048 rows: 245 us, 247 with two).
 constexpr int kDistThreads = 512;
-constexpr int kDistUnroll = 2;
+constexpr int kSumUnroll = 2;
+constexpr int kBothUnroll = 3;
+constexpr int kGradUnroll = 4;
 constexpr int kEntries = VSV_MAX_TOP / kWave;   // entries per lane of the wave that handles them
 // Vectors whose named elements one LDS map holds, a byte per vector (and two
 // for the elements before and after them). Longer rows go in pieces.
@@ -540,7 +546,7 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a) {
   __shared__ float teach[VSV_MAX_TOP];
   const int64_t r = blockIdx.x;
   row_state<E, NT, U, kRest, kLoadNormal>(a, r, L);
-  grad_range<E, NT, U>(a, r, 0, a.x.V, L.row, ids, teach);
+  grad_range<E, NT, kGradUnroll>(a, r, 0, a.x.V, L.row, ids, teach);
 }
 
 template <typename E>
@@ -548,14 +554,14 @@ hipError_t forward_t(const DistillArgs& a, hipStream_t s) {
   const bool rest = a.tlse != nullptr;
   if (a.parts > 1) {
     const int64_t grid = static_cast<int64_t>(a.x.N) * a.parts;
-    auto part = rest ? distill_part_kernel<E, kDistThreads, kDistUnroll, true>
-                     : distill_part_kernel<E, kDistThreads, kDistUnroll, false>;
+    auto part = rest ? distill_part_kernel<E, kDistThreads, kSumUnroll, true>
+                     : distill_part_kernel<E, kDistThreads, kSumUnroll, false>;
     part<<<dim3(static_cast<unsigned>(grid)), dim3(kDistThreads), 0, s>>>(a);
     auto join = rest ? distill_join_kernel<E, true> : distill_join_kernel<E, false>;
     join<<<dim3(a.x.N), dim3(kWave), 0, s>>>(a);
   } else {
-    auto k = rest ? distill_forward_kernel<E, kDistThreads, kDistUnroll, true>
-                  : distill_forward_kernel<E, kDistThreads, kDistUnroll, false>;
+    auto k = rest ? distill_forward_kernel<E, kDistThreads, kSumUnroll, true>
+                  : distill_forward_kernel<E, kDistThreads, kSumUnroll, false>;
     k<<<dim3(a.x.N), dim3(kDistThreads), 0, s>>>(a);
   }
   return hipGetLastError();
@@ -564,15 +570,15 @@ hipError_t forward_t(const DistillArgs& a, hipStream_t s) {
 template <typename E>
 hipError_t backward_t(const DistillArgs& a, hipStream_t s) {
   const int64_t grid = static_cast<int64_t>(a.x.N) * a.parts;
-  distill_backward_kernel<E, kDistThreads, kDistUnroll>
+  distill_backward_kernel<E, kDistThreads, kGradUnroll>
       <<<dim3(static_cast<unsigned>(grid)), dim3(kDistThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename E>
 hipError_t grad_t(const DistillArgs& a, hipStream_t s) {
-  auto k = a.tlse ? distill_grad_kernel<E, kDistThreads, kDistUnroll, true>
-                  : distill_grad_kernel<E, kDistThreads, kDistUnroll, false>;
+  auto k = a.tlse ? distill_grad_kernel<E, kDistThreads, kBothUnroll, true>
+                  : distill_grad_kernel<E, kDistThreads, kBothUnroll, false>;
   k<<<dim3(a.x.N), dim3(kDistThreads), 0, s>>>(a);
   return hipGetLastError();
 }
@@ -582,7 +588,13 @@ hipError_t grad_t(const DistillArgs& a, hipStream_t s) {
 int32_t distill_parts(int32_t num_rows, int32_t vocab, int32_t dtype) {
   const int64_t bytes = static_cast<int64_t>(vocab) * (dtype == VSV_BF16 ? 2 : 4);
   const int64_t n = num_rows > 0 ? num_rows : 1;
-  int64_t p = 512 / n;
+  // Rows are cut while whole rows would leave CUs idle. From 128 rows on a
+  // workgroup per row is the better use, since it needs no second launch and
+  // its gradient follows the sums in the same one: 128 fp32 rows of 32768
+  // take 8.8 us forward and 17.7 with the gradient, 10.7 and 23 in two parts;
+  // 160 bf16 rows of 152064 14.6 and 33.6, against 16.0 and 40.7 in three.
+  // 64 of them take 11.8 and 25.5 in parts, 13.0 and 30.6 whole.
+  int64_t p = 192 / n;
   const int64_t most = bytes / 16384;
   if (p > most) p = most;
   if (p > kWave) p = kWave;
