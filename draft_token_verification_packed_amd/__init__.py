@@ -413,60 +413,70 @@ def draft_confidence(draft_logits, selected=None, vocab=None, stream=None):
     return conf, lse, flag
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _on:
     """The device of a call's tensors as the current one, and the stream its
     outputs are allocated and its kernels run on: `stream`, or the device's
     current stream. Kernels launch on the current device, so a call on
     another device's tensors switches to it."""
 
-    __slots__ = ("device", "stream", "other", "_back", "_swap")
+    __slots__ = ("device", "raw", "_swap", "other")
 
     def __init__(self, device, stream):
         self.device = device
-        self.other = stream is not None and stream != torch.cuda.current_stream(device)
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise ValueError("the stream belongs to %s, the tensors to %s" % (self.stream.device, device))
+        self._swap = self.other = None
+        if stream is None:
+            self.raw = _raw_stream(device.index)
+            if device.index != torch.cuda.current_device():
+                self._swap = torch.cuda.device(device)
+        else:
+            if stream.device != device:
+                raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, device))
+            self.raw = stream.cuda_stream
+            if stream != torch.cuda.current_stream(device) or device.index != torch.cuda.current_device():
+                self.other = stream
+                self._swap = torch.cuda.stream(stream)   # also switches the device
 
     def __enter__(self):
-        self._swap = self._back = None
-        if self.other:
-            self._swap = torch.cuda.stream(self.stream)   # also switches the device
+        if self._swap is not None:
             self._swap.__enter__()
-        elif self.device.index != torch.cuda.current_device():
-            self._back = torch.cuda.device(self.device)
-            self._back.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        return self.raw
 
     def __exit__(self, *exc):
-        for c in (self._swap, self._back):
-            if c is not None:
-                c.__exit__(*exc)
+        if self._swap is not None:
+            self._swap.__exit__(*exc)
         return False
 
     def keep(self, *tensors):
-        if self.other:
+        if self.other is not None:
             for t in tensors:
                 if t is not None:
-                    t.record_stream(self.stream)
+                    t.record_stream(self.other)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError("%s is on %s, the logits on %s" % (name, t.device, device))
+            raise ValueError("a tensor is on %s, the logits on %s" % (t.device, device))
 
 
 _flag_words = {}
 
 
-def _new_flag(device, stream):
+def _new_flag(device, raw_stream):
     """A zeroed int32 [1] error word of its own: cut from a block that is
     zero-filled on the call's stream once in a thousand calls, or filled by
     the call itself where it is captured (so that a replay starts from 0)."""
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(1, dtype=torch.int32, device=device)
-    words = _flag_words.setdefault((device.index, stream.cuda_stream), [])
+    words = _flag_words.setdefault((device.index, raw_stream), [])
     try:
         return words.pop()
     except IndexError:
@@ -478,7 +488,7 @@ def _flag(error_flag, device):
     """The caller's sticky error word, if given."""
     if error_flag is not None:
         _vec(error_flag, 1, torch.int32, "error_flag")
-        _same_device(device, error_flag=error_flag)
+        _same_device(device, error_flag)
     return error_flag
 
 
@@ -495,17 +505,17 @@ def sample_rows(logits, temperature, top_k, top_p, min_p, uniforms, vocab=None, 
     for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (uniforms, "uniforms")):
         _vec(t, R, torch.float32, n)
     _vec(top_k, R, torch.int32, "top_k")
-    _same_device(dev, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, uniforms=uniforms)
+    _same_device(dev, temperature, top_k, top_p, min_p, uniforms)
     on = _on(dev, stream)
     with on as s:
         out = dict(token=torch.empty(R, dtype=torch.int32, device=dev),
                    logprob=torch.empty(R, dtype=torch.float32, device=dev),
                    lse=torch.empty(R, dtype=torch.float32, device=dev),
-                   error_flag=_new_flag(dev, on.stream))
+                   error_flag=_new_flag(dev, s))
         on.keep(logits, temperature, top_k, top_p, min_p, uniforms)
-        _check(lib().vsv_sample_rows(_ptr(logits), dtype, V, ld, R, _ptr(temperature), _ptr(top_k), _ptr(top_p),
-                                     _ptr(min_p), _ptr(uniforms), _ptr(out["token"]), _ptr(out["logprob"]),
-                                     _ptr(out["lse"]), _ptr(out["error_flag"]), s))
+        _check(lib().vsv_sample_rows(_at(logits), dtype, V, ld, R, _at(temperature), _at(top_k), _at(top_p),
+                                     _at(min_p), _at(uniforms), _at(out["token"]), _at(out["logprob"]),
+                                     _at(out["lse"]), _at(out["error_flag"]), s))
     return out
 
 
@@ -523,10 +533,10 @@ def top_logits(logits, k, temperature=1.0, vocab=None, stream=None):
         out = dict(values=torch.empty((R, k), dtype=torch.float32, device=dev),
                    ids=torch.empty((R, k), dtype=torch.int32, device=dev),
                    lse=torch.empty(R, dtype=torch.float32, device=dev),
-                   error_flag=_new_flag(dev, on.stream))
+                   error_flag=_new_flag(dev, s))
         on.keep(logits)
-        _check(lib().vsv_top_logits(_ptr(logits), dtype, V, ld, R, k, float(temperature), _ptr(out["values"]),
-                                    _ptr(out["ids"]), _ptr(out["lse"]), _ptr(out["error_flag"]), s))
+        _check(lib().vsv_top_logits(_at(logits), dtype, V, ld, R, k, float(temperature), _at(out["values"]),
+                                    _at(out["ids"]), _at(out["lse"]), _at(out["error_flag"]), s))
     return out
 
 
@@ -541,9 +551,9 @@ def _distill_args(student_logits, teacher_ids, teacher_logits, teacher_lse, temp
             raise ValueError("%s must be a contiguous %s CUDA matrix [%d, %d]" % (n, dt, N, K))
     if teacher_lse is not None:
         _vec(teacher_lse, N, torch.float32, "teacher_lse")
-    _same_device(dev, teacher_ids=teacher_ids, teacher_logits=teacher_logits, teacher_lse=teacher_lse)
-    return Distill(_ptr(student_logits), dtype, V, ld, N, K, _ptr(teacher_ids), _ptr(teacher_logits),
-                   _ptr(teacher_lse), float(temperature))
+    _same_device(dev, teacher_ids, teacher_logits, teacher_lse)
+    return Distill(_at(student_logits), dtype, V, ld, N, K, _at(teacher_ids), _at(teacher_logits),
+                   _at(teacher_lse), float(temperature))
 
 
 def _distill_scratch(d, dev):
@@ -554,8 +564,23 @@ def _distill_scratch(d, dev):
 def _row_weight(row_weight, d, dev):
     if row_weight is not None:
         _vec(row_weight, d.num_rows, torch.float32, "row_weight")
-        _same_device(dev, row_weight=row_weight)
+        _same_device(dev, row_weight)
     return row_weight
+
+
+def _distill_losses(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature, error_flag, stream,
+                    with_state):
+    d = _distill_args(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    dev = student_logits.device
+    _flag(error_flag, dev)
+    on = _on(dev, stream)
+    with on as s:
+        loss = torch.empty(d.num_rows, dtype=torch.float32, device=dev)
+        state = torch.empty((d.num_rows, DISTILL_STATE), dtype=torch.float64, device=dev) if with_state else None
+        ws, n = _distill_scratch(d, dev)
+        on.keep(student_logits, teacher_ids, teacher_logits, teacher_lse, error_flag)
+        _check(lib().vsv_distill_forward(ctypes.byref(d), _at(loss), _at(state), _at(error_flag), _at(ws), n, s))
+    return loss, state
 
 
 def distill_forward(student_logits, teacher_ids, teacher_logits, teacher_lse=None, temperature=1.0, error_flag=None,
@@ -563,17 +588,8 @@ def distill_forward(student_logits, teacher_ids, teacher_logits, teacher_lse=Non
     """(loss [N] float32, state [N, DISTILL_STATE] float64) of every student row
     (vsv_distill_forward); `state` is what distill_backward takes. Device
     conditions set bits in `error_flag` (int32 [1]) if given."""
-    d = _distill_args(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature)
-    dev = student_logits.device
-    _flag(error_flag, dev)
-    on = _on(dev, stream)
-    with on as s:
-        loss = torch.empty(d.num_rows, dtype=torch.float32, device=dev)
-        state = torch.empty((d.num_rows, DISTILL_STATE), dtype=torch.float64, device=dev)
-        ws, n = _distill_scratch(d, dev)
-        on.keep(student_logits, teacher_ids, teacher_logits, teacher_lse, error_flag)
-        _check(lib().vsv_distill_forward(ctypes.byref(d), _ptr(loss), _ptr(state), _ptr(error_flag), _ptr(ws), n, s))
-    return loss, state
+    return _distill_losses(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature, error_flag, stream,
+                           True)
 
 
 def distill_backward(row_weight, student_logits, teacher_ids, teacher_logits, state, teacher_lse=None,
@@ -590,7 +606,7 @@ def distill_backward(row_weight, student_logits, teacher_ids, teacher_logits, st
     with on as s:
         grad = torch.empty((d.num_rows, d.vocab), dtype=student_logits.dtype, device=dev)
         on.keep(row_weight, student_logits, teacher_ids, teacher_logits, teacher_lse, state)
-        _check(lib().vsv_distill_backward(ctypes.byref(d), _ptr(state), _ptr(row_weight), _ptr(grad), d.vocab, s))
+        _check(lib().vsv_distill_backward(ctypes.byref(d), _at(state), _at(row_weight), _at(grad), d.vocab, s))
     return grad
 
 
@@ -608,8 +624,8 @@ def distill_loss_grad(student_logits, teacher_ids, teacher_logits, row_weight=No
         grad = torch.empty((d.num_rows, d.vocab), dtype=student_logits.dtype, device=dev)
         ws, n = _distill_scratch(d, dev)
         on.keep(student_logits, teacher_ids, teacher_logits, teacher_lse, row_weight, error_flag)
-        _check(lib().vsv_distill_grad(ctypes.byref(d), _ptr(row_weight), _ptr(loss), _ptr(grad), d.vocab,
-                                      _ptr(error_flag), _ptr(ws), n, s))
+        _check(lib().vsv_distill_grad(ctypes.byref(d), _at(row_weight), _at(loss), _at(grad), d.vocab,
+                                      _at(error_flag), _at(ws), n, s))
     return loss, grad
 
 
@@ -649,6 +665,9 @@ def distill_loss(student_logits, teacher_ids, teacher_logits, teacher_lse=None, 
         student_logits = student_logits[:, :int(vocab)]
     if student_logits.dim() == 2 and student_logits.shape[0] > 1 and student_logits.stride(0) < student_logits.shape[1]:
         student_logits = student_logits.contiguous()   # one row standing for several
+    if not (student_logits.requires_grad and torch.is_grad_enabled()):
+        return _distill_losses(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature, error_flag, None,
+                               False)[0]
     return _DistillLoss.apply(student_logits, teacher_ids, teacher_logits, teacher_lse, float(temperature), error_flag)
 
 

@@ -590,12 +590,14 @@ int32_t distill_parts(int32_t num_rows, int32_t vocab, int32_t dtype) {
   const int64_t n = num_rows > 0 ? num_rows : 1;
   // Rows are cut while whole rows would leave CUs idle. From 128 rows on a
   // workgroup per row is the better use, since it needs no second launch and
-  // its gradient follows the sums in the same one: 128 fp32 rows of 32768
-  // take 8.8 us forward and 17.7 with the gradient, 10.7 and 23 in two parts;
-  // 160 bf16 rows of 152064 14.6 and 33.6, against 16.0 and 40.7 in three.
-  // 64 of them take 11.8 and 25.5 in parts, 13.0 and 30.6 whole.
+  // its gradient follows the sums in the same one: 160 bf16 rows of 152064
+  // take 14.6 us forward and 33.6 with the gradient, against 16.0 and 40.7 in
+  // three parts; 64 of them take 11.8 and 25.5 in parts, 13.0 and 30.6 whole.
+  // Short rows are not worth the second launch: 128 fp32 rows of 32768 take
+  // 8.8 us whole and 10.7 in two parts.
+  if (bytes < 196608) return 1;
   int64_t p = 192 / n;
-  const int64_t most = bytes / 16384;
+  const int64_t most = bytes / 49152;
   if (p > most) p = most;
   if (p > kWave) p = kWave;
   return p < 1 ? 1 : static_cast<int32_t>(p);
