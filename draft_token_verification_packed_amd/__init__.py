@@ -24,6 +24,7 @@ Entry points mirror the C ABI in include/vspec_verify.h:
     goodput_select(prefix_acceptance, cost_ms, batch_size, current, switch_min_gain)
 """
 import ctypes
+import itertools
 import os
 
 import torch  # load torch's HIP runtime first so the library binds to it
@@ -468,6 +469,7 @@ def _same_device(device, *tensors):
 
 
 _flag_words = {}
+_FLAG_BLOCK = 1024
 
 
 def _new_flag(device, raw_stream):
@@ -476,12 +478,14 @@ def _new_flag(device, raw_stream):
     the call itself where it is captured (so that a replay starts from 0)."""
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(1, dtype=torch.int32, device=device)
-    words = _flag_words.setdefault((device.index, raw_stream), [])
-    try:
-        return words.pop()
-    except IndexError:
-        words.extend(torch.zeros((1024, 1), dtype=torch.int32, device=device).unbind(0))
-        return words.pop()
+    key = (device.index, raw_stream)
+    block, count = _flag_words.get(key, (None, None))
+    i = next(count) if block is not None else _FLAG_BLOCK
+    if i >= _FLAG_BLOCK:
+        block, count = torch.zeros(_FLAG_BLOCK, dtype=torch.int32, device=device), itertools.count()
+        i = next(count)
+        _flag_words[key] = (block, count)
+    return block[i:i + 1]
 
 
 def _flag(error_flag, device):
