@@ -85,7 +85,8 @@ DISTILL_STATE = 5
 SYMBOLS = ("vsv_workspace_bytes", "vsv_workspace_init", "vsv_verify_greedy", "vsv_verify_greedy_relaxed",
            "vsv_verify_greedy_static",
            "vsv_verify_sampled",
-           "vsv_verify_probabilistic", "vsv_draft_confidence", "vsv_sample_rows", "vsv_top_logits",
+           "vsv_verify_probabilistic", "vsv_draft_confidence", "vsv_sample_workspace_bytes", "vsv_sample_rows",
+           "vsv_top_logits",
            "vsv_distill_workspace_bytes", "vsv_distill_forward", "vsv_distill_backward", "vsv_distill_grad",
            "vsv_allocate_verify", "vsv_goodput_init", "vsv_goodput_observe",
            "vsv_goodput_step", "vsv_goodput_select", "vsv_status_string", "vsv_test_withhold_row_word", "vsv_version")
@@ -134,7 +135,9 @@ def lib():
     L.vsv_verify_probabilistic.restype = ctypes.c_int
     L.vsv_draft_confidence.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp]
     L.vsv_draft_confidence.restype = ctypes.c_int
-    L.vsv_sample_rows.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.vsv_sample_workspace_bytes.argtypes = [i32, i32, i32]
+    L.vsv_sample_workspace_bytes.restype = sz
+    L.vsv_sample_rows.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.vsv_sample_rows.restype = ctypes.c_int
     L.vsv_top_logits.argtypes = [vp, i32, i32, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]
     L.vsv_top_logits.restype = ctypes.c_int
@@ -516,10 +519,12 @@ def sample_rows(logits, temperature, top_k, top_p, min_p, uniforms, vocab=None, 
                    logprob=torch.empty(R, dtype=torch.float32, device=dev),
                    lse=torch.empty(R, dtype=torch.float32, device=dev),
                    error_flag=_new_flag(dev, s))
+        n = lib().vsv_sample_workspace_bytes(R, V, dtype)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         on.keep(logits, temperature, top_k, top_p, min_p, uniforms)
         _check(lib().vsv_sample_rows(_at(logits), dtype, V, ld, R, _at(temperature), _at(top_k), _at(top_p),
                                      _at(min_p), _at(uniforms), _at(out["token"]), _at(out["logprob"]),
-                                     _at(out["lse"]), _at(out["error_flag"]), s))
+                                     _at(out["lse"]), _at(out["error_flag"]), _at(ws), n, s))
     return out
 
 

@@ -231,16 +231,26 @@ vsv_status vsv_draft_confidence(const void* draft_logits, int32_t dtype, int32_t
   return vsv::launch_confidence(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 
+size_t vsv_sample_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtype) {
+  if (num_rows < 1 || vocab < 1 || !dtype_ok(dtype)) return 0;
+  const size_t parts = static_cast<size_t>(vsv::draw_parts(num_rows, vocab, dtype));
+  return parts < 2 ? 0 : static_cast<size_t>(num_rows) * parts * vsv::draw_part_bytes(dtype);
+}
+
 vsv_status vsv_sample_rows(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows,
                            const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                            const float* uniform, int32_t* token, float* logprob, float* lse, int32_t* error_flag,
-                           hipStream_t stream) {
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (num_rows < 0) return VSV_EINVAL;
   if (num_rows == 0) return VSV_OK;
   if (!rows_ok(logits, dtype, vocab, ld, num_rows)) return VSV_EINVAL;
   if (!temperature || !top_k || !top_p || !min_p || !uniform || !token) return VSV_EINVAL;
+  const int32_t parts = vsv::draw_parts(num_rows, vocab, dtype);
+  if (parts > 1 && (!workspace || !aligned(workspace, 16) ||
+                    workspace_bytes < vsv_sample_workspace_bytes(num_rows, vocab, dtype)))
+    return VSV_EWORKSPACE;
   const vsv::DrawArgs a{{logits, ld, vocab, num_rows, dtype}, temperature, top_k, top_p, min_p, uniform,
-                        token, logprob, lse, error_flag};
+                        token, logprob, lse, error_flag, workspace, parts};
   return vsv::launch_draw(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 

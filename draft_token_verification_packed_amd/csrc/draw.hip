@@ -36,8 +36,10 @@ constexpr int kDrawThreads = 512;
 constexpr int kDrawUnroll = 2;
 constexpr int kBins = 4096;
 constexpr int kReach = 1536;       // bins below the maximum that count (48 T)
+constexpr int kBase = kReach + 2;  // about where the first group's maximum lies
 constexpr double kPerT = 32.0;     // bins per T
 constexpr int kList = 4096;        // elements the gathered list holds
+constexpr int kMostParts = 8;
 constexpr int kFew = 128;          // lists decided by direct comparison
 // Beyond this |32 x / T| bins are too coarse in float64 to trust.
 constexpr double kFarBin = 4194304.0;
@@ -86,12 +88,16 @@ template <int NT> struct DrawLds {
   ull kept;
   double cut;
   int n, before, j[8], digit[2];
+  uint32_t parts;
+  double ptop[kMostParts];
 };
 
 // ---------------------------------------------------------------- bins
 
 // Position of an element among the bins: t = fma(x, s, k) with k = 1.5 2^52
-// minus an integer rounds to the bin's number in the low bits of t.
+// minus an even integer rounds to the bin's number in the low bits of t
+// (even, so that a y halfway between two bins goes to the same one on every
+// grid).
 constexpr double kMagic = 6755399441055744.0;         // 1.5 * 2^52
 constexpr uint32_t kMagicHi = 0x43380000u;
 struct Grid {
@@ -386,23 +392,22 @@ __device__ __forceinline__ Draw load_draw(const DrawArgs& a, int64_t r, int& bit
 // and one below 2^52.
 __device__ __forceinline__ double weight_units(int V) { return ldexp(1.0, min(50, 62 - (32 - __clz(V)))); }
 
-// Row r by linear bins, by the whole workgroup.
-template <typename E, int NT, int U>
-__device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<NT>& L) {
-  constexpr int NW = NT / kWave;
-  constexpr int PER = kReach / NT;
-  static_assert(kReach % NT == 0 && kFew <= NT, "bins per thread");
-  const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
-  const int V = a.x.V;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  int bits = 0;
-  bool greedy;
-  const Draw d = load_draw(a, r, bits, greedy);
-  const bool count = d.top_k > 0 && d.top_k < V;
-  const double T = static_cast<double>(d.T);
-  const double one = weight_units(V);
+// ---------------------------------------------------------------- rows and parts
 
-  // ---- the row into bins
+// The bins of a range of a row: where they lie, its IEEE maximum (finite or
+// the bins mean nothing), and whether it lies too far out for bins.
+struct Binned {
+  Grid g;
+  float m;
+  bool far;
+};
+
+// Elements [0, V) at `row` into L.bin (and L.u.cnt), by the whole workgroup.
+template <typename E, int NT, int U>
+__device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, double T, double one, bool count,
+                                           DrawLds<NT>& L) {
+  constexpr int NW = NT / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   Grid g{kPerT / T, 0.0};
   float m = -INFINITY;
   bool far = false;
@@ -421,7 +426,7 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     auto place = [&](float ref) {
       const double y = static_cast<double>(ref) * f.g.s;
       far = !(fabs(y) < kFarBin);
-      f.g.k = kMagic - (far ? 0.0 : rint(y)) + static_cast<double>(kReach);
+      f.g.k = kMagic - (far ? 0.0 : 2.0 * rint(0.5 * y)) + static_cast<double>(kBase);
     };
     visit_row<E, NT, U, kLoadNormal>(row, V, f, [&](const u32x4* w, int nvec) {
       float t = m;
@@ -467,17 +472,125 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
   // beyond it
   for (bool known = false;; known = true) {
     pass(known);
-    if (!(m > -INFINITY && m < INFINITY)) {
-      if (tid == 0) {
-        a.token[r] = 0;
-        if (a.logprob) a.logprob[r] = 0.f;
-        if (a.lse) a.lse[r] = m;
-        if (a.error_flag) atomicOr(a.error_flag, bits | VSV_FLAG_LOGITS);
-      }
-      return;
-    }
-    if (known || !(far || Grid::slot(g.t(m)) < 0)) break;
+    if (!(m > -INFINITY && m < INFINITY) || known || !(far || Grid::slot(g.t(m)) < 0)) break;
     lds_barrier();
+  }
+  return Binned{g, m, far};
+}
+
+// A row cut into parts, one workgroup each: what a part leaves in the scratch.
+struct BinPart {
+  double m, top, far;       // maximum, its bin's absolute number, 1 if too far out
+  double pad;
+  ull bin[kReach];          // downwards from the part's own top bin
+  uint32_t cnt[kReach];
+};
+// Part `part` of P equal shares of a row's 16-byte body.
+template <typename E>
+__device__ __forceinline__ void row_part(const E* row, int V, int P, int part, int& e0, int& e1) {
+  constexpr int N = Elem<E>::kVec;
+  const int head = row_head(row, V);
+  const int64_t nv = (V - head) / N;
+  e0 = part == 0 ? 0 : head + static_cast<int>(nv * part / P) * N;
+  e1 = part == P - 1 ? V : head + static_cast<int>(nv * (part + 1) / P) * N;
+}
+
+template <int NT>
+__device__ __forceinline__ void leave_bins(const Binned& b, bool count, BinPart* out, const DrawLds<NT>& L) {
+  const bool fine = b.m > -INFINITY && b.m < INFINITY;
+  const int top = fine && !b.far ? Grid::slot(b.g.t(b.m)) : 0;
+  if (threadIdx.x == 0) {
+    out->m = static_cast<double>(b.m);
+    out->top = static_cast<double>(top) - (b.g.k - kMagic);
+    out->far = fine && b.far ? 1.0 : 0.0;
+  }
+  if (fine && !b.far) {
+    for (int j = threadIdx.x; j < kReach; j += NT) {
+      out->bin[j] = L.bin[top - j];
+      if (count) out->cnt[j] = L.u.cnt[top - j];
+    }
+  }
+}
+
+// The bins of the whole row from its parts'. What other workgroups have just
+// written is far away (a microsecond a load), so every load of a step is
+// issued before any is used: one lane per part reads the heads, and the
+// parts' bins are read for all parts at once.
+template <int NT>
+__device__ __forceinline__ Binned join_bins(const BinPart* in, int P, double T, bool count, DrawLds<NT>& L) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  Binned b{Grid{kPerT / T, 0.0}, -INFINITY, false};
+  const BinPart& mine = in[lane < P ? lane : 0];
+  const float pm = static_cast<float>(mine.m);
+  const bool fine = pm > -INFINITY;
+  const double ptop = fine ? mine.top : -INFINITY;   // -inf: the part holds nothing
+  const int pfar = fine && mine.far != 0.0 ? 1 : 0;
+  if (tid < kMostParts) L.ptop[tid] = tid < P ? ptop : -INFINITY;
+  b.m = wave_all(pm, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
+  b.far = wave_all(pfar, MaxOp()) != 0;
+  const double top = wave_all(ptop, MaxOp());
+  if (!(b.m > -INFINITY && b.m < INFINITY) || b.far) return b;
+  lds_barrier();
+  const double even = 2.0 * floor(0.5 * top);
+  b.g.k = kMagic - even + static_cast<double>(kBase);
+  const int at = kBase + static_cast<int>(top - even);   // the maximum's bin
+  int shift[kMostParts];   // bins between the row's top and the part's
+#pragma unroll
+  for (int p = 0; p < kMostParts; ++p) shift[p] = top - L.ptop[p] < kReach ? static_cast<int>(top - L.ptop[p]) : kReach;
+  for (int j = tid; j < kReach; j += NT) {
+    ull s[kMostParts];
+    uint32_t n[kMostParts];
+#pragma unroll
+    for (int p = 0; p < kMostParts; ++p) {
+      const int q = max(0, j - shift[p]);
+      const BinPart& part = in[p < P ? p : 0];
+      s[p] = part.bin[q];
+      n[p] = count ? part.cnt[q] : 0u;
+    }
+    ull sum = 0;
+    uint32_t num = 0;
+#pragma unroll
+    for (int p = 0; p < kMostParts; ++p) {
+      sum += j >= shift[p] ? s[p] : 0ull;
+      num += j >= shift[p] ? n[p] : 0u;
+    }
+    L.bin[at - j] = sum;
+    if (count) L.u.cnt[at - j] = num;
+  }
+  lds_barrier();
+  return b;
+}
+
+// Row r by linear bins, by the whole workgroup; kJoin: from its parts' bins.
+template <typename E, int NT, int U, bool kJoin>
+__device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<NT>& L) {
+  constexpr int NW = NT / kWave;
+  constexpr int PER = kReach / NT;
+  static_assert(kReach % NT == 0 && kFew <= NT, "bins per thread");
+  const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
+  const int V = a.x.V;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  int bits = 0;
+  bool greedy;
+  const Draw d = load_draw(a, r, bits, greedy);
+  const bool count = d.top_k > 0 && d.top_k < V;
+  const double T = static_cast<double>(d.T);
+  const double one = weight_units(V);
+  const BinPart* parts = kJoin ? reinterpret_cast<const BinPart*>(a.part) + r * a.parts : nullptr;
+  Binned binned;
+  if constexpr (kJoin) binned = join_bins<NT>(parts, a.parts, T, count, L);
+  else binned = row_bins<E, NT, U>(row, V, T, one, count, L);
+  const Grid g = binned.g;
+  const float m = binned.m;
+  const bool far = binned.far;
+  if (!(m > -INFINITY && m < INFINITY)) {
+    if (tid == 0) {
+      a.token[r] = 0;
+      if (a.logprob) a.logprob[r] = 0.f;
+      if (a.lse) a.lse[r] = m;
+      if (a.error_flag) atomicOr(a.error_flag, bits | VSV_FLAG_LOGITS);
+    }
+    return;
   }
   const Weigh w{static_cast<double>(m), T, one};
   const double top_p = static_cast<double>(d.top_p), u = static_cast<double>(d.u);
@@ -538,6 +651,7 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     if (tid == 0) {
       L.n = 0;
       L.before = 0;
+      L.parts = 0;
     }
     lds_barrier();
     wb -= sum;
@@ -613,12 +727,29 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
         const int j = bin_of(x);
         return j >= first && j <= last && (L.mark[j >> 5] >> (j & 31) & 1u) != 0;
       };
+      int e0 = 0, e1 = V;
       auto put = [&](int at, int e) {
-        if (at < kList) L.u.list[at] = rank_key(Elem<E>::at(row, e), e);
+        if (at < kList) L.u.list[at] = rank_key(Elem<E>::at(row, e0 + e), e0 + e);
       };
       WantBetween<E, decltype(marked)> want{marked, low, high};
-      GatherVisit<E, NT, U, decltype(want), decltype(put)> v{want, put, &L.n, row_head(row, V)};
-      visit_row<E, NT, U, kLoadNormal>(row, V, v);
+      if constexpr (kJoin) {
+        // only the parts that hold something in those bins
+        for (int i = tid; i < a.parts * (last - first + 1); i += NT) {
+          const int p = i % a.parts, j = first + i / a.parts;
+          if (!(L.mark[j >> 5] >> (j & 31) & 1u)) continue;
+          const double q = static_cast<double>(j) - (static_cast<double>(top) - (g.k - kMagic) - L.ptop[p]);
+          if (q >= 0.0 && parts[p].bin[static_cast<int>(q)] != 0) atomicOr(&L.parts, 1u << p);
+        }
+        lds_barrier();
+      }
+      const uint32_t take = kJoin ? L.parts : 1u;
+#pragma unroll 1
+      for (int p = 0; p < (kJoin ? a.parts : 1); ++p) {
+        if (!(take >> p & 1u)) continue;
+        if (kJoin) row_part<E>(row, V, a.parts, p, e0, e1);
+        GatherVisit<E, NT, U, decltype(want), decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
+        visit_row<E, NT, U, kLoadNormal>(row + e0, e1 - e0, v);
+      }
     }
     lds_barrier();
     n = L.n;
@@ -1045,6 +1176,130 @@ __device__ __forceinline__ int cell_count(const CodeLds<NT>& L, int j) {
   return j < kCells ? static_cast<int>(L.tab[4096 + j - kCodes - 1]) : 0;
 }
 
+// What a part of a bfloat16 row leaves: its cells' counts (a part has fewer
+// than 2^16 elements), two to a word, and the rest of its table.
+constexpr int kCellWords = (kCells + 1) / 2;
+struct CodePart {
+  uint32_t cells[kCellWords];
+  uint32_t low;
+  ull tiny;
+  uint32_t bad, pad;
+};
+
+template <int NT>
+__device__ __forceinline__ void leave_codes(CodePart* out, const CodeLds<NT>& L) {
+  for (int i = threadIdx.x; i < kCellWords; i += NT)
+    out->cells[i] = static_cast<uint32_t>(cell_count(L, 2 * i)) | static_cast<uint32_t>(cell_count(L, 2 * i + 1)) << 16;
+  if (threadIdx.x == 0) {
+    out->low = L.low;
+    out->tiny = L.tiny;
+    out->bad = static_cast<uint32_t>(L.bad);
+  }
+}
+__device__ __forceinline__ int part_count(const CodePart& in, int j) { return static_cast<int>(in.cells[j >> 1] >> (j & 1) * 16 & 0xFFFFu); }
+
+template <typename E, int NT, int U>
+__global__ __launch_bounds__(NT, 4) void draw_part_kernel(DrawArgs a) {
+  const int64_t r = blockIdx.x / a.parts;
+  const int part = static_cast<int>(blockIdx.x - r * a.parts);
+  const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
+  int e0, e1;
+  row_part<E>(row, a.x.V, a.parts, part, e0, e1);
+  int bits = 0;
+  bool greedy;
+  const Draw d = load_draw(a, r, bits, greedy);
+  if constexpr (sizeof(E) == 2) {
+    __shared__ CodeLds<NT> L;
+    clear_codes(L);
+    CodeVisit<NT, U> f{L, 1.0 / static_cast<double>(d.T), weight_units(a.x.V)};
+    visit_row<E, NT, U, kLoadNormal>(row + e0, e1 - e0, f);
+    lds_barrier();
+    leave_codes(reinterpret_cast<CodePart*>(a.part) + blockIdx.x, L);
+  } else {
+    __shared__ DrawLds<NT> L;
+    const bool count = d.top_k > 0 && d.top_k < a.x.V;
+    const Binned b = row_bins<E, NT, U>(row + e0, e1 - e0, static_cast<double>(d.T), weight_units(a.x.V), count, L);
+    leave_bins<NT>(b, count, reinterpret_cast<BinPart*>(a.part) + blockIdx.x, L);
+  }
+}
+
+template <typename E, int NT, int U>
+__global__ __launch_bounds__(NT, 4) void draw_join_kernel(DrawArgs a) {
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x;
+  if constexpr (sizeof(E) == 2) {
+    __shared__ union {
+      DrawLds<NT> row;
+      CodeLds<NT> code;
+    } L;
+    constexpr int PER = cells_per<NT>();
+    int bits = 0;
+    bool greedy;
+    const Draw d = load_draw(a, r, bits, greedy);
+    const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
+    const CodePart* in = reinterpret_cast<const CodePart*>(a.part) + r * a.parts;
+    // the cells' sums in rank order, through LDS; every load of a step is
+    // issued before any is used (see join_bins)
+    if (tid == 0) {
+      L.code.bad = 0;
+      L.code.low = 0;
+      L.code.tiny = 0;
+    }
+    const CodePart& head = in[tid < a.parts ? tid : 0];
+    const uint32_t bad = head.bad, low = head.low;
+    const ull tiny = head.tiny;
+    lds_barrier();
+    if (tid < a.parts) {
+      atomicOr(&L.code.bad, static_cast<int>(bad));
+      atomicMax(&L.code.low, low);
+      atomicAdd(&L.code.tiny, tiny);
+    }
+#pragma unroll 2
+    for (int i = tid; i < kCellWords; i += NT) {
+      uint32_t c[kMostParts];
+#pragma unroll
+      for (int p = 0; p < kMostParts; ++p) c[p] = in[p < a.parts ? p : 0].cells[i];
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (int p = 0; p < kMostParts; ++p) {
+        lo += p < a.parts ? c[p] & 0xFFFFu : 0u;
+        hi += p < a.parts ? c[p] >> 16 : 0u;
+      }
+      L.code.tab[2 * i] = lo;
+      L.code.tab[2 * i + 1] = hi;
+    }
+    lds_barrier();
+    int cnt[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int j = tid * PER + k;
+      cnt[k] = j < kCells ? static_cast<int>(L.code.tab[j]) : 0;
+    }
+    const bool done = draw_codes<NT, PER>(a, r, d, greedy, bits, cnt, L.code, [&](uint32_t code, int q) {
+      // the part that holds the q-th, and there the rest of the way
+      const int j = (code & 0x8000u) ? kCodes + 1 + static_cast<int>(code - (0x8000u | kCodeLow))
+                                     : kCodes - 1 - static_cast<int>(code - kCodeLow);
+      const int lane = tid & (kWave - 1);
+      const int held = part_count(in[lane < a.parts ? lane : 0], j);
+      int p = 0;
+      for (; p < a.parts - 1; ++p) {
+        const int n = read_lane(held, p);
+        if (q <= n) break;
+        q -= n;
+      }
+      int e0, e1;
+      row_part<E>(row, a.x.V, a.parts, p, e0, e1);
+      return nth_code<NT, U>(row, e0, e1, code, q, L.code);
+    });
+    if (done) return;
+    lds_barrier();
+    draw_row<E, NT, U, false>(a, r, L.row);
+  } else {
+    __shared__ DrawLds<NT> L;
+    draw_row<E, NT, U, true>(a, r, L);
+  }
+}
+
 template <typename E, int NT, int U>
 __global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
   const int64_t r = blockIdx.x;
@@ -1070,20 +1325,40 @@ __global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
     });
     if (done) return;
     lds_barrier();
-    draw_row<E, NT, U>(a, r, L.row);
+    draw_row<E, NT, U, false>(a, r, L.row);
   } else {
     __shared__ DrawLds<NT> L;
-    draw_row<E, NT, U>(a, r, L);
+    draw_row<E, NT, U, false>(a, r, L);
   }
 }
 
 template <typename E>
 hipError_t draw_t(const DrawArgs& a, hipStream_t s) {
-  draw_kernel<E, kDrawThreads, kDrawUnroll><<<dim3(a.x.N), dim3(kDrawThreads), 0, s>>>(a);
+  if (a.parts > 1) {
+    draw_part_kernel<E, kDrawThreads, kDrawUnroll>
+        <<<dim3(static_cast<unsigned>(a.x.N * a.parts)), dim3(kDrawThreads), 0, s>>>(a);
+    draw_join_kernel<E, kDrawThreads, kDrawUnroll><<<dim3(a.x.N), dim3(kDrawThreads), 0, s>>>(a);
+  } else {
+    draw_kernel<E, kDrawThreads, kDrawUnroll><<<dim3(a.x.N), dim3(kDrawThreads), 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
+
+int32_t draw_parts(int32_t num_rows, int32_t vocab, int32_t dtype) {
+  const int64_t bytes = static_cast<int64_t>(vocab) * (dtype == VSV_BF16 ? 2 : 4);
+  if (bytes < 131072) return 1;
+  int64_t p = 512 / (num_rows > 0 ? num_rows : 1);
+  const int64_t most = bytes / 32768;
+  if (p > most) p = most;
+  if (p > kMostParts) p = kMostParts;
+  // a part's counts are 16 bits wide
+  if (p < 2 || vocab / p >= 65000) return 1;
+  return static_cast<int32_t>(p);
+}
+
+size_t draw_part_bytes(int32_t dtype) { return dtype == VSV_BF16 ? sizeof(CodePart) : sizeof(BinPart); }
 
 hipError_t launch_draw(const DrawArgs& a, hipStream_t s) {
   return a.x.dtype == VSV_BF16 ? draw_t<uint16_t>(a, s) : draw_t<float>(a, s);

@@ -72,7 +72,12 @@ struct DrawArgs {
   float* logprob;
   float* lse;
   int32_t* error_flag;
+  void* part;              // [N, parts] of draw_part_bytes when parts > 1
+  int32_t parts;
 };
+// Parts a row is cut into (by the call's sizes alone), and a part's scratch.
+int32_t draw_parts(int32_t num_rows, int32_t vocab, int32_t dtype);
+size_t draw_part_bytes(int32_t dtype);
 hipError_t launch_draw(const DrawArgs& a, hipStream_t s);
 
 }  // namespace vsv

@@ -265,17 +265,21 @@ vsv_status vsv_draft_confidence(const void* draft_logits, int32_t dtype,
  *   lse [num_rows]      log-sum-exp of x / T over the whole row (of x when
  *                       the temperature is 0), or NULL: x[t] / T - lse is the
  *                       log-probability without the filters
- * Needs no workspace; calls are independent of each other. VSV_FLAG_LOGITS:
- * a NaN or +inf logit or no finite one (token 0); VSV_FLAG_PARAMS: a
+ * `workspace` is scratch of vsv_sample_workspace_bytes bytes (0 for many rows
+ * or short ones; 16-byte aligned): it needs no initial value and nothing in
+ * it outlives the call, so calls are independent of each other.
+ * VSV_FLAG_LOGITS: a NaN or +inf logit or no finite one (token 0); VSV_FLAG_PARAMS: a
  * parameter or number outside its range (temperature counts as 0, a filter
  * as off, the number as 0).
  * Errors: VSV_EINVAL (num_rows < 0, NULL logits, parameters, uniform or
  * token, vocab outside 1 .. 2^30 - 1 or a row of 2 GiB, ld < vocab,
- * misaligned logits, unknown dtype), VSV_EHIP. */
+ * misaligned logits, unknown dtype), VSV_EWORKSPACE, VSV_EHIP. */
+size_t vsv_sample_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtype);
 vsv_status vsv_sample_rows(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows,
                            const float* temperature, const int32_t* top_k, const float* top_p,
                            const float* min_p, const float* uniform, int32_t* token, float* logprob,
-                           float* lse, int32_t* error_flag, hipStream_t stream);
+                           float* lse, int32_t* error_flag, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
 
 /* The first k logits of every row in the order (value desc, index asc), with
  * the row's log-sum-exp: what vsv_distill reads of a teacher, taken from the

@@ -20,11 +20,12 @@ def L():
 
 def _sample(L, **kw):
     a = dict(logits=0x10000, dtype=1, vocab=1024, ld=1024, rows=4, temperature=8, top_k=8, top_p=8, min_p=8, uniform=8,
-             token=8)
+             token=8, ws=0x1000, wsn=1 << 24)
     a.update(kw)
     p = {k: P(a[k]) if a[k] else None for k in ("logits", "temperature", "top_k", "top_p", "min_p", "uniform", "token")}
     return L.vsv_sample_rows(p["logits"], a["dtype"], a["vocab"], a["ld"], a["rows"], p["temperature"], p["top_k"],
-                             p["top_p"], p["min_p"], p["uniform"], p["token"], None, None, None, None)
+                             p["top_p"], p["min_p"], p["uniform"], p["token"], None, None, None, P(a["ws"]) if a["ws"] else None, a["wsn"],
+                             None)
 
 
 BAD_ROWS = [dict(logits=None), dict(logits=0x10001), dict(dtype=0, logits=0x10002), dict(dtype=2), dict(vocab=0),
@@ -36,6 +37,18 @@ BAD_ROWS = [dict(logits=None), dict(logits=0x10001), dict(dtype=0, logits=0x1000
                                             ("temperature", "top_k", "top_p", "min_p", "uniform", "token")])
 def test_sample_rows_refusals(L, bad):
     assert _sample(L, **bad) == 1
+
+
+def test_sample_scratch(L):
+    size = L.vsv_sample_workspace_bytes
+    assert size(0, 1024, 1) == 0 and size(4, 0, 1) == 0 and size(4, 152064, 9) == 0 and size(4, 1024, 0) == 0
+    for dtype in (0, 1):
+        need = size(4, 152064, dtype)
+        big = dict(dtype=dtype, vocab=152064, ld=152064)
+        assert 0 < need < 1 << 24
+        assert _sample(L, ws=0, **big) == 3
+        assert _sample(L, wsn=need - 1, **big) == 3
+        assert _sample(L, ws=0x1008, **big) == 3
 
 
 def test_no_rows_is_a_noop(L):
