@@ -86,7 +86,7 @@ SYMBOLS = ("vsv_workspace_bytes", "vsv_workspace_init", "vsv_verify_greedy", "vs
            "vsv_verify_greedy_static",
            "vsv_verify_sampled",
            "vsv_verify_probabilistic", "vsv_draft_confidence", "vsv_sample_workspace_bytes", "vsv_sample_rows",
-           "vsv_top_logits",
+           "vsv_top_workspace_bytes", "vsv_top_logits",
            "vsv_distill_workspace_bytes", "vsv_distill_forward", "vsv_distill_backward", "vsv_distill_grad",
            "vsv_allocate_verify", "vsv_goodput_init", "vsv_goodput_observe",
            "vsv_goodput_step", "vsv_goodput_select", "vsv_status_string", "vsv_test_withhold_row_word", "vsv_version")
@@ -139,7 +139,9 @@ def lib():
     L.vsv_sample_workspace_bytes.restype = sz
     L.vsv_sample_rows.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.vsv_sample_rows.restype = ctypes.c_int
-    L.vsv_top_logits.argtypes = [vp, i32, i32, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]
+    L.vsv_top_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.vsv_top_workspace_bytes.restype = sz
+    L.vsv_top_logits.argtypes = [vp, i32, i32, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]
     L.vsv_top_logits.restype = ctypes.c_int
     dp = ctypes.POINTER(Distill)
     L.vsv_distill_workspace_bytes.argtypes = [i32, i32, i32]
@@ -543,9 +545,11 @@ def top_logits(logits, k, temperature=1.0, vocab=None, stream=None):
                    ids=torch.empty((R, k), dtype=torch.int32, device=dev),
                    lse=torch.empty(R, dtype=torch.float32, device=dev),
                    error_flag=_new_flag(dev, s))
+        n = lib().vsv_top_workspace_bytes(R, V, dtype, k)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         on.keep(logits)
         _check(lib().vsv_top_logits(_at(logits), dtype, V, ld, R, k, float(temperature), _at(out["values"]),
-                                    _at(out["ids"]), _at(out["lse"]), _at(out["error_flag"]), s))
+                                    _at(out["ids"]), _at(out["lse"]), _at(out["error_flag"]), _at(ws), n, s))
     return out
 
 

@@ -254,17 +254,27 @@ vsv_status vsv_sample_rows(const void* logits, int32_t dtype, int32_t vocab, int
   return vsv::launch_draw(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 
+size_t vsv_top_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtype, int32_t k) {
+  if (num_rows < 1 || vocab < 1 || k < 1 || k > VSV_MAX_TOP || !dtype_ok(dtype)) return 0;
+  const size_t parts = static_cast<size_t>(vsv::top_parts(num_rows, vocab, dtype, k));
+  return parts < 2 ? 0 : static_cast<size_t>(num_rows) * parts * vsv::top_part_bytes(k);
+}
+
 vsv_status vsv_top_logits(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows, int32_t k,
                           float temperature, float* values, int32_t* ids, float* lse, int32_t* error_flag,
-                          hipStream_t stream) {
+                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (num_rows < 0) return VSV_EINVAL;
   if (num_rows == 0) return VSV_OK;
   if (!rows_ok(logits, dtype, vocab, ld, num_rows) || !values || !ids) return VSV_EINVAL;
   if (k < 1 || k > VSV_MAX_TOP || k > vocab) return VSV_EINVAL;
   if (!(temperature > 0.f) || !(temperature < INFINITY)) return VSV_EINVAL;
+  const int32_t parts = vsv::top_parts(num_rows, vocab, dtype, k);
+  if (parts > 1 && (!workspace || !aligned(workspace, 16) ||
+                    workspace_bytes < vsv_top_workspace_bytes(num_rows, vocab, dtype, k)))
+    return VSV_EWORKSPACE;
   const vsv::TopArgs a{{logits, ld, vocab, num_rows, dtype}, k,
                        static_cast<float>(1.44269504088896340736 / static_cast<double>(temperature)),
-                       values, ids, lse, error_flag};
+                       values, ids, lse, error_flag, workspace, parts};
   return vsv::launch_top(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 

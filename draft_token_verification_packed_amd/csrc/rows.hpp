@@ -58,7 +58,12 @@ struct TopArgs {
   int32_t* ids;            // [N, k]
   float* lse;              // [N] or NULL
   int32_t* error_flag;
+  void* part;              // [N, parts] of top_part_bytes when parts > 1
+  int32_t parts;
 };
+// Parts a row is cut into (by the call's sizes alone), and a part's scratch.
+int32_t top_parts(int32_t num_rows, int32_t vocab, int32_t dtype, int32_t k);
+size_t top_part_bytes(int32_t k);
 hipError_t launch_top(const TopArgs& a, hipStream_t s);
 
 struct DrawArgs {

@@ -43,6 +43,11 @@ __device__ __forceinline__ uint64_t rank_key(float x, int e) {
 
 constexpr int kTopKeys = 1024;    // of them, those that are ranked
 
+__device__ __forceinline__ void top_lse(const TopArgs& a, int64_t r, float mc, double total) {
+  if (a.lse) a.lse[r] = static_cast<float>(0.69314718055994530942 * (static_cast<double>(mc) + log2(total)));
+  if (!(total > 0.0 && total < INFINITY) && a.error_flag) atomicOr(a.error_flag, VSV_FLAG_LOGITS);
+}
+
 template <int NT> struct TopLds {
   static constexpr int NW = NT / kWave;
   uint32_t list[kTopList];
@@ -187,16 +192,34 @@ __device__ __forceinline__ uint64_t nth_key(const E* row, int V, int k, TopLds<N
   return prefix;
 }
 
-template <typename E, int NT, int U, int kWaves>
+// What a part of a row leaves in the scratch: its sum, and behind the heads
+// of all parts its first keys in rank order, k words of them (0: no element).
+struct TopPart {
+  double mc, sum;
+};
+
+// A workgroup per row, or (kPart) per part of a row.
+template <typename E, int NT, int U, int kWaves, bool kPart>
 __global__ __launch_bounds__(NT, kWaves) void top_kernel(TopArgs a) {
   __shared__ TopLds<NT> L;
   constexpr int NW = NT / kWave;
-  const int64_t r = blockIdx.x;
-  const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
-  const int V = a.x.V;
+  int64_t r = blockIdx.x;
+  int e0 = 0, V = a.x.V;
+  if (kPart) {
+    r = blockIdx.x / a.parts;
+    const E* whole = static_cast<const E*>(a.x.p) + r * a.x.ld;
+    const int part = static_cast<int>(blockIdx.x - r * a.parts);
+    const int head = row_head(whole, V);
+    const int64_t nv = (V - head) / Elem<E>::kVec;
+    const int e1 = part == a.parts - 1 ? V : head + static_cast<int>(nv * (part + 1) / a.parts) * Elem<E>::kVec;
+    e0 = part == 0 ? 0 : head + static_cast<int>(nv * part / a.parts) * Elem<E>::kVec;
+    V = e1 - e0;
+  }
+  const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld + e0;
+  const int k = kPart ? min(a.k, V) : a.k;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   if (tid == 0) L.n = L.m = 0;
-  TopVisit<E, NT, U> f{L, ExpSum{-FLT_MAX, 0.0}, a.c, -INFINITY, -INFINITY, a.k, row_head(row, V), 0};
+  TopVisit<E, NT, U> f{L, ExpSum{-FLT_MAX, 0.0}, a.c, -INFINITY, -INFINITY, k, row_head(row, V), 0};
   visit_row<E, NT, U, kLoadStream>(row, V, f, [&](const u32x4* w, int nvec) {
     float t = -INFINITY;
 #pragma unroll
@@ -234,9 +257,9 @@ __global__ __launch_bounds__(NT, kWaves) void top_kernel(TopArgs a) {
   }
   lds_barrier();
   int m = L.m;
-  if (m > kTopKeys || m < a.k) {
+  if (m > kTopKeys || m < k) {
     // too many ties at the bound (or NaN elements, which no bound keeps)
-    const uint64_t last = nth_key<E, NT>(row, V, a.k, L);
+    const uint64_t last = nth_key<E, NT>(row, V, k, L);
     if (tid == 0) L.m = 0;
     lds_barrier();
     each_elem<E, NT>(row, V, [&](float x, int e) {
@@ -249,38 +272,117 @@ __global__ __launch_bounds__(NT, kWaves) void top_kernel(TopArgs a) {
     lds_barrier();
     m = min(L.m, kTopKeys);
   }
+  uint64_t* keys = nullptr;
+  if (kPart) {
+    keys = reinterpret_cast<uint64_t*>(static_cast<TopPart*>(a.part) + static_cast<int64_t>(a.x.N) * a.parts) +
+           blockIdx.x * static_cast<int64_t>(a.k);
+    for (int i = tid; i < a.k; i += NT)
+      if (i >= k) keys[i] = 0;
+  }
   for (int i = tid; i < m; i += NT) {
     const uint64_t key = L.keys[i];
     int rank = 0;
 #pragma unroll 4
     for (int j = 0; j < m; ++j) rank += L.keys[j] > key ? 1 : 0;
-    if (rank < a.k) {
-      a.values[r * a.k + rank] = key_value(static_cast<uint32_t>(key >> 32));
-      a.ids[r * a.k + rank] = static_cast<int>(~static_cast<uint32_t>(key));
+    if (rank < k) {
+      if (kPart) {
+        keys[rank] = key - static_cast<uint32_t>(e0);   // ~(e + e0) = ~e - e0
+      } else {
+        a.values[r * a.k + rank] = key_value(static_cast<uint32_t>(key >> 32));
+        a.ids[r * a.k + rank] = static_cast<int>(~static_cast<uint32_t>(key));
+      }
     }
   }
   if (tid == 0) {
     double total = 0.0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) total += L.s[w];
-    const bool ok = total > 0.0 && total < INFINITY;
-    if (a.lse) a.lse[r] = static_cast<float>(0.69314718055994530942 * (static_cast<double>(mc) + log2(total)));
-    if (!ok && a.error_flag) atomicOr(a.error_flag, VSV_FLAG_LOGITS);
+    if (kPart) {
+      static_cast<TopPart*>(a.part)[blockIdx.x] = TopPart{static_cast<double>(mc), total};
+    } else {
+      top_lse(a, r, mc, total);
+    }
+  }
+}
+
+// A row's result from its parts': a key's rank is its place in its own part
+// and, by bisection, the number of larger keys in each of the others.
+constexpr int kMostTopParts = 8;
+constexpr int kJoinKeys = 1024;   // keys of all parts of a row
+__global__ __launch_bounds__(256) void top_join_kernel(TopArgs a) {
+  __shared__ uint64_t key[kJoinKeys];
+  const int64_t r = blockIdx.x;
+  const int n = a.parts * a.k;
+  const TopPart* head = static_cast<const TopPart*>(a.part) + r * a.parts;
+  const uint64_t* in = reinterpret_cast<const uint64_t*>(static_cast<const TopPart*>(a.part) +
+                                                         static_cast<int64_t>(a.x.N) * a.parts) + r * n;
+  const int lane = threadIdx.x & (kWave - 1);
+  const TopPart mine = lane < a.parts ? head[lane] : TopPart{-FLT_MAX, 0.0};
+  for (int i = threadIdx.x; i < n; i += 256) key[i] = in[i];
+  lds_barrier();
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const uint64_t x = key[i];
+    if (x == 0) continue;
+    const int own = i / a.k;
+    int rank = i - own * a.k;
+    for (int p = 0; p < a.parts; ++p) {
+      if (p == own) continue;
+      int lo = 0, hi = a.k;   // keys [0, lo) of part p are larger
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (key[p * a.k + mid] > x) lo = mid + 1;
+        else hi = mid;
+      }
+      rank += lo;
+    }
+    if (rank < a.k) {
+      a.values[r * a.k + rank] = key_value(static_cast<uint32_t>(x >> 32));
+      a.ids[r * a.k + rank] = static_cast<int>(~static_cast<uint32_t>(x));
+    }
+  }
+  if (threadIdx.x < kWave) {
+    const float mc = static_cast<float>(mine.mc);
+    const float all = wave_all(mc, MaxOp());
+    const double total = wave_sum_f64(sum_at(mine.sum, mc, all));
+    if (lane == 0) top_lse(a, r, all, total);
+  }
+}
+
+template <typename E, bool kPart>
+void top_rows(const TopArgs& a, hipStream_t s) {
+  constexpr bool kTwo = sizeof(E) == 2;
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.x.N) * (kPart ? a.parts : 1)));
+  if (a.k <= kFewTop) {
+    top_kernel<E, 256, 4, 4, kPart><<<grid, dim3(256), 0, s>>>(a);
+  } else {
+    top_kernel<E, 512, kTwo ? 2 : 4, kTwo ? 6 : 4, kPart><<<grid, dim3(512), 0, s>>>(a);
   }
 }
 
 template <typename E>
 hipError_t top_t(const TopArgs& a, hipStream_t s) {
-  constexpr bool kTwo = sizeof(E) == 2;
-  if (a.k <= kFewTop) {
-    top_kernel<E, 256, 4, 4><<<dim3(a.x.N), dim3(256), 0, s>>>(a);
+  if (a.parts > 1) {
+    top_rows<E, true>(a, s);
+    top_join_kernel<<<dim3(a.x.N), dim3(256), 0, s>>>(a);
   } else {
-    top_kernel<E, 512, kTwo ? 2 : 4, kTwo ? 6 : 4><<<dim3(a.x.N), dim3(512), 0, s>>>(a);
+    top_rows<E, false>(a, s);
   }
   return hipGetLastError();
 }
 
 }  // namespace
+
+int32_t top_parts(int32_t num_rows, int32_t vocab, int32_t dtype, int32_t k) {
+  const int64_t bytes = static_cast<int64_t>(vocab) * (dtype == VSV_BF16 ? 2 : 4);
+  if (bytes < 131072) return 1;
+  int64_t p = 512 / (num_rows > 0 ? num_rows : 1);
+  const int64_t most = bytes / 32768;
+  if (p > most) p = most;
+  if (p > kMostTopParts) p = kMostTopParts;
+  if (p * k > kJoinKeys) p = kJoinKeys / k;
+  return p < 2 ? 1 : static_cast<int32_t>(p);
+}
+size_t top_part_bytes(int32_t k) { return sizeof(TopPart) + sizeof(uint64_t) * static_cast<size_t>(k); }
 
 hipError_t launch_top(const TopArgs& a, hipStream_t s) {
   return a.x.dtype == VSV_BF16 ? top_t<uint16_t>(a, s) : top_t<float>(a, s);

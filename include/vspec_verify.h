@@ -289,14 +289,16 @@ vsv_status vsv_sample_rows(const void* logits, int32_t dtype, int32_t vocab, int
  *   lse [num_rows]        log-sum-exp of x / temperature, or NULL
  * -inf logits count as the last. A NaN or +inf logit, or a row whose largest
  * x / temperature is beyond float range, sets VSV_FLAG_LOGITS (ids stay
- * inside the row). Needs no workspace.
+ * inside the row). `workspace`: scratch of vsv_top_workspace_bytes bytes, as in
+ * vsv_sample_rows.
  * Errors: VSV_EINVAL (num_rows < 0, NULL logits, values or ids, k outside
  * 1 .. min(vocab, VSV_MAX_TOP), temperature not positive and finite, vocab,
- * ld, alignment and dtype as above), VSV_EHIP. */
+ * ld, alignment and dtype as above), VSV_EWORKSPACE, VSV_EHIP. */
 #define VSV_MAX_TOP 256
+size_t vsv_top_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtype, int32_t k);
 vsv_status vsv_top_logits(const void* logits, int32_t dtype, int32_t vocab, int64_t ld, int32_t num_rows,
                           int32_t k, float temperature, float* values, int32_t* ids, float* lse,
-                          int32_t* error_flag, hipStream_t stream);
+                          int32_t* error_flag, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Distillation of a draft head from the target's top logits. With y a
  * student row, q = softmax(y / T), and a row's used entries (ids[r, k] >= 0;

@@ -77,12 +77,25 @@ def test_draws(vsv, dtype, V, pad, shift):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_draws_over_a_full_vocabulary(vsv, dtype):
-    n, V = 24, 152064
-    rng, x, xs = _store(7, n, V, dtype, ("plain", "spikes", "masked", "ties", "equal"), 0, 0)
+@pytest.mark.parametrize("V,pad,shift", [(152064, 0, 0), (70001, 3, 1)])
+def test_draws_over_a_full_vocabulary(vsv, dtype, V, pad, shift):
+    # few long rows: each is cut into parts
+    n = 24
+    rng, x, xs = _store(7, n, V, dtype, ("plain", "spikes", "masked", "ties", "equal", "one_left", "lowest"), pad, shift)
     a = _params(rng, n, V)
     a[0][a[0] == 0] = 1.0
     _check_draws(vsv.sample_rows(x, *[to_dev(q) for q in a], vocab=V), xs, *a)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_draws_of_many_long_rows(vsv, dtype):
+    # enough rows that each is one workgroup's
+    import torch
+    m, n, V = 4, 520, 70001
+    rng, x, xs = _store(17, m, V, dtype, ("plain", "spikes", "ties", "masked"), 1, 0)
+    x = x[torch.arange(n, device="cuda") % m].contiguous()
+    a = _params(rng, n, V)
+    _check_draws(vsv.sample_rows(x, *[to_dev(q) for q in a], vocab=V), [xs[r % m] for r in range(n)], *a)
 
 
 def test_every_token_of_a_law_is_reached(vsv):
@@ -172,14 +185,15 @@ def test_top_logits(vsv, dtype, V, k, pad, shift, T):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("order", ["rising", "falling", "blocks", "stride"])
-def test_top_logits_of_ordered_rows(vsv, dtype, order):
-    # the largest elements late, early, together, or all in the same lanes
-    V, k = 30000, 200
+@pytest.mark.parametrize("V,k", [(30000, 200), (30000, 40), (90001, 130)])
+def test_top_logits_of_ordered_rows(vsv, dtype, order, V, k):
+    # the largest elements late, early, together, or all in the same lanes;
+    # rows taken whole and in parts
     x = np.sort(np.random.default_rng(8).standard_normal(V).astype(np.float32) * 3)
     if order == "falling":
         x = x[::-1].copy()
     elif order == "blocks":
-        x = np.concatenate((x[10000:20000], x[20000:], x[:10000]))
+        x = np.concatenate((x[V // 3:V // 2], x[V // 2:], x[:V // 3]))
     elif order == "stride":
         x = x.copy()
         big = np.sort(np.random.default_rng(9).random(2000).astype(np.float32)) + 20

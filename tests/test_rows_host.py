@@ -51,6 +51,18 @@ def test_sample_scratch(L):
         assert _sample(L, ws=0x1008, **big) == 3
 
 
+def test_top_scratch(L):
+    size = L.vsv_top_workspace_bytes
+    assert size(0, 152064, 1, 8) == 0 and size(4, 0, 1, 8) == 0 and size(4, 152064, 9, 8) == 0
+    assert size(4, 152064, 1, 0) == 0 and size(4, 152064, 1, 257) == 0 and size(4, 1024, 0, 8) == 0
+    need = size(4, 152064, 1, 100)
+    big = dict(vocab=152064, ld=152064, k=100)
+    assert 0 < need < 1 << 24
+    assert _top(L, ws=0, **big) == 3
+    assert _top(L, wsn=need - 1, **big) == 3
+    assert _top(L, ws=0x1008, **big) == 3
+
+
 def test_no_rows_is_a_noop(L):
     assert _sample(L, rows=0, logits=None) == 0
     assert _top(L, rows=0, logits=None) == 0
@@ -59,11 +71,11 @@ def test_no_rows_is_a_noop(L):
 
 
 def _top(L, **kw):
-    a = dict(logits=0x10000, dtype=1, vocab=1024, ld=1024, rows=4, k=8, T=1.0, values=8, ids=8)
+    a = dict(logits=0x10000, dtype=1, vocab=1024, ld=1024, rows=4, k=8, T=1.0, values=8, ids=8, ws=0x1000, wsn=1 << 24)
     a.update(kw)
     return L.vsv_top_logits(P(a["logits"]) if a["logits"] else None, a["dtype"], a["vocab"], a["ld"], a["rows"], a["k"],
                             a["T"], P(a["values"]) if a["values"] else None, P(a["ids"]) if a["ids"] else None, None,
-                            None, None)
+                            None, P(a["ws"]) if a["ws"] else None, a["wsn"], None)
 
 
 @pytest.mark.parametrize("bad", BAD_ROWS + [
