@@ -37,11 +37,12 @@ constexpr int kDrawUnroll = 2;
 constexpr int kBins = 4096;
 constexpr int kReach = 1536;       // bins below the maximum that count (48 T)
 constexpr int kBase = kReach + 2;  // about where the first group's maximum lies
-constexpr double kPerT = 32.0;     // bins per T
+constexpr double kPerT = 32.0;     // bins per T, at least
+constexpr double kMostPerT = 1024.0;
 constexpr int kList = 4096;        // elements the gathered list holds
 constexpr int kMostParts = 8;
 constexpr int kFew = 128;          // lists decided by direct comparison
-// Beyond this |32 x / T| bins are too coarse in float64 to trust.
+// Beyond this |x| per / T bins are too coarse in float64 to trust.
 constexpr double kFarBin = 4194304.0;
 
 // Sums hold to about 1e-13 of the row's weight (a weight's integer is off by
@@ -101,7 +102,7 @@ template <int NT> struct DrawLds {
 constexpr double kMagic = 6755399441055744.0;         // 1.5 * 2^52
 constexpr uint32_t kMagicHi = 0x43380000u;
 struct Grid {
-  double s, k;
+  double s, k, per;   // s = per / T: bins per T
   __device__ __forceinline__ double t(float x) const { return fma(static_cast<double>(x), s, k); }
   // bin number, or -1 where the element lies outside the bins
   static __device__ __forceinline__ int slot(double t) {
@@ -118,13 +119,15 @@ struct BinVisit {
   uint32_t* cnt;
   double c[6];   // the polynomial's coefficients, in weight units
   float top;     // IEEE maximum: a NaN stays
+  float cut;     // an element outside the bins, but above this, is missed
+  int* missed;
 
   __device__ __forceinline__ void put(float x) {
     const double t = g.t(x);
     const uint64_t b = __builtin_bit_cast(uint64_t, t);
     const uint32_t lo = static_cast<uint32_t>(b);
     if (static_cast<uint32_t>(b >> 32) == kMagicHi && lo < static_cast<uint32_t>(kBins)) {
-      // r in [-1/2, 1/2]; exp(r / 32) in weight units, the integer in the low
+      // r in [-1/2, 1/2]; exp(r / per) in weight units, the integer in the low
       // bits of a double between 2^52 and 2^53
       const double r = fma(static_cast<double>(x), g.s, -(t - g.k));
       double h = fma(r, c[5], c[4]);
@@ -134,6 +137,8 @@ struct BinVisit {
       h = fma(r, h, c[0]);
       atomicAdd(&bin[lo], __builtin_bit_cast(uint64_t, h) - 0x4330000000000000ull);
       if (kCount) atomicAdd(&cnt[lo], 1u);
+    } else if (x > cut) {
+      *missed = 1;
     }
   }
   template <bool kPartial>
@@ -403,52 +408,91 @@ struct Binned {
 };
 
 // Elements [0, V) at `row` into L.bin (and L.u.cnt), by the whole workgroup.
+// The grid goes by the first group of `sample` (the row, of `sampled`
+// elements, that the range belongs to): its maximum, and how far its other
+// elements lie below. The flatter the row, the more bins per T, so that a bin
+// of a bulk of near equals still holds few; a row the grid then misses
+// something of goes again on the widest grid.
 template <typename E, int NT, int U>
-__device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, double T, double one, bool count,
-                                           DrawLds<NT>& L) {
+__device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, const E* __restrict__ sample, int sampled,
+                                           double T, double one, bool count, DrawLds<NT>& L) {
   constexpr int NW = NT / kWave;
+  constexpr int N = Elem<E>::kVec;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  Grid g{kPerT / T, 0.0};
+  Grid g{kPerT / T, 0.0, kPerT};
   float m = -INFINITY;
-  bool far = false;
-  auto bins = [&](auto& f, bool known) {
-    f.g = g;
+  bool far = false, missed = false, known = false;
+  double per = kPerT;
+  auto bins = [&](auto& f) {
     f.bin = L.bin;
     f.cnt = L.u.cnt;
     f.top = -INFINITY;
-    f.c[0] = one;
-#pragma unroll
-    for (int k = 1; k < 6; ++k) f.c[k] = f.c[k - 1] * (1.0 / (kPerT * k));
-    f.c[0] += 4503599627370496.0;
+    f.missed = &L.n;
     for (int b = tid; b < kBins; b += NT) L.bin[b] = 0;
     if (count)
       for (int b = tid; b < kBins; b += NT) L.u.cnt[b] = 0;
-    auto place = [&](float ref) {
+    if (tid == 0) L.n = 0;
+    visit_row<E, NT, U, kLoadNormal>(row, V, f, [&](const u32x4* w, int nvec) {
+      float ref = m;
+      if (!known) {
+        // the sample's vectors, and its elements before and after its body
+        const int head = row_head(sample, sampled);
+        const int sv = (sampled - head) / N, tail = sampled - head - sv * N;
+        u32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = tid + u * NT;
+          if (V != sampled && i < sv) v[u] = reinterpret_cast<const u32x4*>(sample + head)[i];
+          else v[u] = w[u];
+        }
+        float hx = tid < head ? Elem<E>::at(sample, tid) : -INFINITY;
+        float tx = tid < tail ? Elem<E>::at(sample, sampled - 1 - tid) : -INFINITY;
+        float t = fmaxf(hx, tx);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[N];
+          if (tid + u * NT < sv) t = fmaxf(t, vec_max<E>(v[u], x));
+        }
+        t = wave_all(t, MaxOp());
+        if (lane == 0) L.red_f[wave] = t;
+        lds_barrier();
+        ref = L.red_f[0];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) ref = fmaxf(ref, L.red_f[k]);
+        const float cut = static_cast<float>(static_cast<double>(ref) - 48.0 * T);
+        auto lower = [&](float lo, float x) { return x > cut ? fminf(lo, x) : lo; };
+        float lo = lower(lower(ref, hx), tx);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[N];
+          Elem<E>::decode(v[u], x);
+          if (tid + u * NT < sv) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) lo = lower(lo, x[k]);
+          }
+        }
+        lo = wave_all(lo, MinOp());
+        if (lane == 0) L.red_d[wave] = static_cast<double>(lo);
+        lds_barrier();
+        double least = L.red_d[0];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) least = fmin(least, L.red_d[k]);
+        // half as much again as the sample spans, and 12 T of rise above it,
+        // in kReach bins
+        const double span = (static_cast<double>(ref) - least) / T * 1.5 + 12.0;
+        while (per < kMostPerT && 2.0 * per * span <= kReach - 100) per *= 2.0;
+      } else {
+        lds_barrier();
+      }
+      f.cut = per > kPerT ? static_cast<float>(static_cast<double>(ref) - 48.0 * T) : INFINITY;
+      f.g = Grid{per / T, 0.0, per};
       const double y = static_cast<double>(ref) * f.g.s;
       far = !(fabs(y) < kFarBin);
       f.g.k = kMagic - (far ? 0.0 : 2.0 * rint(0.5 * y)) + static_cast<double>(kBase);
-    };
-    visit_row<E, NT, U, kLoadNormal>(row, V, f, [&](const u32x4* w, int nvec) {
-      float t = m;
-      if (!known) {
+      f.c[0] = one;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float x[Elem<E>::kVec];
-          if (tid + u * NT < nvec) t = fmaxf(t, vec_max<E>(w[u], x));
-        }
-        const int head = row_head(row, V);
-        if (tid < head) t = fmaxf(t, Elem<E>::at(row, tid));
-        if (tid < V - head - nvec * Elem<E>::kVec) t = fmaxf(t, Elem<E>::at(row, V - 1 - tid));
-        t = wave_all(t, MaxOp());
-        if (lane == 0) L.red_f[wave] = t;
-      }
-      lds_barrier();
-      if (!known) {
-        t = L.red_f[0];
-#pragma unroll
-        for (int k = 1; k < NW; ++k) t = fmaxf(t, L.red_f[k]);
-      }
-      place(t);
+      for (int k = 1; k < 6; ++k) f.c[k] = f.c[k - 1] * (1.0 / (per * k));
+      f.c[0] += 4503599627370496.0;
     });
     g = f.g;
     const float t = wave_all(f.top, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
@@ -458,30 +502,48 @@ __device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, dou
     m = L.red_f[0];
 #pragma unroll
     for (int k = 1; k < NW; ++k) m = __builtin_elementwise_maximum(m, L.red_f[k]);
-  };
-  auto pass = [&](bool known) {
-    if (count) {
-      BinVisit<E, NT, U, true> f;
-      bins(f, known);
-    } else {
-      BinVisit<E, NT, U, false> f;
-      bins(f, known);
+    // bins further below the maximum than will be looked at have to be empty,
+    // unless the grid is the widest, where they weigh nothing
+    missed = L.n != 0;
+    if (per > kPerT && m > -INFINITY && m < INFINITY && !far) {
+      const int top = Grid::slot(g.t(m));
+      int held = 0;
+      for (int b = tid; b <= top - kReach; b += NT) held |= L.bin[b] != 0;
+      held = wave_all(held, MaxOp());
+      if (lane == 0 && held) atomicOr(&L.n, 1);
+      lds_barrier();
+      missed = L.n != 0;
     }
   };
-  // again where the first group held nothing to go by, or the row rises far
-  // beyond it
-  for (bool known = false;; known = true) {
-    pass(known);
-    if (!(m > -INFINITY && m < INFINITY) || known || !(far || Grid::slot(g.t(m)) < 0)) break;
+  for (;;) {
+    if (count) {
+      BinVisit<E, NT, U, true> f;
+      bins(f);
+    } else {
+      BinVisit<E, NT, U, false> f;
+      bins(f);
+    }
+    if (!(m > -INFINITY && m < INFINITY)) break;
+    const bool above = !far && g.t(m) >= kMagic + static_cast<double>(kBins);
+    if (known && far) break;
+    if (!known && above) {
+      // from the true maximum
+    } else if ((!known && far) || (missed && per > kPerT)) {
+      per = kPerT;
+    } else {
+      break;
+    }
+    known = true;
     lds_barrier();
   }
+  lds_barrier();
   return Binned{g, m, far};
 }
 
 // A row cut into parts, one workgroup each: what a part leaves in the scratch.
 struct BinPart {
   double m, top, far;       // maximum, its bin's absolute number, 1 if too far out
-  double pad;
+  double per;               // bins per T
   ull bin[kReach];          // downwards from the part's own top bin
   uint32_t cnt[kReach];
 };
@@ -498,16 +560,18 @@ __device__ __forceinline__ void row_part(const E* row, int V, int P, int part, i
 template <int NT>
 __device__ __forceinline__ void leave_bins(const Binned& b, bool count, BinPart* out, const DrawLds<NT>& L) {
   const bool fine = b.m > -INFINITY && b.m < INFINITY;
-  const int top = fine && !b.far ? Grid::slot(b.g.t(b.m)) : 0;
+  // (a part may lie wholly below the row's bins)
+  const int top = fine && !b.far ? Grid::slot(b.g.t(b.m)) : -1;
   if (threadIdx.x == 0) {
     out->m = static_cast<double>(b.m);
-    out->top = static_cast<double>(top) - (b.g.k - kMagic);
+    out->top = top < 0 ? -INFINITY : static_cast<double>(top) - (b.g.k - kMagic);
     out->far = fine && b.far ? 1.0 : 0.0;
+    out->per = b.g.per;
   }
-  if (fine && !b.far) {
+  if (top >= 0) {
     for (int j = threadIdx.x; j < kReach; j += NT) {
-      out->bin[j] = L.bin[top - j];
-      if (count) out->cnt[j] = L.u.cnt[top - j];
+      out->bin[j] = j <= top ? L.bin[top - j] : 0ull;
+      if (count) out->cnt[j] = j <= top ? L.u.cnt[top - j] : 0u;
     }
   }
 }
@@ -519,7 +583,7 @@ __device__ __forceinline__ void leave_bins(const Binned& b, bool count, BinPart*
 template <int NT>
 __device__ __forceinline__ Binned join_bins(const BinPart* in, int P, double T, bool count, DrawLds<NT>& L) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  Binned b{Grid{kPerT / T, 0.0}, -INFINITY, false};
+  Binned b{Grid{kPerT / T, 0.0, kPerT}, -INFINITY, false};
   const BinPart& mine = in[lane < P ? lane : 0];
   const float pm = static_cast<float>(mine.m);
   const bool fine = pm > -INFINITY;
@@ -527,8 +591,14 @@ __device__ __forceinline__ Binned join_bins(const BinPart* in, int P, double T, 
   const int pfar = fine && mine.far != 0.0 ? 1 : 0;
   if (tid < kMostParts) L.ptop[tid] = tid < P ? ptop : -INFINITY;
   b.m = wave_all(pm, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
-  b.far = wave_all(pfar, MaxOp()) != 0;
+  // parts that went by different grids cannot be added
+  const double pper = ptop > -INFINITY ? mine.per : 0.0;
+  const double per = wave_all(pper, MaxOp());
+  b.far = wave_all(pfar | (ptop > -INFINITY && pper != per ? 1 : 0), MaxOp()) != 0;
+  b.g.per = per;
+  b.g.s = per / T;
   const double top = wave_all(ptop, MaxOp());
+  b.far = b.far || !(top > -INFINITY);
   if (!(b.m > -INFINITY && b.m < INFINITY) || b.far) return b;
   lds_barrier();
   const double even = 2.0 * floor(0.5 * top);
@@ -577,9 +647,18 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
   const double T = static_cast<double>(d.T);
   const double one = weight_units(V);
   const BinPart* parts = kJoin ? reinterpret_cast<const BinPart*>(a.part) + r * a.parts : nullptr;
-  Binned binned;
-  if constexpr (kJoin) binned = join_bins<NT>(parts, a.parts, T, count, L);
-  else binned = row_bins<E, NT, U>(row, V, T, one, count, L);
+  int P = 1;   // parts the gathering goes by
+  Binned binned{Grid{0.0, 0.0, 0.0}, -INFINITY, true};
+  if constexpr (kJoin) {
+    binned = join_bins<NT>(parts, a.parts, T, count, L);
+    P = a.parts;
+  }
+  if (!kJoin || binned.far) {
+    // (parts that went by different grids: the row again, as one)
+    lds_barrier();
+    binned = row_bins<E, NT, U>(row, V, row, V, T, one, count, L);
+    P = 1;
+  }
   const Grid g = binned.g;
   const float m = binned.m;
   const bool far = binned.far;
@@ -626,6 +705,44 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
   auto at_least = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] >= t; }); };
   auto more_than = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] > t; }); };
 
+  // the elements of the marked bins, all of them between first and last, into
+  // the list
+  auto collect = [&](int first, int last) {
+    // a little outside the outermost bins' borders; bin_of decides
+    const double at = static_cast<double>(top) - (g.k - kMagic);
+    const double to = (at - first + 0.5) / g.s, from = (at - last - 0.5) / g.s;
+    const float high = static_cast<float>(to + fabs(to) * (1.0 / 1048576.0) + 1e-30);
+    const float low = static_cast<float>(from - fabs(from) * (1.0 / 1048576.0) - 1e-30);
+    auto marked = [&](float x) {
+      const int j = bin_of(x);
+      return j >= first && j <= last && (L.mark[j >> 5] >> (j & 31) & 1u) != 0;
+    };
+    int e0 = 0, e1 = V;
+    auto put = [&](int at, int e) {
+      if (at < kList) L.u.list[at] = rank_key(Elem<E>::at(row, e0 + e), e0 + e);
+    };
+    WantBetween<E, decltype(marked)> want{marked, low, high};
+    if (kJoin && P > 1) {
+      // only the parts that hold something in those bins
+      for (int i = tid; i < P * (last - first + 1); i += NT) {
+        const int p = i % P, j = first + i / P;
+        if (!(L.mark[j >> 5] >> (j & 31) & 1u)) continue;
+        const double q = static_cast<double>(j) - (static_cast<double>(top) - (g.k - kMagic) - L.ptop[p]);
+        if (q >= 0.0 && parts[p].bin[static_cast<int>(q)] != 0) atomicOr(&L.parts, 1u << p);
+      }
+      lds_barrier();
+    }
+    const uint32_t take = P > 1 ? L.parts : 1u;
+#pragma unroll 1
+    for (int p = 0; p < P; ++p) {
+      if (!(take >> p & 1u)) continue;
+      if (P > 1) row_part<E>(row, V, P, p, e0, e1);
+      GatherVisit<E, NT, U, decltype(want), decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
+      visit_row<E, NT, U, kLoadNormal>(row + e0, e1 - e0, v);
+    }
+  };
+
+  bool two = false;   // the cuts' bins first, the draw's after them
   if (!far) {
     // ---- cumulative weights, downwards from the maximum's bin
     top = Grid::slot(g.t(m));
@@ -635,7 +752,7 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int b = top - (tid * PER + k);
-      sum += static_cast<double>(L.bin[b]) / one * exp((static_cast<double>(b) - mpos) / kPerT);
+      sum += static_cast<double>(L.bin[b]) / one * exp((static_cast<double>(b) - mpos) / g.per);
       through[k] = sum;
       num += count ? static_cast<int>(L.u.cnt[b]) : 0;
       seen[k] = num;
@@ -699,7 +816,7 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
       hi = fmin(hi, upto(p1));
     }
     if (d.min_p > 0.f) {
-      const double jz = static_cast<double>(top) - rint(mpos + kPerT * zmin);
+      const double jz = static_cast<double>(top) - rint(mpos + g.per * zmin);
       if (jz < static_cast<double>(kReach)) {
         jm = jz > 0.0 ? static_cast<int>(jz) : 0;
         lo = fmin(lo, upto(jm - 1));
@@ -710,51 +827,39 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     more_than(4, exceed(u * hi));
     lds_barrier();
     const int d0 = L.j[3], d1 = L.j[4];
-    const int last = max(max(jk, jm), max(p1, d1));
-    const int first = min(min(jk < 0 ? d0 : jk, jm < 0 ? d0 : jm), min(p0, d0));
+    int last = max(max(jk, jm), max(p1, d1));
+    int first = min(min(jk < 0 ? d0 : jk, jm < 0 ? d0 : jm), min(p0, d0));
+    auto is_cut = [&](int j) { return j == jk || j == jm || (j >= p0 && j <= p1); };
+    auto is_draw = [&](int j) { return j >= d0 && j <= d1; };
+    // how many elements they hold, from their weights
+    double held = 0.0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int j = tid * PER + k;
+      if (is_cut(j) || is_draw(j))
+        held += (through[k] - (k ? through[k > 0 ? k - 1 : 0] : wb)) * exp((mpos - static_cast<double>(top - j)) / g.per);
+    }
+    held = wave_all(held, SumOp());
+    if (lane == 0) L.red_d[wave] = held;
+    lds_barrier();
+    held = 0.0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) held += L.red_d[k];
+    two = held > static_cast<double>(kList - kList / 16);
+    if (two) {
+      last = max(max(jk, jm), p1);
+      first = min(min(jk < 0 ? kReach : jk, jm < 0 ? kReach : jm), p0);
+    }
     for (int j = tid; j <= last; j += NT)
-      if (j == jk || j == jm || (j >= p0 && j <= p1) || (j >= d0 && j <= d1)) atomicOr(&L.mark[j >> 5], 1u << (j & 31));
+      if (is_cut(j) || (!two && is_draw(j))) atomicOr(&L.mark[j >> 5], 1u << (j & 31));
     lds_barrier();
 
     // ---- the elements of those bins
-    {
-      // a little outside the outermost bins' borders; bin_of decides
-      const double at = static_cast<double>(top) - (g.k - kMagic);
-      const double to = (at - first + 0.5) / g.s, from = (at - last - 0.5) / g.s;
-      const float high = static_cast<float>(to + fabs(to) * (1.0 / 1048576.0) + 1e-30);
-      const float low = static_cast<float>(from - fabs(from) * (1.0 / 1048576.0) - 1e-30);
-      auto marked = [&](float x) {
-        const int j = bin_of(x);
-        return j >= first && j <= last && (L.mark[j >> 5] >> (j & 31) & 1u) != 0;
-      };
-      int e0 = 0, e1 = V;
-      auto put = [&](int at, int e) {
-        if (at < kList) L.u.list[at] = rank_key(Elem<E>::at(row, e0 + e), e0 + e);
-      };
-      WantBetween<E, decltype(marked)> want{marked, low, high};
-      if constexpr (kJoin) {
-        // only the parts that hold something in those bins
-        for (int i = tid; i < a.parts * (last - first + 1); i += NT) {
-          const int p = i % a.parts, j = first + i / a.parts;
-          if (!(L.mark[j >> 5] >> (j & 31) & 1u)) continue;
-          const double q = static_cast<double>(j) - (static_cast<double>(top) - (g.k - kMagic) - L.ptop[p]);
-          if (q >= 0.0 && parts[p].bin[static_cast<int>(q)] != 0) atomicOr(&L.parts, 1u << p);
-        }
-        lds_barrier();
-      }
-      const uint32_t take = kJoin ? L.parts : 1u;
-#pragma unroll 1
-      for (int p = 0; p < (kJoin ? a.parts : 1); ++p) {
-        if (!(take >> p & 1u)) continue;
-        if (kJoin) row_part<E>(row, V, a.parts, p, e0, e1);
-        GatherVisit<E, NT, U, decltype(want), decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
-        visit_row<E, NT, U, kLoadNormal>(row + e0, e1 - e0, v);
-      }
-    }
+    if (!two || first <= last) collect(first, last);
     lds_barrier();
     n = L.n;
     left = total;
-    if (n <= kFew) {
+    if (n <= kFew && !two) {
       // ---- few: each element's cumulative weight from the others of its bin
       uint64_t mine = 0;
       int j = -1;
@@ -804,7 +909,7 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     // ---- more: each cut by a radix search, over its own bin's elements or,
     // where the bins hold too many or cannot place them (or rounding hides a
     // border from the list), over the row
-    bool list = !far && n > kFew && n <= kList;
+    bool list = !far && (n > kFew || two) && n <= kList;
     int j = -1;
     auto each = [&](auto&& f) {
       if (list) {
@@ -843,6 +948,21 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
             else more_than(6, t);
             lds_barrier();
             j = L.j[4 + c];
+          }
+          if (c == 2 && two) {
+            if (tid < kReach / 32) L.mark[tid] = tid == j >> 5 ? 1u << (j & 31) : 0u;
+            if (tid == 0) {
+              L.n = 0;
+              L.parts = 0;
+            }
+            lds_barrier();
+            collect(j, j);
+            lds_barrier();
+            n = L.n;
+            if (n > kList) {
+              key = 0;
+              break;
+            }
           }
         }
         double to;
@@ -1218,7 +1338,7 @@ __global__ __launch_bounds__(NT, 4) void draw_part_kernel(DrawArgs a) {
   } else {
     __shared__ DrawLds<NT> L;
     const bool count = d.top_k > 0 && d.top_k < a.x.V;
-    const Binned b = row_bins<E, NT, U>(row + e0, e1 - e0, static_cast<double>(d.T), weight_units(a.x.V), count, L);
+    const Binned b = row_bins<E, NT, U>(row + e0, e1 - e0, row, a.x.V, static_cast<double>(d.T), weight_units(a.x.V), count, L);
     leave_bins<NT>(b, count, reinterpret_cast<BinPart*>(a.part) + blockIdx.x, L);
   }
 }
