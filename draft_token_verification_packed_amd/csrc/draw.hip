@@ -80,7 +80,6 @@ template <int NT> struct DrawLds {
   uint32_t num[256];
   double w[kFew];
   int at[kFew];
-  uint32_t mark[kReach / 32];  // bins to gather
   ull red_u[NW];
   double red_d[NW];
   float red_f[NW];
@@ -198,23 +197,50 @@ struct GatherVisit {
   }
 };
 
-// Elements between two bounds whose bin is marked (bin(x): whether it is).
-template <typename E, typename Bin> struct WantBetween {
-  Bin& bin;
-  float low, high;
-  __device__ __forceinline__ bool in(float x) const { return __builtin_amdgcn_fmed3f(x, low, high) == x; }
-  __device__ __forceinline__ bool one(float x) const { return in(x) && bin(x); }
+// Up to four ranges of bins, as positions downwards from the maximum's.
+struct Ranges {
+  int n = 0, a[4], b[4];
+  __device__ __forceinline__ void add(int x, int y) {
+    bool known = x > y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) known = known || (i < n && x >= a[i] && y <= b[i]);
+    if (known) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i == n) {
+        a[i] = x;
+        b[i] = y;
+      }
+    }
+    ++n;
+  }
+};
+
+// Elements within any of up to four closed intervals.
+template <typename E> struct WantBetween {
+  int n;
+  float least;            // the lowest of the bounds
+  float low[4], high[4];
+  __device__ __forceinline__ bool one(float x) const {
+    bool r = __builtin_amdgcn_fmed3f(x, low[0], high[0]) == x;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (i < n) r = r || __builtin_amdgcn_fmed3f(x, low[i], high[i]) == x;
+    return r;
+  }
   __device__ __forceinline__ uint32_t operator()(const u32x4& w) const {
     constexpr int N = Elem<E>::kVec;
     float x[N];
-    Elem<E>::decode(w, x);
     uint32_t m = 0;
+    // most vectors lie wholly below where the cuts are
+    if (vec_max<E, true>(w, x) < least) return m;
 #pragma unroll
-    for (int k = 0; k < N; ++k) m |= in(x[k]) ? 1u << k : 0u;
-    if (m) {
+    for (int k = 0; k < N; ++k) m |= __builtin_amdgcn_fmed3f(x[k], low[0], high[0]) == x[k] ? 1u << k : 0u;
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (m >> k & 1) m &= bin(x[k]) ? ~0u : ~(1u << k);
+    for (int i = 1; i < 4; ++i) {
+      if (i >= n) break;
+#pragma unroll
+      for (int k = 0; k < N; ++k) m |= __builtin_amdgcn_fmed3f(x[k], low[i], high[i]) == x[k] ? 1u << k : 0u;
     }
     return m;
   }
@@ -705,30 +731,43 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
   auto at_least = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] >= t; }); };
   auto more_than = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] > t; }); };
 
-  // the elements of the marked bins, all of them between first and last, into
-  // the list
-  auto collect = [&](int first, int last) {
-    // a little outside the outermost bins' borders; bin_of decides
-    const double at = static_cast<double>(top) - (g.k - kMagic);
-    const double to = (at - first + 0.5) / g.s, from = (at - last - 0.5) / g.s;
-    const float high = static_cast<float>(to + fabs(to) * (1.0 / 1048576.0) + 1e-30);
-    const float low = static_cast<float>(from - fabs(from) * (1.0 / 1048576.0) - 1e-30);
-    auto marked = [&](float x) {
-      const int j = bin_of(x);
-      return j >= first && j <= last && (L.mark[j >> 5] >> (j & 31) & 1u) != 0;
-    };
+  // the least float whose bin is at least b
+  auto least_in = [&](int b) {
+    auto in = [&](float x) { return g.t(x) >= kMagic + static_cast<double>(b); };
+    float x = static_cast<float>((static_cast<double>(b) - 0.5 - (g.k - kMagic)) / g.s);
+    while (in(x)) x = key_value(up_key(x) - 1u);
+    while (!in(x)) x = key_value(up_key(x) + 1u);
+    return x;
+  };
+  // the elements of the ranges' bins into the list
+  auto collect = [&](const Ranges& rs) {
+    WantBetween<E> want;
+    want.n = rs.n;
+    want.least = INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      want.low[i] = INFINITY;
+      want.high[i] = -INFINITY;
+      if (i < rs.n) {
+        want.low[i] = least_in(top - rs.b[i]);
+        want.least = fminf(want.least, want.low[i]);
+        want.high[i] = rs.a[i] > 0 ? key_value(up_key(least_in(top - rs.a[i] + 1)) - 1u) : m;
+      }
+    }
     int e0 = 0, e1 = V;
     auto put = [&](int at, int e) {
-      if (at < kList) L.u.list[at] = rank_key(Elem<E>::at(row, e0 + e), e0 + e);
+      if (at < kList) L.u.list[at] = static_cast<uint64_t>(e0 + e);
     };
-    WantBetween<E, decltype(marked)> want{marked, low, high};
     if (kJoin && P > 1) {
       // only the parts that hold something in those bins
-      for (int i = tid; i < P * (last - first + 1); i += NT) {
-        const int p = i % P, j = first + i / P;
-        if (!(L.mark[j >> 5] >> (j & 31) & 1u)) continue;
-        const double q = static_cast<double>(j) - (static_cast<double>(top) - (g.k - kMagic) - L.ptop[p]);
-        if (q >= 0.0 && parts[p].bin[static_cast<int>(q)] != 0) atomicOr(&L.parts, 1u << p);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q >= rs.n) break;
+        for (int i = tid; i < P * (rs.b[q] - rs.a[q] + 1); i += NT) {
+          const int p = i % P, j = rs.a[q] + i / P;
+          const double at = static_cast<double>(j) - (static_cast<double>(top) - (g.k - kMagic) - L.ptop[p]);
+          if (at >= 0.0 && parts[p].bin[static_cast<int>(at)] != 0) atomicOr(&L.parts, 1u << p);
+        }
       }
       lds_barrier();
     }
@@ -737,8 +776,16 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     for (int p = 0; p < P; ++p) {
       if (!(take >> p & 1u)) continue;
       if (P > 1) row_part<E>(row, V, P, p, e0, e1);
-      GatherVisit<E, NT, U, decltype(want), decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
+      GatherVisit<E, NT, U, WantBetween<E>, decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
       visit_row<E, NT, U, kLoadNormal>(row + e0, e1 - e0, v);
+    }
+    // the values are read again at the end, all at once: a load per element
+    // as it is found would hold its wave up each time
+    lds_barrier();
+    const int got = min(L.n, kList);
+    for (int i = tid; i < got; i += NT) {
+      const int e = static_cast<int>(L.u.list[i]);
+      L.u.list[i] = rank_key(Elem<E>::at(row, e), e);
     }
   };
 
@@ -764,7 +811,6 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
       L.red_i[wave] = nb;
     }
     if (tid < 8) L.j[tid] = kReach - 1;
-    if (tid < kReach / 32) L.mark[tid] = 0;
     if (tid == 0) {
       L.n = 0;
       L.before = 0;
@@ -827,8 +873,6 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     more_than(4, exceed(u * hi));
     lds_barrier();
     const int d0 = L.j[3], d1 = L.j[4];
-    int last = max(max(jk, jm), max(p1, d1));
-    int first = min(min(jk < 0 ? d0 : jk, jm < 0 ? d0 : jm), min(p0, d0));
     auto is_cut = [&](int j) { return j == jk || j == jm || (j >= p0 && j <= p1); };
     auto is_draw = [&](int j) { return j >= d0 && j <= d1; };
     // how many elements they hold, from their weights
@@ -846,16 +890,14 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
 #pragma unroll
     for (int k = 0; k < NW; ++k) held += L.red_d[k];
     two = held > static_cast<double>(kList - kList / 16);
-    if (two) {
-      last = max(max(jk, jm), p1);
-      first = min(min(jk < 0 ? kReach : jk, jm < 0 ? kReach : jm), p0);
-    }
-    for (int j = tid; j <= last; j += NT)
-      if (is_cut(j) || (!two && is_draw(j))) atomicOr(&L.mark[j >> 5], 1u << (j & 31));
-    lds_barrier();
+    Ranges rs;
+    if (jk >= 0) rs.add(jk, jk);
+    rs.add(p0, p1);
+    if (jm >= 0) rs.add(jm, jm);
+    if (!two) rs.add(d0, d1);
 
     // ---- the elements of those bins
-    if (!two || first <= last) collect(first, last);
+    if (rs.n) collect(rs);
     lds_barrier();
     n = L.n;
     left = total;
@@ -950,13 +992,14 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
             j = L.j[4 + c];
           }
           if (c == 2 && two) {
-            if (tid < kReach / 32) L.mark[tid] = tid == j >> 5 ? 1u << (j & 31) : 0u;
             if (tid == 0) {
               L.n = 0;
               L.parts = 0;
             }
             lds_barrier();
-            collect(j, j);
+            Ranges rs;
+            rs.add(j, j);
+            collect(rs);
             lds_barrier();
             n = L.n;
             if (n > kList) {
