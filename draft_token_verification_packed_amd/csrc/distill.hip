@@ -19,6 +19,11 @@
 // once the student agrees with the teacher the ids hold nearly everything
 // and the difference would keep few digits. A bit per element in LDS, read a
 // vector at a time, says which elements are named.
+//
+// HBM bounds all of it: the losses of 640 bf16 rows of 152064 take 38 us (5.1
+// TB/s), the gradient of 2048 from their state 245 us (5.1 TB/s read and
+// written, as a large copy), loss and gradient in one launch 290 us, 240 being
+// one read and one write at a copy's rate.
 #include "row_visit.hpp"
 #include "rows.hpp"
 
@@ -326,15 +331,6 @@ __global__ __launch_bounds__(NT) void distill_forward_kernel(DistillArgs a) {
 
 // Few rows: a workgroup per part of a row leaves the part's sums, and one
 // wave per row joins them.
-template <typename E>
-__device__ __forceinline__ void even_part(const E* row, int V, int P, int part, int& e0, int& e1) {
-  constexpr int N = Elem<E>::kVec;
-  const int head = row_head(row, V);
-  const int64_t nv = (V - head) / N;
-  e0 = part == 0 ? 0 : head + static_cast<int>(nv * part / P) * N;
-  e1 = part == P - 1 ? V : head + static_cast<int>(nv * (part + 1) / P) * N;
-}
-
 template <typename E, int NT, int U, bool kRest>
 __global__ __launch_bounds__(NT) void distill_part_kernel(DistillArgs a) {
   __shared__ DistillLds<NT> L;
@@ -342,7 +338,7 @@ __global__ __launch_bounds__(NT) void distill_part_kernel(DistillArgs a) {
   const int part = static_cast<int>(blockIdx.x - r * a.parts);
   const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld;
   int e0, e1;
-  even_part<E>(row, a.x.V, a.parts, part, e0, e1);
+  row_part<E>(row, a.x.V, a.parts, part, e0, e1);
   Entries t;
   int bits = 0;
   if (threadIdx.x < kWave) {
@@ -532,7 +528,7 @@ __global__ __launch_bounds__(NT) void distill_backward_kernel(DistillArgs a) {
   const int64_t r = blockIdx.x / a.parts;
   const int part = static_cast<int>(blockIdx.x - r * a.parts);
   int e0, e1;
-  even_part<E>(static_cast<const E*>(a.grad) + r * a.grad_ld, a.x.V, a.parts, part, e0, e1);
+  row_part<E>(static_cast<const E*>(a.grad) + r * a.grad_ld, a.x.V, a.parts, part, e0, e1);
   grad_range<E, NT, U>(a, r, e0, e1, a.state + r * kStateWords, ids, teach);
 }
 

@@ -13,18 +13,27 @@
 // 1e-7 decides the wrong token in about one row of a hundred where the law is
 // broad. So weights are summed as 64-bit integers, exact in any order:
 //
-// The row is streamed once. With y = 32 x / T, an element falls into bin
-// rint(y), and its weight relative to the bin's centre, exp((y - rint(y)) /
-// 32) by a polynomial in float64, is added to the bin as an integer (2^44 to
-// one for a vocabulary up to 2^18) by one LDS atomic. Bins reach from 48 T below the first group's
-// maximum to 80 T above it; lower elements weigh less than e^-48 and move no
-// cut, and a row that rises beyond is streamed again from its true maximum.
-// A scan over the 48 T below the maximum then turns bins into cumulative
-// weights, and each cut and the draw are known to within a bin or two (a cut
-// inside a bin leaves the total of what follows it known to within that
-// bin). One more pass, mostly served by the caches, gathers the elements of
-// those bins, and the exact order among them decides. Bins too full for the
-// gathered list fall back to a radix search over the whole row.
+// float32: the row is streamed once. With y = per x / T, an element falls into
+// bin rint(y), and its weight relative to the bin's centre, exp((y - rint(y))
+// / per) by a polynomial in float64, is added to the bin as an integer (2^44
+// to one for a vocabulary up to 2^18) by one LDS atomic. With the widest grid,
+// per = 32, bins reach from 48 T below the first group's maximum to 80 T above
+// it; lower elements weigh less than e^-48 and move no cut. A scan over the
+// bins below the maximum turns them into cumulative weights, and each cut and
+// the draw are known to within a bin or two (a cut inside a bin leaves the
+// total of what follows it known to within that bin). One more pass gathers
+// the elements of those bins, and the exact order among them decides. The
+// float64 work (18 issue slots an element) and the atomics (16 us a row of
+// 152064 and CU, 28 with the counts of a top-k row) bound the stream beside
+// the HBM share of 26 us: 128 rows with every filter take 56 us. Per-element
+// LDS sums in float would be as many atomics and 1e-7; moments per bin more.
+//
+// bfloat16: a count per 16-bit code, see CodeLds: 512 rows of 152064 with
+// top-p take 59 us, of which the counting is 26 and the search for the drawn
+// element, which reads the row again, 13.
+//
+// Rows neither can serve (too many equal elements at a cut for the list,
+// values too large for bins) are searched a byte of the rank key at a time.
 #include "row_visit.hpp"
 #include "rows.hpp"
 
@@ -57,16 +66,6 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ bool any_lane(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
 
-__device__ __forceinline__ uint32_t up_key(float x) {
-  const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-}
-__device__ __forceinline__ uint64_t rank_key(float x, int e) {
-  return (static_cast<uint64_t>(up_key(x)) << 32) | static_cast<uint32_t>(~e);
-}
 __device__ __forceinline__ float key_x(uint64_t k) { return key_value(static_cast<uint32_t>(k >> 32)); }
 
 template <int NT> struct DrawLds {
@@ -573,16 +572,6 @@ struct BinPart {
   ull bin[kReach];          // downwards from the part's own top bin
   uint32_t cnt[kReach];
 };
-// Part `part` of P equal shares of a row's 16-byte body.
-template <typename E>
-__device__ __forceinline__ void row_part(const E* row, int V, int P, int part, int& e0, int& e1) {
-  constexpr int N = Elem<E>::kVec;
-  const int head = row_head(row, V);
-  const int64_t nv = (V - head) / N;
-  e0 = part == 0 ? 0 : head + static_cast<int>(nv * part / P) * N;
-  e1 = part == P - 1 ? V : head + static_cast<int>(nv * (part + 1) / P) * N;
-}
-
 template <int NT>
 __device__ __forceinline__ void leave_bins(const Binned& b, bool count, BinPart* out, const DrawLds<NT>& L) {
   const bool fine = b.m > -INFINITY && b.m < INFINITY;

@@ -16,6 +16,31 @@ __device__ __forceinline__ int row_head(const E* row, int V) {
   return head > V ? V : head;
 }
 
+// Part `part` of P equal shares of a row's 16-byte body, as elements [e0, e1):
+// the first part also takes the elements before the body, the last those
+// after it.
+template <typename E>
+__device__ __forceinline__ void row_part(const E* row, int V, int P, int part, int& e0, int& e1) {
+  constexpr int N = Elem<E>::kVec;
+  const int head = row_head(row, V);
+  const int64_t nv = (V - head) / N;
+  e0 = part == 0 ? 0 : head + static_cast<int>(nv * part / P) * N;
+  e1 = part == P - 1 ? V : head + static_cast<int>(nv * (part + 1) / P) * N;
+}
+
+// Order-preserving unsigned key of a float (-0 mapped to +0), and back.
+__device__ __forceinline__ uint32_t up_key(float x) {
+  const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+// One 64-bit key in rank order (value desc, index asc): larger is earlier.
+__device__ __forceinline__ uint64_t rank_key(float x, int e) {
+  return (static_cast<uint64_t>(up_key(x)) << 32) | static_cast<uint32_t>(~e);
+}
+
 // Running sum of exp2(x c) kept as s 2^mc, mc an integer (log2 units) at or
 // just above the largest x c seen, so every rescale is an exact power of two.
 // Terms are summed in float within a group and the groups in float64.

@@ -28,19 +28,6 @@ namespace {
 constexpr int kFewTop = 64;
 constexpr int kTopList = 4096;    // elements a row may keep
 
-// Order-preserving unsigned key of a float (-0 mapped to +0).
-__device__ __forceinline__ uint32_t up_key(float x) {
-  const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-}
-// One 64-bit key in rank order: larger is earlier.
-__device__ __forceinline__ uint64_t rank_key(float x, int e) {
-  return (static_cast<uint64_t>(up_key(x)) << 32) | static_cast<uint32_t>(~e);
-}
-
 constexpr int kTopKeys = 1024;    // of them, those that are ranked
 
 __device__ __forceinline__ void top_lse(const TopArgs& a, int64_t r, float mc, double total) {
@@ -209,10 +196,8 @@ __global__ __launch_bounds__(NT, kWaves) void top_kernel(TopArgs a) {
     r = blockIdx.x / a.parts;
     const E* whole = static_cast<const E*>(a.x.p) + r * a.x.ld;
     const int part = static_cast<int>(blockIdx.x - r * a.parts);
-    const int head = row_head(whole, V);
-    const int64_t nv = (V - head) / Elem<E>::kVec;
-    const int e1 = part == a.parts - 1 ? V : head + static_cast<int>(nv * (part + 1) / a.parts) * Elem<E>::kVec;
-    e0 = part == 0 ? 0 : head + static_cast<int>(nv * part / a.parts) * Elem<E>::kVec;
+    int e1;
+    row_part<E>(whole, V, a.parts, part, e0, e1);
     V = e1 - e0;
   }
   const E* __restrict__ row = static_cast<const E*>(a.x.p) + r * a.x.ld + e0;
