@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kDrawThreads = 512;
 constexpr int kDrawUnroll = 2;
+constexpr int kGatherUnroll = 4;   // the second readings, which do less per vector
 constexpr int kBins = 4096;
 constexpr int kReach = 1536;       // bins below the maximum that count (48 T)
 constexpr int kBase = kReach + 2;  // about where the first group's maximum lies
@@ -765,8 +766,8 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     for (int p = 0; p < P; ++p) {
       if (!(take >> p & 1u)) continue;
       if (P > 1) row_part<E>(row, V, P, p, e0, e1);
-      GatherVisit<E, NT, U, WantBetween<E>, decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
-      visit_row<E, NT, U, kLoadNormal>(row + e0, e1 - e0, v);
+      GatherVisit<E, NT, kGatherUnroll, WantBetween<E>, decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
+      visit_row<E, NT, kGatherUnroll, kLoadNormal>(row + e0, e1 - e0, v);
     }
     // the values are read again at the end, all at once: a load per element
     // as it is found would hold its wave up each time
@@ -1102,7 +1103,7 @@ struct CodeVisit {
 
 // The r-th (1, 2, ..) element of [e0, e1) that holds `code`, by index, or -1
 // where there are more than the list holds.
-template <int NT, int U>
+template <int NT>
 __device__ __forceinline__ int nth_code(const uint16_t* row, int e0, int e1, uint32_t code, int r, CodeLds<NT>& L) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   if (tid == 0) L.n = 0;
@@ -1111,8 +1112,8 @@ __device__ __forceinline__ int nth_code(const uint16_t* row, int e0, int e1, uin
   auto put = [&](int at, int e) {
     if (at < kCodeList) L.list[at] = static_cast<uint32_t>(e);
   };
-  GatherVisit<uint16_t, NT, U, WantCode, decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
-  visit_row<uint16_t, NT, U, kLoadNormal>(row + e0, e1 - e0, v);
+  GatherVisit<uint16_t, NT, kGatherUnroll, WantCode, decltype(put)> v{want, put, &L.n, row_head(row + e0, e1 - e0)};
+  visit_row<uint16_t, NT, kGatherUnroll, kLoadNormal>(row + e0, e1 - e0, v);
   lds_barrier();
   const int n = L.n;
   if (n > kCodeList || r > n) return -1;
@@ -1441,7 +1442,7 @@ __global__ __launch_bounds__(NT, 4) void draw_join_kernel(DrawArgs a) {
       }
       int e0, e1;
       row_part<E>(row, a.x.V, a.parts, p, e0, e1);
-      return nth_code<NT, U>(row, e0, e1, code, q, L.code);
+      return nth_code<NT>(row, e0, e1, code, q, L.code);
     });
     if (done) return;
     lds_barrier();
@@ -1473,7 +1474,7 @@ __global__ __launch_bounds__(NT, 4) void draw_kernel(DrawArgs a) {
 #pragma unroll
     for (int k = 0; k < PER; ++k) cnt[k] = cell_count(L.code, static_cast<int>(threadIdx.x) * PER + k);
     const bool done = draw_codes<NT, PER>(a, r, d, greedy, bits, cnt, L.code, [&](uint32_t code, int q) {
-      return nth_code<NT, U>(row, 0, a.x.V, code, q, L.code);
+      return nth_code<NT>(row, 0, a.x.V, code, q, L.code);
     });
     if (done) return;
     lds_barrier();
