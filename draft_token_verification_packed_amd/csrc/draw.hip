@@ -375,12 +375,22 @@ __device__ __forceinline__ uint64_t find_cut(const Each& each, const Weigh& w, c
       L.red_u[0] = im;
       L.red_u[1] = im - dm;
       L.red_i[0] = in - dn;
+      L.red_i[1] = dn;
     }
     lds_barrier();
     through = w0 + static_cast<double>(L.red_u[0]) / w.one;
     mass = L.red_u[1];
     num = L.red_i[0];
     prefix |= static_cast<uint64_t>(kDigits - 1 - hit) << shift;
+    if (shift > 0 && L.red_i[1] == 1) {
+      // one element left: its key needs no more digits
+      each([&](float x, int e) {
+        const uint64_t key = rank_key(x, e);
+        if (key >> shift == prefix >> shift) L.key[0] = key;
+      });
+      lds_barrier();
+      return L.key[0];
+    }
   }
   lds_barrier();
   return prefix;
