@@ -273,6 +273,13 @@ struct Weigh {
 __device__ __forceinline__ double reach(double t) { return t - t * kEqual; }
 __device__ __forceinline__ double exceed(double t) { return t + t * kEqual; }
 
+// Log-probability of a token at z among survivors of weight `left`; a lone
+// survivor's is 0, which the sums' last bits would not always say.
+__device__ __forceinline__ float log_share(double z, double left) {
+  const double p = z - log(left);
+  return fabs(p) < kEqual ? 0.f : static_cast<float>(p);
+}
+
 // A cut: the first element in rank order with `count` elements through it
 // (count > 0), or a cumulative weight of `target` (strict: more than it).
 struct Cut {
@@ -1018,7 +1025,7 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
   if (tid == 0) {
     const float x = key_x(key);
     a.token[r] = static_cast<int>(~static_cast<uint32_t>(key));
-    if (a.logprob) a.logprob[r] = greedy ? 0.f : static_cast<float>(w.z(x) - log(left));
+    if (a.logprob) a.logprob[r] = greedy ? 0.f : log_share(w.z(x), left);
     if (a.lse) a.lse[r] = static_cast<float>(w.m / T + log(total));
     if (bits && a.error_flag) atomicOr(a.error_flag, bits);
   }
@@ -1322,7 +1329,7 @@ __device__ __forceinline__ bool draw_codes(const DrawArgs& a, int64_t r, const D
   if (token < 0) return false;
   if (tid == 0) {
     a.token[r] = token;
-    if (a.logprob) a.logprob[r] = greedy ? 0.f : static_cast<float>(z_of(j) - log(left));
+    if (a.logprob) a.logprob[r] = greedy ? 0.f : log_share(z_of(j), left);
     if (a.lse) a.lse[r] = static_cast<float>(w.m / T + log(total));
     if (bits && a.error_flag) atomicOr(a.error_flag, bits);
   }

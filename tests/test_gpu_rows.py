@@ -126,6 +126,19 @@ def test_draws_agree_with_sampled_verification(vsv):
     assert np.array_equal(host(out["token"]), host(ref["row_token"]))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_lone_survivor_is_certain(vsv, dtype):
+    # whatever leaves one token, its log-probability is 0 and not a rounding
+    n, V = 40, 4099
+    rng, x, _ = _store(19, n, V, dtype, ("plain", "spikes", "wide"), 0, 0)
+    f = lambda v: to_dev(np.full(n, v, dtype=np.float32))
+    T, u = to_dev(rng.uniform(0.3, 2.0, n).astype(np.float32)), to_dev(rng.random(n, dtype=np.float32))
+    one, off = to_dev(np.ones(n, dtype=np.int32)), to_dev(np.zeros(n, dtype=np.int32))
+    for k, p, mp in ((one, 1.0, 0.0), (one, 0.9, 0.3), (off, 1e-6, 0.0), (one, 1.0, 0.05)):
+        out = vsv.sample_rows(x, T, k, f(p), f(mp), u)
+        assert not np.any(host(out["logprob"]))
+
+
 def test_draw_flags(vsv):
     import torch
     V = 130
