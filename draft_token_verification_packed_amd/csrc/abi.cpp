@@ -291,7 +291,7 @@ vsv_status vsv_distill_forward(const vsv_distill* d, float* loss, double* state,
   vsv::DistillArgs a;
   vsv_status st = prepare_distill(d, &a);
   if (st != VSV_OK) return st;
-  if (!loss) return VSV_EINVAL;
+  if (!loss || !aligned(state, 8)) return VSV_EINVAL;
   st = distill_scratch(&a, workspace, workspace_bytes);
   if (st != VSV_OK) return st;
   a.loss = loss;
@@ -307,7 +307,7 @@ vsv_status vsv_distill_backward(const vsv_distill* d, const double* state, const
   vsv::DistillArgs a;
   const vsv_status st = prepare_distill(d, &a);
   if (st != VSV_OK) return st;
-  if (!state || !distill_grad_ok(a, grad, grad_ld)) return VSV_EINVAL;
+  if (!state || !aligned(state, 8) || !distill_grad_ok(a, grad, grad_ld)) return VSV_EINVAL;
   a.state = const_cast<double*>(state);
   a.weight = weight;
   a.grad = grad;

@@ -336,8 +336,8 @@ size_t vsv_distill_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtyp
  * [num_rows, VSV_DISTILL_STATE], or NULL). VSV_FLAG_LOGITS: a NaN or +inf
  * logit in a row that has entries, or none finite; VSV_FLAG_TOKEN: an id at
  * or beyond vocab (counts as unused).
- * Errors: VSV_EINVAL (NULL student, ids, top or loss; sizes, alignment,
- * dtype, temperature), VSV_EWORKSPACE, VSV_EHIP. */
+ * Errors: VSV_EINVAL (NULL student, ids, top or loss; sizes, alignment of
+ * the logits or the state, dtype, temperature), VSV_EWORKSPACE, VSV_EHIP. */
 #define VSV_DISTILL_STATE 5
 vsv_status vsv_distill_forward(const vsv_distill* d, float* loss, double* state, int32_t* error_flag,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -120,6 +120,7 @@ def test_distill_output_refusals(L):
     assert _forward(L, loss=None) == 1
     assert _grad(L, loss=None) == 1
     assert _backward(L, state=None) == 1
+    assert _backward(L, state=0x1004) == 1
     for call in (_backward, _grad):
         assert call(L, grad=None) == 1
         assert call(L, grad=0x20001) == 1
