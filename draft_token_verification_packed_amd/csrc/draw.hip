@@ -34,6 +34,7 @@
 //
 // Rows neither can serve (too many equal elements at a cut for the list,
 // values too large for bins) are searched a byte of the rank key at a time.
+#include "draw_grid.hpp"
 #include "row_visit.hpp"
 #include "rows.hpp"
 
@@ -44,17 +45,11 @@ namespace {
 constexpr int kDrawThreads = 512;
 constexpr int kDrawUnroll = 2;
 constexpr int kGatherUnroll = 4;   // the second readings, which do less per vector
-constexpr int kBins = 4096;
-constexpr int kReach = 1536;       // bins below the maximum that count (48 T)
-constexpr int kBase = kReach + 2;  // about where the first group's maximum lies
 constexpr double kPerT = 32.0;     // bins per T, at least
 constexpr double kMostPerT = 1024.0;
 constexpr int kList = 4096;        // elements the gathered list holds
 constexpr int kMostParts = 8;
 constexpr int kFew = 128;          // lists decided by direct comparison
-// Beyond this |x| per / T bins are too coarse in float64 to trust.
-constexpr double kFarBin = 4194304.0;
-
 // Sums hold to about 1e-13 of the row's weight (a weight's integer is off by
 // up to half a unit, 2^-45 of it for a vocabulary up to 2^18; the polynomial
 // by 2e-14), so two that differ by less than this share are taken as equal:
@@ -93,23 +88,6 @@ template <int NT> struct DrawLds {
 };
 
 // ---------------------------------------------------------------- bins
-
-// Position of an element among the bins: t = fma(x, s, k) with k = 1.5 2^52
-// minus an even integer rounds to the bin's number in the low bits of t
-// (even, so that a y halfway between two bins goes to the same one on every
-// grid).
-constexpr double kMagic = 6755399441055744.0;         // 1.5 * 2^52
-constexpr uint32_t kMagicHi = 0x43380000u;
-struct Grid {
-  double s, k, per;   // s = per / T: bins per T
-  __device__ __forceinline__ double t(float x) const { return fma(static_cast<double>(x), s, k); }
-  // bin number, or -1 where the element lies outside the bins
-  static __device__ __forceinline__ int slot(double t) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, t);
-    const uint32_t lo = static_cast<uint32_t>(b);
-    return (static_cast<uint32_t>(b >> 32) == kMagicHi && lo < static_cast<uint32_t>(kBins)) ? static_cast<int>(lo) : -1;
-  }
-};
 
 template <typename E, int NT, int U, bool kCount>
 struct BinVisit {
@@ -528,10 +506,7 @@ __device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, con
         lds_barrier();
       }
       f.cut = per > kPerT ? static_cast<float>(static_cast<double>(ref) - 48.0 * T) : INFINITY;
-      f.g = Grid{per / T, 0.0, per};
-      const double y = static_cast<double>(ref) * f.g.s;
-      far = !(fabs(y) < kFarBin);
-      f.g.k = kMagic - (far ? 0.0 : 2.0 * rint(0.5 * y)) + static_cast<double>(kBase);
+      f.g = Grid::around(ref, T, per, far);
       f.c[0] = one;
 #pragma unroll
       for (int k = 1; k < 6; ++k) f.c[k] = f.c[k - 1] * (1.0 / (per * k));
@@ -738,14 +713,6 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
   auto at_least = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] >= t; }); };
   auto more_than = [&](int q, double t) { first_bin(q, [&](int k) { return through[k] > t; }); };
 
-  // the least float whose bin is at least b
-  auto least_in = [&](int b) {
-    auto in = [&](float x) { return g.t(x) >= kMagic + static_cast<double>(b); };
-    float x = static_cast<float>((static_cast<double>(b) - 0.5 - (g.k - kMagic)) / g.s);
-    while (in(x)) x = key_value(up_key(x) - 1u);
-    while (!in(x)) x = key_value(up_key(x) + 1u);
-    return x;
-  };
   // the elements of the ranges' bins into the list
   auto collect = [&](const Ranges& rs) {
     WantBetween<E> want;
@@ -756,9 +723,11 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
       want.low[i] = INFINITY;
       want.high[i] = -INFINITY;
       if (i < rs.n) {
-        want.low[i] = least_in(top - rs.b[i]);
+        want.low[i] = g.least_in(top - rs.b[i]);
+        want.high[i] = rs.a[i] > 0 ? next_down(g.least_in(top - rs.a[i] + 1)) : m;
+        // (bins narrower than the floats may hold none)
+        if (want.high[i] < want.low[i]) want.low[i] = want.high[i] = INFINITY;
         want.least = fminf(want.least, want.low[i]);
-        want.high[i] = rs.a[i] > 0 ? key_value(up_key(least_in(top - rs.a[i] + 1)) - 1u) : m;
       }
     }
     int e0 = 0, e1 = V;

@@ -5,6 +5,7 @@
 #pragma once
 
 #include "device.hpp"
+#include "float_order.hpp"
 #include "row_stream.hpp"
 
 namespace vsv {
@@ -28,14 +29,6 @@ __device__ __forceinline__ void row_part(const E* row, int V, int P, int part, i
   e1 = part == P - 1 ? V : head + static_cast<int>(nv * (part + 1) / P) * N;
 }
 
-// Order-preserving unsigned key of a float (-0 mapped to +0), and back.
-__device__ __forceinline__ uint32_t up_key(float x) {
-  const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-}
 // One 64-bit key in rank order (value desc, index asc): larger is earlier.
 __device__ __forceinline__ uint64_t rank_key(float x, int e) {
   return (static_cast<uint64_t>(up_key(x)) << 32) | static_cast<uint32_t>(~e);
