@@ -18,7 +18,11 @@
 // q_r is summed over the elements outside the ids, not taken from 1 - q(ids):
 // once the student agrees with the teacher the ids hold nearly everything
 // and the difference would keep few digits. A bit per element in LDS, read a
-// vector at a time, says which elements are named.
+// vector at a time, says which elements are named. That sum has an exponent
+// reference of its own, and the unnamed elements' gradient is taken relative
+// to it, exp2(x c - reference) times M / (sum of the row) - t_r / (sum of the
+// rest): with the row's reference both factors of q_i t_r / q_r would leave
+// the float range once the named logits lie 88 T above the rest.
 //
 // HBM bounds all of it: the losses of 640 bf16 rows of 152064 take 38 us (5.1
 // TB/s), the gradient of 2048 from their state 245 us (5.1 TB/s read and
@@ -58,7 +62,7 @@ __device__ __forceinline__ int map_slot(int e, int head, int& bit) {
 template <typename E, int NT, int U, bool kRest>
 struct SumVisit {
   ExpSum p;
-  float c;
+  float c, most;   // most: the largest element seen
   const uint8_t* map;
   int head;
 
@@ -79,6 +83,7 @@ struct SumVisit {
 #pragma unroll
       for (int k = 0; k < N; ++k) gmax = fmaxf(gmax, f[u * N + k]);
     }
+    if (kRest) most = fmaxf(most, gmax);
     add_terms<U * N>(p, f, gmax, c);
   }
   __device__ __forceinline__ void one(float x, int e) {
@@ -87,21 +92,25 @@ struct SumVisit {
       const int slot = map_slot<E>(e, head, bit);
       if (map[slot] >> bit & 1) return;
     }
+    if (kRest) most = fmaxf(most, x);
     add_term(p, x, c);
   }
 };
 
-// A range's sums relative to one exponent reference.
+// A range's sums outside and over the named ids, each relative to its own
+// exponent reference, and the largest elements there. Without a rest
+// everything counts as outside.
 struct Sums {
-  float mc;
-  double rest, named;
+  double rest = 0.0, named = 0.0;
+  float mr = -FLT_MAX, xr = -INFINITY, mn = -FLT_MAX, xn = -INFINITY;
 };
+static_assert(sizeof(Sums) == kPartDoubles * sizeof(double), "a part's scratch");
 
 template <int NT> struct DistillLds {
   static constexpr int NW = NT / kWave;
   uint32_t map[kMapWords];
-  float mc[NW];
-  double rest[NW], named[NW];
+  float mr[NW], xr[NW];
+  double rest[NW];
   double row[kStateWords];
   int any;
 };
@@ -140,7 +149,8 @@ __device__ __forceinline__ void load_entries(const DistillArgs& a, int64_t r, co
 }
 
 // The sums of elements [e0, e1) of a row over the whole workgroup. With
-// kRest the named elements' weights are kept apart, each id counted once.
+// kRest the named elements' weights are kept apart, each id counted once; the
+// wave that handles the entries receives those.
 template <typename E, int NT, int U, bool kRest, int kAux>
 __device__ __forceinline__ Sums range_sums(const DistillArgs& a, const E* __restrict__ row, int e0, int e1, Entries& t,
                                            DistillLds<NT>& L) {
@@ -150,6 +160,7 @@ __device__ __forceinline__ Sums range_sums(const DistillArgs& a, const E* __rest
   SumVisit<E, NT, U, kRest> f;
   f.p = ExpSum{-FLT_MAX, 0.0};
   f.c = a.c;
+  f.most = -INFINITY;
   f.map = reinterpret_cast<const uint8_t*>(L.map);
   // pieces end at 16-byte boundaries of the row, so only the first has
   // elements before its body and only the last some after it
@@ -178,39 +189,57 @@ __device__ __forceinline__ Sums range_sums(const DistillArgs& a, const E* __rest
     p0 = p1;
     if (kRest && p0 < e1) lds_barrier();
   }
-  if (kRest && wave == 0) {
-#pragma unroll
-    for (int j = 0; j < kEntries; ++j)
-      if (t.first[j]) raise_ref(f.p, t.y[j], a.c);
-  }
-  const float mw = wave_all(f.p.mc, MaxOp());
-  if (lane == 0) L.mc[wave] = mw;
-  lds_barrier();
-  Sums o{L.mc[0], 0.0, 0.0};
-#pragma unroll
-  for (int w = 1; w < NW; ++w) o.mc = fmaxf(o.mc, L.mc[w]);
-  double named = 0.0;
-  if (kRest && wave == 0) {
-#pragma unroll
-    for (int j = 0; j < kEntries; ++j)
-      if (t.first[j]) named += static_cast<double>(fast_exp2(exp_arg(t.y[j], a.c, o.mc)));
-  }
-  const double sr = wave_sum_f64(sum_at(f.p.s, f.p.mc, o.mc));
-  const double sn = wave_sum_f64(named);
+  const float mw = wave_all(f.p.mc, MaxOp()), xw = wave_all(f.most, MaxOp());
   if (lane == 0) {
-    L.rest[wave] = sr;
-    L.named[wave] = sn;
+    L.mr[wave] = mw;
+    L.xr[wave] = xw;
   }
   lds_barrier();
+  Sums o;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    o.rest += L.rest[w];
-    o.named += L.named[w];
+    o.mr = fmaxf(o.mr, L.mr[w]);
+    o.xr = fmaxf(o.xr, L.xr[w]);
+  }
+  const double sr = wave_sum_f64(sum_at(f.p.s, f.p.mc, o.mr));
+  if (lane == 0) L.rest[wave] = sr;
+  lds_barrier();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) o.rest += L.rest[w];
+  if (kRest && wave == 0) {
+#pragma unroll
+    for (int j = 0; j < kEntries; ++j)
+      if (t.first[j]) o.xn = fmaxf(o.xn, t.y[j]);
+    o.xn = wave_all(o.xn, MaxOp());
+    ExpSum n{-FLT_MAX, 0.0};
+    raise_ref(n, o.xn, a.c);
+    o.mn = n.mc;
+    double named = 0.0;
+#pragma unroll
+    for (int j = 0; j < kEntries; ++j)
+      if (t.first[j]) named += static_cast<double>(fast_exp2(exp_arg(t.y[j], a.c, o.mn)));
+    o.named = wave_sum_f64(named);
   }
   return o;
 }
 
+// The exponent references of a row's unnamed elements and of its whole, one
+// word of its state. (Put together as an integer: the cast of a struct of two
+// floats goes through memory, which the compiler moves to LDS by way of the
+// dispatch packet, and the kernels took up to 7 us more.)
+__device__ __forceinline__ double pack_refs(float rest, float row) {
+  return __builtin_bit_cast(double, static_cast<uint64_t>(__float_as_uint(row)) << 32 | __float_as_uint(rest));
+}
+__device__ __forceinline__ float rest_ref(double s) { return __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, s))); }
+__device__ __forceinline__ float row_ref(double s) { return __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, s) >> 32)); }
+
 constexpr double kLn2 = 0.69314718055994530942;
+
+// x c as the terms took it, above their reference m.
+__device__ __forceinline__ double above_ref(float x, float c, float m) {
+  return fabsf(m) < kFarRef ? static_cast<double>(x) * static_cast<double>(c) - static_cast<double>(m)
+                            : static_cast<double>(far_arg(x, c, m));
+}
 
 // The row's loss and state from its sums, by one whole wave: `st` receives
 // what the backward pass needs.
@@ -218,7 +247,8 @@ template <bool kRest>
 __device__ __forceinline__ void finish_distill(const DistillArgs& a, int64_t r, const Sums& s, const Entries& t, int bits,
                                                double* st) {
   const int lane = threadIdx.x & (kWave - 1);
-  const double total = s.rest + s.named;
+  const float mc = fmaxf(s.mr, s.mn);
+  const double total = sum_at(s.rest, s.mr, mc) + sum_at(s.named, s.mn, mc);
   const double lg = log2(total);
   // log t_k = z_k / T - lt
   double lt;
@@ -245,33 +275,36 @@ __device__ __forceinline__ void finish_distill(const DistillArgs& a, int64_t r, 
       if (!(tk == 0.0)) {
         mass += tk;
         // ln q_k; the exponent is exact where its float would not be
-        const double at = fabsf(s.mc) < kFarRef
-                              ? static_cast<double>(t.y[j]) * static_cast<double>(a.c) - static_cast<double>(s.mc)
-                              : static_cast<double>(far_arg(t.y[j], a.c, s.mc));
+        const double at = above_ref(t.y[j], a.c, mc);
         loss += tk * (lk - kLn2 * (at - lg));
       }
     }
   }
   mass = wave_sum_f64(mass);
   loss = wave_sum_f64(loss);
-  double every = mass, scale = mass;
+  double every = mass, off = 0.0;   // off: what t_r takes off the unnamed tokens' factor
   if (kRest) {
     const double tr = 1.0 - mass;
     if (tr > 0.0) {
       every += tr;
-      const double qr = s.rest / total;
-      loss += tr * (log(tr) - log(qr));
-      scale = s.rest > 0.0 ? every - tr / qr : every;
-    } else {
-      scale = every;
+      const float xm = fmaxf(s.xr, s.xn);
+      // ln q_r by way of the two largest elements, whose difference may be
+      // most of it: in float64, where x c is rounded
+      const double log_qr = s.rest == 0.0 ? -INFINITY
+                                          : (static_cast<double>(s.xr) - static_cast<double>(xm)) * a.inv_t +
+                                                kLn2 * ((log2(s.rest) - above_ref(s.xr, a.c, s.mr)) -
+                                                        (lg - above_ref(xm, a.c, mc)));
+      loss += tr * (log(tr) - log_qr);
+      off = s.rest == 0.0 ? 0.0 : tr / s.rest;
     }
   }
   if (!(total > 0.0 && total < INFINITY) || !(mass < INFINITY)) bits |= VSV_FLAG_LOGITS;
   bits = wave_all(bits, [](int p, int q) { return p | q; });
   if (lane == 0) {
-    st[0] = static_cast<double>(s.mc);
-    st[1] = 1.0 / total;
-    st[2] = scale;
+    const double norm = 1.0 / total;
+    st[0] = pack_refs(s.mr, mc);
+    st[1] = norm;
+    st[2] = sum_at(every, s.mr, mc) * norm - off;
     st[3] = every;
     st[4] = lt;
     if (a.loss) a.loss[r] = static_cast<float>(loss);
@@ -352,10 +385,7 @@ __global__ __launch_bounds__(NT) void distill_part_kernel(DistillArgs a) {
   }
   const Sums s = range_sums<E, NT, U, kRest, kLoadStream>(a, row, e0, e1, t, L);
   if (threadIdx.x == 0) {
-    double* out = a.part + blockIdx.x * static_cast<int64_t>(kPartDoubles);
-    out[0] = s.mc;
-    out[1] = s.rest;
-    out[2] = s.named;
+    reinterpret_cast<Sums*>(a.part)[blockIdx.x] = s;
   }
 }
 
@@ -374,17 +404,15 @@ __global__ __launch_bounds__(kWave) void distill_join_kernel(DistillArgs a) {
   if (__builtin_amdgcn_ballot_w64(used) == 0) {
     finish_unused(a, r, bits, st);
   } else {
-    Sums mine{-FLT_MAX, 0.0, 0.0};
-    if (lane < a.parts) {
-      const double* in = a.part + (r * a.parts + lane) * kPartDoubles;
-      mine.mc = static_cast<float>(in[0]);
-      mine.rest = in[1];
-      mine.named = in[2];
-    }
+    Sums mine;
+    if (lane < a.parts) mine = reinterpret_cast<const Sums*>(a.part)[r * a.parts + lane];
     Sums s;
-    s.mc = wave_all(mine.mc, MaxOp());
-    s.rest = wave_sum_f64(sum_at(mine.rest, mine.mc, s.mc));
-    s.named = wave_sum_f64(sum_at(mine.named, mine.mc, s.mc));
+    s.mr = wave_all(mine.mr, MaxOp());
+    s.xr = wave_all(mine.xr, MaxOp());
+    s.mn = wave_all(mine.mn, MaxOp());
+    s.xn = wave_all(mine.xn, MaxOp());
+    s.rest = wave_sum_f64(sum_at(mine.rest, mine.mr, s.mr));
+    s.named = wave_sum_f64(sum_at(mine.named, mine.mn, s.mn));
     finish_distill<kRest>(a, r, s, t, bits, st);
   }
   lds_barrier();
@@ -481,8 +509,8 @@ __device__ __forceinline__ void grad_range(const DistillArgs& a, int64_t r, int 
   const E* row = static_cast<const E*>(a.x.p) + r * a.x.ld;
   E* out = static_cast<E*>(a.grad) + r * a.grad_ld;
   const int tid = threadIdx.x;
-  const float mc = static_cast<float>(st[0]);
-  const double norm = st[1], scale = st[2], every = st[3], lt = st[4];
+  const float mr = rest_ref(st[0]), mc = row_ref(st[0]);
+  const double norm = st[1], factor = st[2], every = st[3], lt = st[4];
   const double g = (a.weight ? static_cast<double>(a.weight[r]) : 1.0) * a.inv_t;
   if (every == 0.0 || g == 0.0) {
     fill_zero<E, NT>(out, e0, e1);
@@ -505,7 +533,9 @@ __device__ __forceinline__ void grad_range(const DistillArgs& a, int64_t r, int 
     teach[tid] = t;
   }
   lds_barrier();
-  scaled_softmax<E, NT, U>(row, out, e0, e1, a.c, mc, static_cast<float>(norm * scale * g));
+  // (what this leaves at the named ids, which may lie far above the rest, is
+  // written over)
+  scaled_softmax<E, NT, U>(row, out, e0, e1, a.c, mr, static_cast<float>(factor * g));
   __syncthreads();   // the pass's stores come before the named ids' own
   if (id >= e0 && id < e1) {
     double t = 0.0;

@@ -34,12 +34,13 @@ struct DistillArgs {
   int32_t parts;
 };
 
-// What the backward pass needs of a row: the student's exponent reference and
-// one over its sum relative to that, the scale of the unnamed tokens, the
-// teacher's total, and the teacher's log-sum-exp (over the entries where none
-// was given).
+// What the backward pass needs of a row: the student's exponent references of
+// the unnamed tokens and of the whole row (two floats), one over the row's
+// sum relative to its own, the factor of the unnamed tokens relative to
+// theirs, the teacher's total, and the teacher's log-sum-exp (over the
+// entries where none was given).
 constexpr int kStateWords = VSV_DISTILL_STATE;
-constexpr int kPartDoubles = 3;   // exponent reference, sum outside the ids, sum over the ids
+constexpr int kPartDoubles = 4;   // two sums, two exponent references, two maxima (floats)
 
 // Parts a row is cut into, so that a call of few rows still gives every CU
 // something to stream; a function of the call's sizes alone, because the

@@ -51,9 +51,10 @@ def distill_row(y, ids, z, teacher_lse, temperature, weight=1.0):
         total = float(np.sum(t)) + rest
         grad = q * total
         if rest > 0.0:
-            q_rest = float(np.sum(q[~named]))
-            loss += rest * (math.log(rest) - np.log(q_rest))
-            if q_rest > 0.0:
-                grad[~named] -= rest * q[~named] / q_rest
+            # (by logarithms: q_rest may lie far below the smallest float64)
+            log_rest = logsumexp(y[~named], temperature) if np.any(y[~named] > -np.inf) else -np.inf
+            loss += rest * (math.log(rest) - (log_rest - logsumexp(y, temperature)))
+            if log_rest > -np.inf:
+                grad[~named] -= rest * np.exp(y[~named] / temperature - log_rest)
     np.subtract.at(grad, ids, t)
     return loss, weight * grad / temperature

@@ -47,3 +47,68 @@ def test_draws_at_subnormal_temperatures(vsv, dtype, V):
          np.where(np.arange(n) % 3, 0.0, 0.05).astype(np.float32), rng.random(n, dtype=np.float32))
     print("subnormal temperatures V=%d dtype=%d" % (V, dtype), flush=True)
     _check_draws(vsv.sample_rows(to_dev(store), *[to_dev(q) for q in a]), rows_f64(store, dtype, V, 0), *a)
+
+
+# ------------------------------------------------------------- distillation
+
+def _both(vsv, x, ids, z, w, **kw):
+    """(loss, gradient) in one call, and by the two halves."""
+    loss, state = vsv.distill_forward(x, ids, z, **kw)
+    return vsv.distill_loss_grad(x, ids, z, w, **kw), (loss, vsv.distill_backward(w, x, ids, z, state, **kw))
+
+
+def _check_rest(loss, grad, xs, ids, z, lse, T, w, dtype):
+    """As _check_distill of test_gpu_rows.py, for rows whose mass outside the
+    ids may be too small for a float64. With s the softmax over the unnamed
+    tokens alone, their gradient is (M q - t_r s) weight / T, and both terms
+    are exponentials within D, so it is within 4 D (M q + t_r s) weight / T;
+    D counts the largest |x| / T of every token, named or not."""
+    half = {F32: 2.0 ** -24, BF16: 2.0 ** -8}[dtype]
+    for r, x in enumerate(xs):
+        want, g = oracle.distill_row(x, ids[r], z[r].astype(np.float64), float(lse[r]), T, float(w[r]))
+        D = 2.0 ** -22 * (1 + np.abs(x[np.isfinite(x)]).max() / T)
+        if np.isfinite(want):
+            assert abs(loss[r] - want) <= 2 * D + 2.0 ** -24 * abs(want), (r, loss[r], want)
+        else:
+            assert loss[r] == want, (r, loss[r], want)
+        named = np.zeros(x.shape[0], dtype=bool)
+        named[ids[r][ids[r] >= 0]] = True
+        size = np.exp(x / T - oracle.logsumexp(x, T))
+        rest = x[~named]
+        if np.any(rest > -np.inf):
+            t_r = max(0.0, 1 - np.exp(z[r][ids[r] >= 0].astype(np.float64) / T - float(lse[r])).sum())
+            size[~named] += t_r * np.exp(rest / T - oracle.logsumexp(rest, T))
+        tol = (4 * D * size + 2.0 ** -23 * named) * w[r] / T + half * np.abs(g) + 1e-37
+        bad = np.flatnonzero(~(np.abs(grad[r] - g) <= tol))
+        assert bad.size == 0, (r, bad[:5], grad[r][bad[:5]], g[bad[:5]], tol[bad[:5]])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,n", [(4099, 5), (152064, 5), (152064, 130)])
+@pytest.mark.parametrize("T", [0.5, 1.0])
+def test_distill_of_a_student_far_above_the_rest(vsv, dtype, V, n, T):
+    # the named logits lie so far above the others that the mass outside them
+    # leaves the range of a float, then of a double: loss and gradient are
+    # finite all the same. Rows in one workgroup and in parts.
+    import torch
+    gaps, K = (60, 90, 200, 700, 3000), 12
+    m = len(gaps)
+    rng = np.random.default_rng(44)
+    ids = np.stack([rng.permutation(V)[:K] for _ in range(m)]).astype(np.int32)
+    ids[:, 3] = ids[:, 0]                         # (named twice)
+    rows = []
+    for r, gap in enumerate(gaps):
+        x = rng.standard_normal(V).astype(np.float32)
+        x[ids[r]] += np.float32(gap * T)
+        rows.append(x)
+    z = rng.standard_normal((m, K)).astype(np.float32)
+    lse = np.array([oracle.logsumexp(q.astype(np.float64), T) + 0.1 for q in z], dtype=np.float32)
+    w = rng.random(m, dtype=np.float32)
+    store = store_rows(rows, dtype)
+    xs = rows_f64(store, dtype, V, 0)
+    pick = torch.arange(n, device="cuda") % m
+    up = lambda a: to_dev(a)[pick].contiguous()
+    print("far above the rest V=%d n=%d dtype=%d" % (V, n, dtype), flush=True)
+    for loss, grad in _both(vsv, up(store), up(ids), up(z), up(w), teacher_lse=up(lse), temperature=T):
+        _check_rest(host(loss)[:m], host(grad[:m].float()), xs, ids, z, lse, T, w, dtype)
+        assert bool((grad == grad[:m][pick]).all()) and bool((loss == loss[:m][pick]).all())
