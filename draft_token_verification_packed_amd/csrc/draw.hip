@@ -50,9 +50,9 @@ constexpr double kMostPerT = 1024.0;
 constexpr int kList = 4096;        // elements the gathered list holds
 constexpr int kMostParts = 8;
 constexpr int kFew = 128;          // lists decided by direct comparison
-// Sums hold to about 1e-13 of the row's weight (a weight's integer is off by
-// up to half a unit, 2^-45 of it for a vocabulary up to 2^18; the polynomial
-// by 2e-14), so two that differ by less than this share are taken as equal:
+// Sums hold to about 1e-13 of the row's weight (in the bins a weight's integer
+// is off by up to half a unit, 2^-45 of it for a vocabulary up to 2^18 and
+// more for a larger one as its units grow; the polynomial by 2e-14), so two that differ by less than this share are taken as equal:
 // where weights are equal and a border falls exactly between tokens, it is
 // decided as exact sums would.
 constexpr double kEqual = 1.0 / 4398046511104.0;   // 2^-42
@@ -71,11 +71,11 @@ template <int NT> struct DrawLds {
     uint32_t cnt[kBins];       // counts (top-k rows), until the cuts are located
     uint64_t list[kList];      // rank keys of the gathered elements
   } u;
-  ull mass[256];               // radix search
+  ull mass[256], mass_lo[256]; // radix search
   uint32_t num[256];
   double w[kFew];
   int at[kFew];
-  ull red_u[NW];
+  ull red_u[NW], red_v[NW];
   double red_d[NW];
   float red_f[NW];
   int red_i[NW];
@@ -239,11 +239,34 @@ struct WantCode {
 
 // ---------------------------------------------------------------- radix search
 
+// A weight relative to the row's maximum as two integers, in units of one over
+// `one` and 2^-32 of that: sums are exact in any order, and thousands of equal
+// elements far below the maximum, whose roundings all point one way, still
+// hold to 2^-77 of the total each (with the first word alone 150000 of them
+// at z = -15 were off by 2e-9 of it, a hundredth of a token's share).
+struct Mass {
+  ull hi = 0, lo = 0;
+  __device__ __forceinline__ Mass& operator+=(const Mass& o) {
+    hi += o.hi;
+    lo += o.lo;
+    return *this;
+  }
+};
+
 struct Weigh {
   double m, T, one;   // row maximum, temperature, 2^s
   __device__ __forceinline__ double z(float x) const { return (static_cast<double>(x) - m) / T; }
   __device__ __forceinline__ double exact(float x) const { return exp(z(x)); }
-  __device__ __forceinline__ ull operator()(float x) const { return static_cast<ull>(rint(exact(x) * one)); }
+  __device__ __forceinline__ Mass operator()(float x) const {
+    const double v = exact(x) * one, whole = floor(v);
+    Mass w;
+    w.hi = static_cast<ull>(whole);
+    w.lo = static_cast<ull>(rint((v - whole) * 4294967296.0));   // below 2^62 for 2^30 of them
+    return w;
+  }
+  __device__ __forceinline__ double value(const Mass& s) const {
+    return (static_cast<double>(s.hi) + static_cast<double>(s.lo) * (1.0 / 4294967296.0)) / one;
+  }
 };
 
 // A cumulative weight reaches t / exceeds t exactly where it is at least /
@@ -299,7 +322,7 @@ __device__ __forceinline__ uint64_t find_cut(const Each& each, const Weigh& w, c
   any = L.mass[1];
   const ull differ = L.mass[0] ^ any;
   uint64_t prefix = 0;
-  ull mass = 0;
+  Mass mass;
   int num = n0;
 #pragma unroll 1
   for (int shift = 56; shift >= 0; shift -= 8) {
@@ -311,6 +334,7 @@ __device__ __forceinline__ uint64_t find_cut(const Each& each, const Weigh& w, c
     if (tid < kDigits) {
       L.num[tid] = 0;
       L.mass[tid] = 0;
+      L.mass_lo[tid] = 0;
     }
     if (tid == 0) {
       L.digit[0] = kDigits;
@@ -322,20 +346,25 @@ __device__ __forceinline__ uint64_t find_cut(const Each& each, const Weigh& w, c
       if (shift == 56 || (key >> (shift + 8)) == (prefix >> (shift + 8))) {
         const int d = static_cast<int>(key >> shift) & 255;
         atomicAdd(&L.num[d], 1u);
-        atomicAdd(&L.mass[d], w(x));
+        const Mass m = w(x);
+        atomicAdd(&L.mass[d], m.hi);
+        atomicAdd(&L.mass_lo[d], m.lo);
       }
     });
     lds_barrier();
     // thread t holds digit 255 - t; the first that reaches the cut is taken
-    ull dm = 0, im = 0;
+    Mass dm, im;
     int dn = 0, in = 0;
     if (wave < DW) {
-      dm = L.mass[kDigits - 1 - tid];
+      dm.hi = L.mass[kDigits - 1 - tid];
+      dm.lo = L.mass_lo[kDigits - 1 - tid];
       dn = static_cast<int>(L.num[kDigits - 1 - tid]);
-      im = wave_scan_incl(dm);
+      im.hi = wave_scan_incl(dm.hi);
+      im.lo = wave_scan_incl(dm.lo);
       in = wave_scan_incl(dn);
       if (lane == kWave - 1) {
-        L.red_u[wave] = im;
+        L.red_u[wave] = im.hi;
+        L.red_v[wave] = im.lo;
         L.red_i[wave] = in;
       }
     }
@@ -343,12 +372,13 @@ __device__ __forceinline__ uint64_t find_cut(const Each& each, const Weigh& w, c
     if (wave < DW) {
 #pragma unroll
       for (int k = 0; k < DW; ++k) {
-        im += k < wave ? L.red_u[k] : 0ull;
+        im.hi += k < wave ? L.red_u[k] : 0ull;
+        im.lo += k < wave ? L.red_v[k] : 0ull;
         in += k < wave ? L.red_i[k] : 0;
       }
       im += mass;
       in += num;
-      const double cum = w0 + static_cast<double>(im) / w.one;
+      const double cum = w0 + w.value(im);
       const bool done = dn > 0 && (c.count > 0 ? in >= c.count : (c.strict ? cum > c.target : cum >= c.target));
       if (done) atomicMin(&L.digit[0], tid);
       if (dn > 0) atomicMax(&L.digit[1], tid);
@@ -357,14 +387,20 @@ __device__ __forceinline__ uint64_t find_cut(const Each& each, const Weigh& w, c
     const int hit = L.digit[0] < kDigits ? L.digit[0] : L.digit[1];
     if (hit < 0) return 0;   // nothing to search (every thread returns)
     if (tid == hit) {
-      L.red_u[0] = im;
-      L.red_u[1] = im - dm;
+      L.red_u[0] = im.hi;
+      L.red_v[0] = im.lo;
+      L.red_u[1] = im.hi - dm.hi;
+      L.red_v[1] = im.lo - dm.lo;
       L.red_i[0] = in - dn;
       L.red_i[1] = dn;
     }
     lds_barrier();
-    through = w0 + static_cast<double>(L.red_u[0]) / w.one;
-    mass = L.red_u[1];
+    Mass to;
+    to.hi = L.red_u[0];
+    to.lo = L.red_v[0];
+    through = w0 + w.value(to);
+    mass.hi = L.red_u[1];
+    mass.lo = L.red_v[1];
     num = L.red_i[0];
     prefix |= static_cast<uint64_t>(kDigits - 1 - hit) << shift;
     if (shift > 0 && L.red_i[1] == 1) {
@@ -387,14 +423,20 @@ struct Draw {
 };
 
 template <int NT>
-__device__ __forceinline__ ull block_sum(ull v, DrawLds<NT>& L) {
-  v = wave_all(v, SumOp());
+__device__ __forceinline__ Mass block_sum(const Mass& v, DrawLds<NT>& L) {
+  const ull hi = wave_all(v.hi, SumOp()), lo = wave_all(v.lo, SumOp());
   lds_barrier();
-  if ((threadIdx.x & (kWave - 1)) == 0) L.red_u[threadIdx.x / kWave] = v;
+  if ((threadIdx.x & (kWave - 1)) == 0) {
+    L.red_u[threadIdx.x / kWave] = hi;
+    L.red_v[threadIdx.x / kWave] = lo;
+  }
   lds_barrier();
-  ull t = 0;
+  Mass t;
 #pragma unroll
-  for (int w = 0; w < NT / kWave; ++w) t += L.red_u[w];
+  for (int w = 0; w < NT / kWave; ++w) {
+    t.hi += L.red_u[w];
+    t.lo += L.red_v[w];
+  }
   return t;
 }
 
@@ -943,18 +985,20 @@ __device__ __forceinline__ void draw_row(const DrawArgs& a, int64_t r, DrawLds<N
     for (;; list = false) {
       if (!list) {
         top_k = count ? d.top_k : 0;
-        ull mine = 0;
+        Mass mine;
         each([&](float x, int) { mine += w(x); });
-        total = static_cast<double>(block_sum<NT>(mine, L)) / w.one;
+        total = w.value(block_sum<NT>(mine, L));
         left = total;
       }
 #pragma unroll 1
       for (int c = 0; c < 3; ++c) {
         if (c == 2 && d.min_p > 0.f && (!list || jm >= 0)) {
           j = jm;
-          ull kept = 0;
-          each([&](float x, int) { kept += w.z(x) >= zmin ? w(x) : 0ull; });
-          left = fmin(left, (list ? upto(jm - 1) : 0.0) + static_cast<double>(block_sum<NT>(kept, L)) / w.one);
+          Mass kept;
+          each([&](float x, int) {
+            if (w.z(x) >= zmin) kept += w(x);
+          });
+          left = fmin(left, (list ? upto(jm - 1) : 0.0) + w.value(block_sum<NT>(kept, L)));
         }
         if ((c == 0 && !top_k) || (c == 1 && !(d.top_p < 1.f))) continue;
         const double t = c == 1 ? reach(top_p * left) : exceed(u * left);

@@ -257,8 +257,9 @@ vsv_status vsv_draft_confidence(const void* draft_logits, int32_t dtype,
  * lowest-index arg-max), top_k[r], top_p[r] and min_p[r], and the draw is the
  * inverse CDF at uniform[r] in [0, 1): filters, order and draw are those of
  * vsv_verify_sampled, so the same number gives the same token. The sums that
- * decide a cut or a draw hold to about 1e-13 of the row's total; two within
- * 2^-42 of each other count as equal.
+ * decide a cut or a draw hold to about 1e-13 of the row's total for a
+ * vocabulary up to 2^18 (vocab / 2^18 times that beyond it); two within 2^-42
+ * of each other count as equal.
  *   token [num_rows]    the drawn token
  *   logprob [num_rows]  log-probability of the token under the law it was
  *                       drawn from (after temperature and filters; 0 when

@@ -49,6 +49,79 @@ def test_draws_at_subnormal_temperatures(vsv, dtype, V):
     _check_draws(vsv.sample_rows(to_dev(store), *[to_dev(q) for q in a]), rows_f64(store, dtype, V, 0), *a)
 
 
+def _tied_bulk(bulk, z):
+    """(weight of a bulk token, total) of a row with one token at 0, `bulk` at
+    -z and the others at -inf, in 64-bit mantissas."""
+    w = np.exp(-np.longdouble(z))
+    return w, 1 + bulk * w
+
+
+def _rounded(V, bulk, z):
+    """The same with weights rounded to 2^-s, s the most that V of them allow
+    in 62 bits."""
+    s = min(50, 62 - int(V).bit_length())
+    w = np.rint(np.exp(-np.longdouble(z)) * 2.0 ** s) / np.longdouble(2.0 ** s)
+    return w, 1 + bulk * w
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,bulk,z", [(152064, 4000, 18.0), (20000, 19999, 17.0), (70001, 70000, 16.0), (152064, 152063, 12.0), (152064, 152063, 15.0)])
+def test_draws_among_many_equal_tokens_far_below_the_maximum(vsv, dtype, V, bulk, z):
+    # thousands of equal weights round alike, so weights rounded relative to
+    # the row's maximum add up to a neighbouring token towards the end. The
+    # numbers are those where that shows, at least 1e-4 of a token's share
+    # off its borders (sums within 1e-13 of the total are 7e-6 of a share).
+    w, total = _tied_bulk(bulk, z)
+    wr, totalr = _rounded(V, bulk, z)
+    first = int(2 ** 24 / total) + 1
+    u = np.arange(first, 2 ** 24).astype(np.longdouble) / 2 ** 24
+    at = (u * total - 1) / w
+    off = (u * totalr - 1) / wr
+    inside = np.abs(at - np.rint(at)) > 1e-4
+    wrong = np.flatnonzero((np.floor(at) != np.floor(off)) & inside)
+    right = np.flatnonzero((np.floor(at) == np.floor(off)) & inside)
+    rng = np.random.default_rng(12)
+    assert wrong.size >= 3
+    pick = np.concatenate((rng.choice(wrong, min(20, wrong.size), replace=False), rng.choice(right, 4)))
+    n = pick.size
+    row = np.full(V, -np.inf, dtype=np.float32)
+    lead = bulk // 3
+    row[:bulk + 1] = -z
+    row[lead] = 0.0
+    par = [np.full(n, v, dtype=t) for v, t in ((1.0, np.float32), (0, np.int32), (1.0, np.float32), (0.0, np.float32))]
+    print("many equal tokens V=%d bulk=%d z=%g dtype=%d" % (V, bulk, z, dtype), flush=True)
+    out = vsv.sample_rows(to_dev(store_rows([row] * n, dtype)), *[to_dev(q) for q in par],
+                          to_dev(u[pick].astype(np.float32)))
+    rank = np.floor(at[pick]).astype(np.int64)
+    assert np.array_equal(host(out["token"]), rank + (rank >= lead))
+    want = float(-z - np.log(total))
+    assert np.all(np.abs(host(out["logprob"]) - want) <= 2.0 ** -24 * abs(want) + 1e-9)
+    assert np.all(np.abs(host(out["lse"]) - float(np.log(total))) <= 2.0 ** -24 * float(np.log(total)) + 1e-9)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_top_p_among_many_equal_tokens_far_below_the_maximum(vsv, dtype):
+    # where the cut falls shows in the leading token's log-probability: a
+    # token more or less is 3e-7 of it, its rounding 3e-9
+    V, z = 152064, 15.0
+    w, total = _tied_bulk(V - 1, z)
+    wr, totalr = _rounded(V, V - 1, z)
+    p = np.arange(int(2 ** 24 / total) + 1, 2 ** 24).astype(np.longdouble) / 2 ** 24
+    need = (p * total - 1) / w                   # bulk tokens that reach it
+    off = (p * totalr - 1) / wr
+    wrong = np.flatnonzero((np.ceil(need) != np.ceil(off)) & (np.abs(need - np.rint(need)) > 1e-5))
+    pick = np.random.default_rng(13).choice(wrong, 24, replace=False)
+    n = pick.size
+    row = np.full(V, -z, dtype=np.float32)
+    row[7] = 0.0
+    full = lambda v, t: to_dev(np.full(n, v, dtype=t))
+    out = vsv.sample_rows(to_dev(store_rows([row] * n, dtype)), full(1.0, np.float32), full(0, np.int32),
+                          to_dev(p[pick].astype(np.float32)), full(0.0, np.float32), full(0.0, np.float32))
+    assert np.all(host(out["token"]) == 7)
+    want = -np.log(1 + np.ceil(need[pick]) * w).astype(np.float64)
+    assert np.all(np.abs(host(out["logprob"]) - want) <= 2.0 ** -24 * np.abs(want) + 1e-9)
+
+
 # ------------------------------------------------------------- distillation
 
 def _both(vsv, x, ids, z, w, **kw):
