@@ -604,25 +604,37 @@ __device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, con
 struct BinPart {
   double m, top, far;       // maximum, its bin's absolute number, 1 if too far out
   double per;               // bins per T
+  int low, pad;             // the lowest bin below that holds weight
   ull bin[kReach];          // downwards from the part's own top bin
   uint32_t cnt[kReach];
 };
 template <int NT>
-__device__ __forceinline__ void leave_bins(const Binned& b, bool count, BinPart* out, const DrawLds<NT>& L) {
+__device__ __forceinline__ void leave_bins(const Binned& b, bool count, BinPart* out, DrawLds<NT>& L) {
   const bool fine = b.m > -INFINITY && b.m < INFINITY;
   // (a part may lie wholly below the row's bins)
   const int top = fine && !b.far ? Grid::slot(b.g.t(b.m)) : -1;
+  int low = 0;
+  if (top >= 0) {
+    for (int j = threadIdx.x; j < kReach; j += NT) {
+      const ull w = j <= top ? L.bin[top - j] : 0ull;
+      out->bin[j] = w;
+      if (count) out->cnt[j] = j <= top ? L.u.cnt[top - j] : 0u;
+      low = w != 0 ? j : low;
+    }
+    low = wave_all(low, MaxOp());
+    if ((threadIdx.x & (kWave - 1)) == 0) L.red_i[threadIdx.x / kWave] = low;
+    lds_barrier();
+  }
   if (threadIdx.x == 0) {
+    if (top >= 0) {
+#pragma unroll
+      for (int k = 0; k < NT / kWave; ++k) low = max(low, L.red_i[k]);
+    }
     out->m = static_cast<double>(b.m);
     out->top = top < 0 ? -INFINITY : static_cast<double>(top) - (b.g.k - kMagic);
     out->far = fine && b.far ? 1.0 : 0.0;
     out->per = b.g.per;
-  }
-  if (top >= 0) {
-    for (int j = threadIdx.x; j < kReach; j += NT) {
-      out->bin[j] = j <= top ? L.bin[top - j] : 0ull;
-      if (count) out->cnt[j] = j <= top ? L.u.cnt[top - j] : 0u;
-    }
+    out->low = low;
   }
 }
 
@@ -649,6 +661,11 @@ __device__ __forceinline__ Binned join_bins(const BinPart* in, int P, double T, 
   b.g.s = per / T;
   const double top = wave_all(ptop, MaxOp());
   b.far = b.far || !(top > -INFINITY);
+  // The finer grid's bins reach less far down than weight counts. A part makes
+  // sure that they hold what lies within reach of its own maximum, which may
+  // be far below the row's: such a row goes again as one.
+  const int lost = per > kPerT && ptop > -INFINITY && top - ptop + static_cast<double>(mine.low) >= static_cast<double>(kReach);
+  b.far = b.far || wave_all(lost, MaxOp()) != 0;
   if (!(b.m > -INFINITY && b.m < INFINITY) || b.far) return b;
   lds_barrier();
   const double even = 2.0 * floor(0.5 * top);

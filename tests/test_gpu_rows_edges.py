@@ -122,6 +122,48 @@ def test_top_p_among_many_equal_tokens_far_below_the_maximum(vsv, dtype):
     assert np.all(np.abs(host(out["logprob"]) - want) <= 2.0 ** -24 * np.abs(want) + 1e-9)
 
 
+@pytest.mark.parametrize("V", [152064, 70001])
+@pytest.mark.parametrize("rise", [24.1, 24.6, 25.2, 40.0])
+def test_draws_of_a_bulk_far_below_another_parts_maximum(vsv, V, rise):
+    # every part of the row but the last holds a flat bulk, the last one token
+    # `rise` above its middle: the bulk still weighs 4e-6 of it at 24.1, and
+    # numbers close to one draw from it. A bulk token's share is down to 4e-12
+    # there, so sums within 1e-13 of the total tell the tokens apart where a
+    # number lies a tenth of a share off the borders.
+    rng = np.random.default_rng(31)
+    n = 12
+    bulk = V * 7 // 8 if V > 100000 else V // 2
+    rows, want, us = [], [], []
+    for r in range(n):
+        x = np.full(V, -np.inf, dtype=np.float32)
+        x[:bulk] = rng.uniform(-1, 1, bulk)
+        x[V - 1 - r] = np.float32(rise)
+        ids = oracle.rank_order(x.astype(np.float64))[:bulk + 1]
+        xl = x.astype(np.longdouble)
+        w = np.exp(xl[ids] - xl[ids[0]])
+        c = np.cumsum(w)
+        token, u = V - 1 - r, 0.5
+        if r % 4:
+            for i in range(1, 80):
+                t = (1 - np.longdouble(i) / 2 ** 24) * c[-1]
+                k = int(np.searchsorted(c, t, side="right"))
+                if k > 0 and min(t - c[k - 1], c[k] - t) > 0.1 * w[k] and i % 4 == r % 4:
+                    token, u = int(ids[k]), 1 - i * 2.0 ** -24
+                    break
+        rows.append(x)
+        us.append(u)
+        want.append((token, float(xl[token] - xl[ids[0]] - np.log(c[-1])), float(xl[ids[0]] + np.log(c[-1]))))
+    assert rise > 30 or sum(u > 0.6 for u in us) >= 6
+    full = lambda v, t: to_dev(np.full(n, v, dtype=t))
+    out = vsv.sample_rows(to_dev(store_rows(rows, F32)), full(1.0, np.float32), full(0, np.int32), full(1.0, np.float32),
+                          full(0.0, np.float32), to_dev(np.array(us, dtype=np.float32)))
+    tok, lp, lse = host(out["token"]), host(out["logprob"]), host(out["lse"])
+    for r, (t, p, s) in enumerate(want):
+        assert int(tok[r]) == t, (r, us[r], int(tok[r]), t)
+        assert abs(lp[r] - p) <= 2.0 ** -24 * abs(p) + 1e-9, (r, lp[r], p)
+        assert abs(lse[r] - s) <= 2.0 ** -24 * abs(s) + 1e-9, (r, lse[r], s)
+
+
 # ------------------------------------------------------------- distillation
 
 def _both(vsv, x, ids, z, w, **kw):
