@@ -8,7 +8,8 @@
 //   with it (L): t_k = exp(z_k / T - L), what they leave of one,
 //     t_r = max(0, 1 - sum t), is the mass of the rest, set against the
 //     student's mass outside the named ids, q_r:
-//     loss = sum_k t_k (ln t_k - ln q_k) + t_r (ln t_r - ln q_r).
+//     loss = sum_k t_k (ln t_k - ln q_k) + t_r (ln t_r - ln q_r)
+//     (t_r counts as 0 where it is the rounding of L and q_r is nothing).
 // With M = sum t + t_r the gradient of a row's loss is
 //   (q_i M - sum of the t that name i) / T   at a named id,
 //   q_i (M - t_r / q_r) / T                  elsewhere,
@@ -233,6 +234,15 @@ __device__ __forceinline__ double pack_refs(float rest, float row) {
 __device__ __forceinline__ float rest_ref(double s) { return __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, s))); }
 __device__ __forceinline__ float row_ref(double s) { return __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, s) >> 32)); }
 
+// A rest of the teacher counts as none where the student's is below 2^-126
+// (ln of it) and it is no more than the float32 log-sum-exp, of float32
+// exponentials, may be off by: those and the terms' arguments are within
+// 2^-22 (1 + |x| / T) together, the result is rounded by 2^-24 of itself, and
+// |x| / T is |lse| but for the few T over which weight spreads. Where the
+// student's rest is larger, such a t_r adds less than 1e-4 and is kept.
+constexpr double kNoRest = -87.33654475055310;
+constexpr double kLseRounding = 1.0 / 1048576.0;   // 2^-20
+
 constexpr double kLn2 = 0.69314718055994530942;
 
 // x c as the terms took it, above their reference m.
@@ -286,7 +296,6 @@ __device__ __forceinline__ void finish_distill(const DistillArgs& a, int64_t r, 
   if (kRest) {
     const double tr = 1.0 - mass;
     if (tr > 0.0) {
-      every += tr;
       const float xm = fmaxf(s.xr, s.xn);
       // ln q_r by way of the two largest elements, whose difference may be
       // most of it: in float64, where x c is rounded
@@ -294,8 +303,13 @@ __device__ __forceinline__ void finish_distill(const DistillArgs& a, int64_t r, 
                                           : (static_cast<double>(s.xr) - static_cast<double>(xm)) * a.inv_t +
                                                 kLn2 * ((log2(s.rest) - above_ref(s.xr, a.c, s.mr)) -
                                                         (lg - above_ref(xm, a.c, mc)));
-      loss += tr * (log(tr) - log_qr);
-      off = s.rest == 0.0 ? 0.0 : tr / s.rest;
+      // of a teacher whose entries hold all of its mass, as where a vocabulary
+      // mask leaves no others, its float32 log-sum-exp leaves a rounding
+      if (!(log_qr < kNoRest && tr <= kLseRounding * (1.0 + fabs(lt)))) {
+        every += tr;
+        loss += tr * (log(tr) - log_qr);
+        off = s.rest == 0.0 ? 0.0 : tr / s.rest;
+      }
     }
   }
   if (!(total > 0.0 && total < INFINITY) || !(mass < INFINITY)) bits |= VSV_FLAG_LOGITS;

@@ -311,8 +311,11 @@ vsv_status vsv_top_logits(const void* logits, int32_t dtype, int32_t vocab, int6
  *                      one, t_r = max(0, 1 - sum t), stands against the
  *                      student's mass q_r outside the row's ids:
  *                      loss = sum_k t_k (ln t_k - ln q_k) + t_r (ln t_r - ln q_r)
- * (the Kullback-Leibler divergence, no factor T^2). Entries of weight 0 add
- * nothing. A row without a used entry has loss 0 and gradient 0 and its
+ * (the Kullback-Leibler divergence, no factor T^2). Where q_r is below 2^-126
+ * (a vocabulary mask that leaves only named tokens), a t_r up to
+ * 2^-20 (1 + |teacher_lse|) is the rounding of teacher_lse and counts as 0.
+ * Logits whose x / T is below the range of float32 count as -inf. Entries of
+ * weight 0 add nothing. A row without a used entry has loss 0 and gradient 0 and its
  * logits are not read. */
 typedef struct {
   const void* logits;       /* [num_rows, ld] the student's rows                */

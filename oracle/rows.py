@@ -32,7 +32,8 @@ def top_row(x, k, temperature=1.0):
 def distill_row(y, ids, z, teacher_lse, temperature, weight=1.0):
     """(loss, weight * gradient in y) of one student row against entries
     (ids, z); negative ids are unused, teacher_lse None renormalises the
-    teacher over its entries."""
+    teacher over its entries. A rest of the teacher within the rounding of a
+    float32 teacher_lse counts as none where the student's is below 2^-126."""
     ids, z = np.asarray(ids), np.asarray(z, dtype=np.float64)
     used = ids >= 0
     grad = np.zeros(y.shape[0])
@@ -48,12 +49,15 @@ def distill_row(y, ids, z, teacher_lse, temperature, weight=1.0):
         named = np.zeros(y.shape[0], dtype=bool)
         named[ids] = True
         rest = 0.0 if teacher_lse is None else max(0.0, 1.0 - float(np.sum(t)))
+        # (by logarithms: q_rest may lie far below the smallest float64)
+        log_rest = logsumexp(y[~named], temperature) if np.any(y[~named] > -np.inf) else -np.inf
+        log_q_rest = log_rest - logsumexp(y, temperature)
+        if log_q_rest < -126 * math.log(2) and rest <= 2.0 ** -20 * (1 + abs(teacher_lse or 0.0)):
+            rest = 0.0                           # the rounding of a float32 teacher_lse
         total = float(np.sum(t)) + rest
         grad = q * total
         if rest > 0.0:
-            # (by logarithms: q_rest may lie far below the smallest float64)
-            log_rest = logsumexp(y[~named], temperature) if np.any(y[~named] > -np.inf) else -np.inf
-            loss += rest * (math.log(rest) - (log_rest - logsumexp(y, temperature)))
+            loss += rest * (math.log(rest) - log_q_rest)
             if log_rest > -np.inf:
                 grad[~named] -= rest * np.exp(y[~named] / temperature - log_rest)
     np.subtract.at(grad, ids, t)

@@ -227,3 +227,38 @@ def test_distill_of_a_student_far_above_the_rest(vsv, dtype, V, n, T):
     for loss, grad in _both(vsv, up(store), up(ids), up(z), up(w), teacher_lse=up(lse), temperature=T):
         _check_rest(host(loss)[:m], host(grad[:m].float()), xs, ids, z, lse, T, w, dtype)
         assert bool((grad == grad[:m][pick]).all()) and bool((loss == loss[:m][pick]).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("mask", ["inf", "lowest"])
+@pytest.mark.parametrize("V,left,K,T", [(64, 64, 64, 1.0), (4099, 50, 64, 1.0), (4099, 256, 256, 0.7), (4099, 1, 8, 1.0),
+                                        (152064, 90, 100, 2.0)])
+def test_distill_on_a_masked_vocabulary(vsv, dtype, mask, V, left, K, T):
+    # top_logits into distill_loss where a mask leaves at most K tokens, on
+    # both sides: what float32 leaves of one is no mass to hold against the
+    # student, so a student like the teacher has next to no loss
+    from tests.row_cases import LOWEST
+    rng = np.random.default_rng(V + left)
+    n = 16
+    rows = []
+    for r in range(n):
+        x = np.full(V, -np.inf if mask == "inf" else LOWEST[dtype], dtype=np.float32)
+        x[rng.permutation(V)[:left]] = rng.standard_normal(left) * 3 + rng.uniform(-30, 30)
+        rows.append(x)
+    store = store_rows(rows, dtype)
+    x, xs = to_dev(store), rows_f64(store, dtype, V, 0)
+    top = vsv.top_logits(x, K, temperature=T)
+    args = (x, top["ids"], top["values"])
+    w = np.ones(n, dtype=np.float32)
+    print("masked V=%d left=%d dtype=%d" % (V, left, dtype), flush=True)
+    ids, z, lse = host(top["ids"]), host(top["values"]), host(top["lse"])
+    for loss, grad in _both(vsv, *args, to_dev(w), teacher_lse=top["lse"], temperature=T):
+        loss, grad = host(loss), host(grad.float())
+        for r in range(n):
+            want, g = oracle.distill_row(xs[r], ids[r], z[r].astype(np.float64), float(lse[r]), T)
+            # logits that hold weight lie within 43 of zero; the teacher's
+            # log-sum-exp is off by D too
+            D = 2.0 ** -22 * (1 + 43 / T)
+            assert abs(want) <= 3 * D and abs(loss[r] - want) <= 2 * D, (r, loss[r], want)
+            assert np.all(np.abs(grad[r] - g) <= 4 * D / T + 2.0 ** -8 * np.abs(g)), r
+            assert np.all(np.abs(grad[r]) <= 8 * D / T), r

@@ -69,3 +69,24 @@ def test_distill_gradient_by_differences(rest, repeat):
         dn[i] -= h
         d = 0.5 * (oracle.distill_row(up, ids, z, lse, T)[0] - oracle.distill_row(dn, ids, z, lse, T)[0]) / (2 * h)
         assert abs(d - g[i]) < 1e-9      # h^2 of a smooth function of order 1, and 1e-16 / h
+
+
+def test_distill_rest_that_is_a_rounding():
+    # a mask that leaves only named tokens, on both sides: the float32
+    # log-sum-exp leaves a rest of 1e-7, which is no mass without a student
+    z = np.array([1.0, 0.25, -0.5])
+    y = np.concatenate((z, np.full(5, -np.inf)))
+    for mask in (-np.inf, float(np.finfo(np.float32).min)):
+        y[3:] = mask
+        loss, g = oracle.distill_row(y, [0, 1, 2], z, oracle.logsumexp(z) + 1e-7, 1.0)
+        assert abs(loss) < 2e-7 and np.all(np.abs(g) < 2e-7)
+    # a rest that is more than that stays: against nothing it is infinite
+    assert oracle.distill_row(y, [0, 1], z[:2], oracle.logsumexp(z), 1.0)[0] < 10.0     # token 2 is outside
+    y[3:] = -np.inf
+    assert oracle.distill_row(y, [0, 1, 2], z, oracle.logsumexp(z) + 1e-3, 1.0)[0] == np.inf
+    # and one within it counts where the student has a rest
+    y[3:] = -20.0
+    loss, _ = oracle.distill_row(y, [0, 1, 2], z, oracle.logsumexp(z) + 1e-7, 1.0)
+    q = 5 * math.exp(-20.0 - oracle.logsumexp(y))
+    want = -1e-7 - math.log1p(-q) + 1e-7 * (math.log(1e-7) - math.log(q))
+    assert abs(loss - want) < 1e-12
