@@ -671,9 +671,12 @@ def distill_loss(student_logits, teacher_ids, teacher_logits, teacher_lse=None, 
     log-sum-exp at the same temperature) the rest of its mass is set against
     the student's mass outside the row's ids. Losses are float32 [N]; runs on
     the current stream, its backward on the same one. The teacher gets no
-    gradient. Columns at or beyond `vocab` are not part of the rows. A step
+    gradient, and a student that carries a forward-mode tangent is refused.
+    Columns at or beyond `vocab` are not part of the rows. A step
     captured into a graph needs leaves of its own (made for the capture, or
     without a live eager graph), as any torch backward pass does."""
+    if torch.autograd.forward_ad.unpack_dual(student_logits).tangent is not None:
+        raise NotImplementedError("distill_loss has no forward-mode derivative")
     if vocab is not None and int(vocab) != student_logits.shape[1]:
         if not 1 <= int(vocab) <= student_logits.shape[1]:
             raise ValueError("vocab exceeds the logits width")

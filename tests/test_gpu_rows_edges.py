@@ -262,3 +262,16 @@ def test_distill_on_a_masked_vocabulary(vsv, dtype, mask, V, left, K, T):
             assert abs(want) <= 3 * D and abs(loss[r] - want) <= 2 * D, (r, loss[r], want)
             assert np.all(np.abs(grad[r] - g) <= 4 * D / T + 2.0 ** -8 * np.abs(g)), r
             assert np.all(np.abs(grad[r]) <= 8 * D / T), r
+
+
+def test_distill_refuses_forward_mode(vsv):
+    import torch
+    import torch.autograd.forward_ad as fw
+    x = torch.randn(3, 50, device="cuda")
+    ids = torch.tensor([[1, 4]] * 3, dtype=torch.int32, device="cuda")
+    z = torch.zeros(3, 2, device="cuda")
+    want = vsv.distill_loss(x, ids, z)
+    with fw.dual_level():
+        with pytest.raises(NotImplementedError):
+            vsv.distill_loss(fw.make_dual(x, torch.ones_like(x)), ids, z)
+        assert torch.equal(vsv.distill_loss(x, ids, z), want)
