@@ -149,6 +149,14 @@ __device__ __forceinline__ void load_entries(const DistillArgs& a, int64_t r, co
   }
 }
 
+// Whether any of a wave's entries is used.
+__device__ __forceinline__ bool any_used(const Entries& t) {
+  bool used = false;
+#pragma unroll
+  for (int j = 0; j < kEntries; ++j) used |= t.id[j] >= 0;
+  return __builtin_amdgcn_ballot_w64(used) != 0;
+}
+
 // The sums of elements [e0, e1) of a row over the whole workgroup. With
 // kRest the named elements' weights are kept apart, each id counted once; the
 // wave that handles the entries receives those.
@@ -347,10 +355,7 @@ __device__ __forceinline__ bool row_state(const DistillArgs& a, int64_t r, Disti
   int bits = 0;
   if (wave == 0) {
     load_entries<E>(a, r, row, t, bits);
-    bool used = false;
-#pragma unroll
-    for (int j = 0; j < kEntries; ++j) used |= t.id[j] >= 0;
-    const bool any = __builtin_amdgcn_ballot_w64(used) != 0;
+    const bool any = any_used(t);
     if (threadIdx.x == 0) L.any = any;
     if (!any) finish_unused(a, r, bits, L.row);
   } else {
@@ -390,6 +395,8 @@ __global__ __launch_bounds__(NT) void distill_part_kernel(DistillArgs a) {
   int bits = 0;
   if (threadIdx.x < kWave) {
     load_entries<E>(a, r, row, t, bits);
+    const bool any = any_used(t);
+    if (threadIdx.x == 0) L.any = any;
   } else {
 #pragma unroll
     for (int j = 0; j < kEntries; ++j) {
@@ -397,6 +404,8 @@ __global__ __launch_bounds__(NT) void distill_part_kernel(DistillArgs a) {
       t.first[j] = false;
     }
   }
+  lds_barrier();
+  if (!L.any) return;   // the join finds the same and reads no sums
   const Sums s = range_sums<E, NT, U, kRest, kLoadStream>(a, row, e0, e1, t, L);
   if (threadIdx.x == 0) {
     reinterpret_cast<Sums*>(a.part)[blockIdx.x] = s;
@@ -412,10 +421,7 @@ __global__ __launch_bounds__(kWave) void distill_join_kernel(DistillArgs a) {
   Entries t;
   int bits = 0;
   load_entries<E>(a, r, row, t, bits);
-  bool used = false;
-#pragma unroll
-  for (int j = 0; j < kEntries; ++j) used |= t.id[j] >= 0;
-  if (__builtin_amdgcn_ballot_w64(used) == 0) {
+  if (!any_used(t)) {
     finish_unused(a, r, bits, st);
   } else {
     Sums mine;

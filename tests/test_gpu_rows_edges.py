@@ -275,3 +275,31 @@ def test_distill_refuses_forward_mode(vsv):
         with pytest.raises(NotImplementedError):
             vsv.distill_loss(fw.make_dual(x, torch.ones_like(x)), ids, z)
         assert torch.equal(vsv.distill_loss(x, ids, z), want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_without_entries_are_not_read_in_parts(vsv, dtype):
+    # few long rows are summed in parts, which leave their sums in the
+    # scratch: nothing is left for a row without a used entry
+    import ctypes
+    import torch
+    n, V, K = 5, 152064, 6
+    x = torch.randn(n, V, device="cuda").to(torch.bfloat16 if dtype == BF16 else torch.float32)
+    ids = torch.randint(0, V, (n, K), dtype=torch.int32, device="cuda")
+    ids[1], ids[4], ids[2, 1:] = -1, -7, -1
+    z, lse = torch.randn(n, K, device="cuda"), torch.full((n,), 3.0, device="cuda")
+    L = vsv.lib()
+    need = L.vsv_distill_workspace_bytes(n, V, dtype)
+    assert need > 0
+    for teacher_lse in (None, lse):
+        ws = torch.full((need // 8,), 77.0, dtype=torch.float64, device="cuda")
+        loss = torch.full((n,), 77.0, device="cuda")
+        d = vsv.Distill(x.data_ptr(), dtype, V, V, n, K, ids.data_ptr(), z.data_ptr(),
+                        None if teacher_lse is None else lse.data_ptr(), 1.0)
+        assert L.vsv_distill_forward(ctypes.byref(d), loss.data_ptr(), None, None, ws.data_ptr(), need,
+                                     torch.cuda.current_stream().cuda_stream) == 0
+        per = (need // 8 - n * vsv.DISTILL_STATE) // n
+        left = host((ws[:n * per].view(n, per) == 77).all(1))
+        assert left.tolist() == [False, True, False, False, True]
+        assert torch.equal(loss, vsv.distill_loss(x, ids, z, teacher_lse))
+        assert float(loss[1]) == 0 and float(loss[4]) == 0 and bool((loss[[0, 2, 3]] != 77).all())
