@@ -487,7 +487,8 @@ def _new_flag(device, raw_stream):
     block, count = _flag_words.get(key, (None, None))
     i = next(count) if block is not None else _FLAG_BLOCK
     if i >= _FLAG_BLOCK:
-        block, count = torch.zeros(_FLAG_BLOCK, dtype=torch.int32, device=device), itertools.count()
+        with torch.inference_mode(False):   # later calls may not be in the mode of this one
+            block, count = torch.zeros(_FLAG_BLOCK, dtype=torch.int32, device=device), itertools.count()
         i = next(count)
         _flag_words[key] = (block, count)
     return block[i:i + 1]

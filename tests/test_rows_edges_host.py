@@ -19,3 +19,20 @@ def test_forward_mode_is_refused():
                 vsv.distill_loss(student, i, f, vocab=15)
         with pytest.raises(ValueError):          # a plain host tensor: refused as that
             vsv.distill_loss(x, i, f)
+
+
+def test_error_words_outlive_inference_mode(monkeypatch):
+    # words are cut from a block that many calls share: one made under
+    # inference mode would be refused in place by a later caller outside it
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(vsv, "_flag_words", {})
+    cpu = torch.device("cpu")
+    with torch.inference_mode():
+        first = vsv._new_flag(cpu, 0)
+        first.zero_()
+    word = vsv._new_flag(cpu, 0)
+    assert word.data_ptr() == first.data_ptr() + 4
+    assert not word.is_inference()
+    word.fill_(3)
+    first.zero_()
+    assert int(word) == 3 and int(first) == 0
