@@ -97,11 +97,20 @@ bool rows_ok(const void* p, int32_t dtype, int32_t vocab, int64_t ld, int32_t ro
   return p && aligned(p, elem_size(dtype)) && ld <= (INT64_MAX / 4) / rows;
 }
 
+// log2(e) / T as the kernels take it, false unless T and it are positive and
+// finite (it is infinite for T below 4.24e-39, where 0 / T would be NaN).
+bool exponent_scale(float temperature, float* c) {
+  if (!(temperature > 0.f) || !(temperature < INFINITY)) return false;
+  *c = static_cast<float>(1.44269504088896340736 / static_cast<double>(temperature));
+  return *c < INFINITY;
+}
+
 // Checks of a distillation's inputs; fills the shared launch args. The
 // caller has dealt with num_rows == 0.
 vsv_status prepare_distill(const vsv_distill* d, vsv::DistillArgs* a) {
   if (d->num_top < 1 || d->num_top > VSV_MAX_TOP || !d->ids || !d->top) return VSV_EINVAL;
-  if (!(d->temperature > 0.f) || !(d->temperature < INFINITY)) return VSV_EINVAL;
+  float c;
+  if (!exponent_scale(d->temperature, &c)) return VSV_EINVAL;
   if (!rows_ok(d->logits, d->dtype, d->vocab, d->ld, d->num_rows)) return VSV_EINVAL;
   *a = vsv::DistillArgs{};
   a->x = vsv::RowsIn{d->logits, d->ld, d->vocab, d->num_rows, d->dtype};
@@ -109,7 +118,7 @@ vsv_status prepare_distill(const vsv_distill* d, vsv::DistillArgs* a) {
   a->top = d->top;
   a->tlse = d->teacher_lse;
   a->K = d->num_top;
-  a->c = static_cast<float>(1.44269504088896340736 / static_cast<double>(d->temperature));
+  a->c = c;
   a->inv_t = 1.0 / static_cast<double>(d->temperature);
   a->parts = vsv::distill_parts(d->num_rows, d->vocab, d->dtype);
   return VSV_OK;
@@ -267,14 +276,13 @@ vsv_status vsv_top_logits(const void* logits, int32_t dtype, int32_t vocab, int6
   if (num_rows == 0) return VSV_OK;
   if (!rows_ok(logits, dtype, vocab, ld, num_rows) || !values || !ids) return VSV_EINVAL;
   if (k < 1 || k > VSV_MAX_TOP || k > vocab) return VSV_EINVAL;
-  if (!(temperature > 0.f) || !(temperature < INFINITY)) return VSV_EINVAL;
+  float c;
+  if (!exponent_scale(temperature, &c)) return VSV_EINVAL;
   const int32_t parts = vsv::top_parts(num_rows, vocab, dtype, k);
   if (parts > 1 && (!workspace || !aligned(workspace, 16) ||
                     workspace_bytes < vsv_top_workspace_bytes(num_rows, vocab, dtype, k)))
     return VSV_EWORKSPACE;
-  const vsv::TopArgs a{{logits, ld, vocab, num_rows, dtype}, k,
-                       static_cast<float>(1.44269504088896340736 / static_cast<double>(temperature)),
-                       values, ids, lse, error_flag, workspace, parts};
+  const vsv::TopArgs a{{logits, ld, vocab, num_rows, dtype}, k, c, values, ids, lse, error_flag, workspace, parts};
   return vsv::launch_top(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 

@@ -294,7 +294,8 @@ vsv_status vsv_sample_rows(const void* logits, int32_t dtype, int32_t vocab, int
  * inside the row). `workspace`: scratch of vsv_top_workspace_bytes bytes, as in
  * vsv_sample_rows.
  * Errors: VSV_EINVAL (num_rows < 0, NULL logits, values or ids, k outside
- * 1 .. min(vocab, VSV_MAX_TOP), temperature not positive and finite, vocab,
+ * 1 .. min(vocab, VSV_MAX_TOP), temperature not positive and finite or
+ * log2(e) / temperature beyond float32 (below 4.24e-39), vocab,
  * ld, alignment and dtype as above), VSV_EWORKSPACE, VSV_EHIP. */
 #define VSV_MAX_TOP 256
 size_t vsv_top_workspace_bytes(int32_t num_rows, int32_t vocab, int32_t dtype, int32_t k);
@@ -328,7 +329,7 @@ typedef struct {
   const float* top;         /* [num_rows, num_top] teacher's logits             */
   const float* teacher_lse; /* [num_rows] log-sum-exp of the teacher's whole    */
                             /* row / T, or NULL                                 */
-  float temperature;        /* T, positive and finite                           */
+  float temperature;        /* T, positive and finite, log2(e) / T too          */
 } vsv_distill;
 
 /* Bytes of scratch that vsv_distill_forward and vsv_distill_grad need (0 for

@@ -36,3 +36,18 @@ def test_error_words_outlive_inference_mode(monkeypatch):
     word.fill_(3)
     first.zero_()
     assert int(word) == 3 and int(first) == 0
+
+
+@pytest.mark.parametrize("T", [1.4e-45, 1e-40, 4.2e-39])
+def test_temperatures_without_a_reciprocal_are_refused(T):
+    # log2(e) / T is beyond float32 there, and 0 / T would come out as NaN
+    import ctypes
+    import os
+    if not os.path.exists(vsv.LIB_PATH):
+        pytest.skip("library not built (run the package build first)")
+    L, P = vsv.lib(), ctypes.c_void_p
+    assert L.vsv_top_logits(P(0x10000), 1, 1024, 1024, 4, 8, T, P(8), P(8), None, None, None, 0, None) == 1
+    d = vsv.Distill(0x10000, 1, 1024, 1024, 4, 8, 8, 8, None, T)
+    assert L.vsv_distill_forward(ctypes.byref(d), P(8), None, None, None, 0, None) == 1
+    assert L.vsv_distill_backward(ctypes.byref(d), P(8), None, P(0x20000), 1024, None) == 1
+    assert L.vsv_distill_grad(ctypes.byref(d), None, P(8), P(0x20000), 1024, None, None, 0, None) == 1
