@@ -26,6 +26,10 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
 # the sampled kernel no longer fits two workgroups per CU while the
 # probabilistic one spills 23 VGPRs (48 instead of 144 bytes of scratch per
 # lane without it; 581 instead of 609 us on the mixed B=512, K=7 batch).
+# The draws' kernels hold several searches one after another, whose constants
+# are hoisted to the kernel's start the same way: 18 to 60 VGPRs spill with it
+# and none without (512 bf16 rows with top-p 58 instead of 61.5 us, 128 fp32
+# rows with every filter 53 instead of 56).
 _NO_LICM = ["-mllvm", "-disable-machine-licm"]
 SOURCE_FLAGS = {"sampled.hip": _NO_LICM, "probabilistic.hip": _NO_LICM, "draw.hip": _NO_LICM}
 

@@ -634,13 +634,17 @@ hipError_t grad_t(const DistillArgs& a, hipStream_t s) {
 int32_t distill_parts(int32_t num_rows, int32_t vocab, int32_t dtype) {
   const int64_t bytes = static_cast<int64_t>(vocab) * (dtype == VSV_BF16 ? 2 : 4);
   const int64_t n = num_rows > 0 ? num_rows : 1;
-  // Rows are cut while whole rows would leave CUs idle. From 128 rows on a
-  // workgroup per row is the better use, since it needs no second launch and
-  // its gradient follows the sums in the same one: 160 bf16 rows of 152064
-  // take 14.6 us forward and 33.6 with the gradient, against 16.0 and 40.7 in
-  // three parts; 64 of them take 11.8 and 25.5 in parts, 13.0 and 30.6 whole.
-  // Short rows are not worth the second launch: 128 fp32 rows of 32768 take
-  // 8.8 us whole and 10.7 in two parts.
+  // Rows are cut while whole rows would leave CUs idle, up to 96 of them: 64
+  // bf16 rows of 152064 take 28 us with the gradient in three parts, 31 whole
+  // (calls back to back). From 97 rows on a workgroup per row is the better
+  // use, since it needs no second launch and its gradient follows the sums in
+  // the same one: 112 bf16 rows take 17.1 us forward and 33.5 with the
+  // gradient, against 15.9 and 36.2 in two parts. (fp32 rows, twice as long,
+  // would still gain from two: 26 and 62 us against 20 and 54.) Short rows
+  // are not worth the second launch: 128 fp32 rows of 32768 take 8.8 us whole
+  // and 10.7 in two parts. The gradient's own pass takes the forward's parts,
+  // though for itself it could take more: those 128 rows leave half of the
+  // CUs without any, 13 us of which 6.5 are the bytes.
   if (bytes < 196608) return 1;
   int64_t p = 192 / n;
   const int64_t most = bytes / 49152;

@@ -16,8 +16,8 @@
 // float32: the row is streamed once. With y = per x / T, an element falls into
 // bin rint(y), and its weight relative to the bin's centre, exp((y - rint(y))
 // / per) by a polynomial in float64, is added to the bin as an integer (2^44
-// to one for a vocabulary up to 2^18) by one LDS atomic. With the widest grid,
-// per = 32, bins reach from 48 T below the first group's maximum to 80 T above
+// to one for a vocabulary up to 2^18) by one LDS atomic. With per = 32 (64 for
+// flat rows) bins reach from 48 T below the first group's maximum to 80 T above
 // it; lower elements weigh less than e^-48 and move no cut. A scan over the
 // bins below the maximum turns them into cumulative weights, and each cut and
 // the draw are known to within a bin or two (a cut inside a bin leaves the
@@ -25,11 +25,11 @@
 // the elements of those bins, and the exact order among them decides. The
 // float64 work (18 issue slots an element) and the atomics (16 us a row of
 // 152064 and CU, 28 with the counts of a top-k row) bound the stream beside
-// the HBM share of 26 us: 128 rows with every filter take 56 us. Per-element
+// the HBM share of 26 us: 128 rows with every filter take 54 us. Per-element
 // LDS sums in float would be as many atomics and 1e-7; moments per bin more.
 //
 // bfloat16: a count per 16-bit code, see CodeLds: 512 rows of 152064 with
-// top-p take 59 us, of which the counting is 26 and the search for the drawn
+// top-p take 58 us, of which the counting is 26 and the search for the drawn
 // element, which reads the row again, 13.
 //
 // Rows neither can serve (too many equal elements at a cut for the list,
@@ -45,8 +45,8 @@ namespace {
 constexpr int kDrawThreads = 512;
 constexpr int kDrawUnroll = 2;
 constexpr int kGatherUnroll = 4;   // the second readings, which do less per vector
-constexpr double kPerT = 32.0;     // bins per T, at least
-constexpr double kMostPerT = 1024.0;
+constexpr double kPerT = 32.0;     // bins per T
+constexpr double kFinePerT = 64.0; // of rows whose bulk spans little
 constexpr int kList = 4096;        // elements the gathered list holds
 constexpr int kMostParts = 8;
 constexpr int kFew = 128;          // lists decided by direct comparison
@@ -473,9 +473,10 @@ struct Binned {
 // Elements [0, V) at `row` into L.bin (and L.u.cnt), by the whole workgroup.
 // The grid goes by the first group of `sample` (the row, of `sampled`
 // elements, that the range belongs to): its maximum, and how far its other
-// elements lie below. The flatter the row, the more bins per T, so that a bin
-// of a bulk of near equals still holds few; a row the grid then misses
-// something of goes again on the widest grid.
+// elements lie below. A row that spans less than 7 T there gets twice the
+// bins per T, so that a bin of its bulk holds half as many; a row the finer
+// grid then misses something of goes again on the wider one. (Finer still
+// would leave no room for a rise of 12 T above the sample's maximum.)
 template <typename E, int NT, int U>
 __device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, const E* __restrict__ sample, int sampled,
                                            double T, double one, bool count, DrawLds<NT>& L) {
@@ -543,7 +544,7 @@ __device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, con
         // half as much again as the sample spans, and 12 T of rise above it,
         // in kReach bins
         const double span = (static_cast<double>(ref) - least) / T * 1.5 + 12.0;
-        while (per < kMostPerT && 2.0 * per * span <= kReach - 100) per *= 2.0;
+        if (kFinePerT * span <= kReach - 100) per = kFinePerT;
       } else {
         lds_barrier();
       }
@@ -563,7 +564,7 @@ __device__ __forceinline__ Binned row_bins(const E* __restrict__ row, int V, con
 #pragma unroll
     for (int k = 1; k < NW; ++k) m = __builtin_elementwise_maximum(m, L.red_f[k]);
     // bins further below the maximum than will be looked at have to be empty,
-    // unless the grid is the widest, where they weigh nothing
+    // unless the grid is the wider, where they weigh nothing
     missed = L.n != 0;
     if (per > kPerT && m > -INFINITY && m < INFINITY && !far) {
       const int top = Grid::slot(g.t(m));
