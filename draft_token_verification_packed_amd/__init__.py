@@ -10,6 +10,7 @@ Entry points mirror the C ABI in include/vspec_verify.h:
     verify_greedy_relaxed(logits, row_offsets, row_owner, draft_tokens, topk=1, margin=0.0,
                           from_position=0, after_tokens=0, generated=None, protected_ids=None)
     verify_greedy_static(logits, row_offsets, row_owner, draft_tokens, relaxed_topk=1)
+    verify_greedy_tree(logits, row_offsets, row_owner, draft_tokens, parents)
     verify_sampled(logits, row_offsets, row_owner, draft_tokens,
                    temperature, top_k, top_p, min_p, seed, offset=0)
     draft_confidence(draft_logits, selected=None)
@@ -19,6 +20,8 @@ Entry points mirror the C ABI in include/vspec_verify.h:
     distill_loss_grad(student_logits, teacher_ids, teacher_logits, row_weight=None, teacher_lse=None, temperature=1.0)
     distill_forward / distill_backward: the two halves of distill_loss
     allocate_verify(confidence, draft_tokens, num_requests, num_drafts, row_budget)
+    adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None, ...)
+    plan_pages(block_table, held, length, row_offsets, free_pages, free_count, page_size, num_rows)
     Goodput(max_steps, window_size=20, update_interval=5, switch_min_gain=0.05)
         .observe(accepted_len, verify_len), .step(cost_ms, batch_size)   (host)
     goodput_select(prefix_acceptance, cost_ms, batch_size, current, switch_min_gain)
@@ -38,6 +41,7 @@ FLAG_LAYOUT = 1
 FLAG_TOKEN = 2
 FLAG_LOGITS = 4
 FLAG_PARAMS = 8
+FLAG_PAGES = 32
 
 _STATUS = {0: "VSV_OK", 1: "VSV_EINVAL", 2: "VSV_EUNSUPPORTED", 3: "VSV_EWORKSPACE", 4: "VSV_EHIP",
            5: "VSV_ELIMIT"}
@@ -78,12 +82,26 @@ class Distill(ctypes.Structure):
                 ("temperature", ctypes.c_float)]
 
 
+class Adjust(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("ld", ctypes.c_int64), ("out_ld", ctypes.c_int64),
+                ("num_requests", ctypes.c_int32), ("num_rows", ctypes.c_int32), ("row_offsets", ctypes.c_void_p),
+                ("draft_tokens", ctypes.c_void_p), ("parents", ctypes.c_void_p), ("history", ctypes.c_void_p),
+                ("history_ld", ctypes.c_int64), ("history_width", ctypes.c_int32), ("prompt_len", ctypes.c_void_p),
+                ("history_len", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_offsets", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("num_bias", ctypes.c_int32), ("mask", ctypes.c_void_p),
+                ("mask_ld", ctypes.c_int64), ("num_masks", ctypes.c_int32), ("mask_index", ctypes.c_void_p)]
+
+
 MAX_PROTECTED = 256
+MAX_TREE_ROWS = 64
+MAX_PLAN_REQUESTS = 8192
 MAX_TOP = 256
 DISTILL_STATE = 5
 
 SYMBOLS = ("vsv_workspace_bytes", "vsv_workspace_init", "vsv_verify_greedy", "vsv_verify_greedy_relaxed",
-           "vsv_verify_greedy_static",
+           "vsv_verify_greedy_static", "vsv_verify_greedy_tree", "vsv_adjust_logits", "vsv_plan_pages",
            "vsv_verify_sampled",
            "vsv_verify_probabilistic", "vsv_draft_confidence", "vsv_sample_workspace_bytes", "vsv_sample_rows",
            "vsv_top_workspace_bytes", "vsv_top_logits",
@@ -127,6 +145,12 @@ def lib():
     L.vsv_verify_greedy_relaxed.restype = ctypes.c_int
     L.vsv_verify_greedy_static.argtypes = [ctypes.POINTER(Batch), i32, ctypes.POINTER(Outputs), vp]
     L.vsv_verify_greedy_static.restype = ctypes.c_int
+    L.vsv_verify_greedy_tree.argtypes = [ctypes.POINTER(Batch), vp, ctypes.POINTER(Outputs), vp, vp, sz, vp]
+    L.vsv_verify_greedy_tree.restype = ctypes.c_int
+    L.vsv_adjust_logits.argtypes = [ctypes.POINTER(Adjust), vp, vp]
+    L.vsv_adjust_logits.restype = ctypes.c_int
+    L.vsv_plan_pages.argtypes = [vp, i64, i32, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.vsv_plan_pages.restype = ctypes.c_int
     L.vsv_verify_sampled.argtypes = [ctypes.POINTER(Batch), vp, vp, vp, vp, u64, u64,
                                      ctypes.POINTER(Outputs), vp, sz, vp]
     L.vsv_verify_sampled.restype = ctypes.c_int
@@ -688,6 +712,155 @@ def distill_loss(student_logits, teacher_ids, teacher_logits, teacher_lse=None, 
         return _distill_losses(student_logits, teacher_ids, teacher_logits, teacher_lse, temperature, error_flag, None,
                                False)[0]
     return _DistillLoss.apply(student_logits, teacher_ids, teacher_logits, teacher_lse, float(temperature), error_flag)
+
+
+def verify_greedy_tree(logits, row_offsets, row_owner, draft_tokens, parents, vocab=None, ws=None, stream=None):
+    """Greedy verification of trees of drafts (vsv_verify_greedy_tree).
+
+    `parents` (int32 [R], a row's parent counted from its request's first
+    row; the roots' entries are not read) or None for chains. At most
+    MAX_TREE_ROWS rows a request. Returns verify_greedy's dict with out_rows
+    [R]: the rows of every accepted path at out_offsets, -1 behind them."""
+    dev = logits.device
+    if not logits.is_cuda or not row_offsets.is_cuda or row_offsets.dim() != 1 or row_offsets.numel() < 1:
+        raise ValueError("logits and row_offsets must be CUDA tensors, row_offsets a vector of B + 1")
+    _same_device(dev, row_offsets, row_owner, draft_tokens, parents)
+    if parents is not None:
+        _vec(parents, logits.shape[0], torch.int32, "parents")
+    on = _on(dev, stream)
+    with on as s:
+        st = torch.cuda.current_stream(dev)
+        batch, outs, out, B, R = _prepare(logits, row_offsets, row_owner, draft_tokens, vocab, st)
+        rows = torch.full((max(R, 1),), -1, dtype=torch.int32, device=dev)
+        ws = workspace(B, R, False, dev, st) if ws is None else ws
+        on.keep(logits, row_offsets, row_owner, draft_tokens, parents, ws)
+        _check(lib().vsv_verify_greedy_tree(ctypes.byref(batch), _at(parents), ctypes.byref(outs), _at(rows),
+                                            _at(ws), ws.numel(), s))
+    out["out_rows"] = rows
+    return out
+
+
+def _adjust_vec(t, n, dtype, name, device):
+    if t is not None:
+        _vec(t, n, dtype, name)
+        _same_device(device, t)
+    return _at(t)
+
+
+def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None, history_len=None, prompt_len=None,
+                  repetition=None, frequency=None, presence=None, bias_offsets=None, bias_tokens=None,
+                  bias_values=None, mask=None, mask_index=None, vocab=None, out=None, error_flag=None, stream=None):
+    """Penalties, biases and grammar masks on packed rows of logits
+    (vsv_adjust_logits); returns the adjusted rows [R, vocab] in the logits'
+    type.
+
+    Row r of request i stands behind the drafts before it (with `parents`:
+    behind those on its path from the root). `history` [B, H] int32 holds each
+    request's prompt and output, `prompt_len` and `history_len` [B] how many
+    tokens of it are the prompt's and how many there are; `repetition`,
+    `frequency` and `presence` are float32 [B]. Biases are lists of tokens and
+    values, request i's at bias_offsets[i] .. bias_offsets[i + 1]. `mask`
+    [M, (vocab + 31) // 32] int32 allows token v where bit v % 32 of word
+    v // 32 is set, and `mask_index` [R] names each row's (negative: none;
+    None: row r has mask r). `out` may be a matrix like the logits or the logits
+    themselves, of which only the touched elements then move; rows of no
+    request are left as they are in it."""
+    dtype, V, ld = _logits(logits, vocab)
+    R, dev = logits.shape[0], logits.device
+    B = row_offsets.numel() - 1
+    at = lambda t, n, dt, name: _adjust_vec(t, n, dt, name, dev)
+    a = Adjust(logits=_at(logits), dtype=dtype, vocab=V, ld=ld, num_requests=B, num_rows=R)
+    a.row_offsets = at(row_offsets, B + 1, torch.int32, "row_offsets")
+    if R > B:
+        _vec(draft_tokens, R - B, torch.int32, "draft_tokens")
+        a.draft_tokens = at(draft_tokens, R - B, torch.int32, "draft_tokens")
+    a.parents = at(parents, R, torch.int32, "parents")
+    if history is not None:
+        if (not history.is_cuda or history.dtype != torch.int32 or history.dim() != 2 or history.shape[0] != B or
+                (history.shape[1] > 1 and history.stride(1) != 1) or history_len is None):
+            raise ValueError("history must be an int32 CUDA matrix [B, H] with unit column stride, with history_len")
+        _same_device(dev, history)
+        a.history, a.history_width = _at(history), history.shape[1]
+        a.history_ld = history.stride(0) if B > 1 else max(history.shape[1], 1)
+        a.history_len = at(history_len, B, torch.int32, "history_len")
+        a.prompt_len = at(prompt_len, B, torch.int32, "prompt_len")
+    a.repetition = at(repetition, B, torch.float32, "repetition")
+    a.frequency = at(frequency, B, torch.float32, "frequency")
+    a.presence = at(presence, B, torch.float32, "presence")
+    if bias_offsets is not None:
+        n = 0 if bias_tokens is None else bias_tokens.numel()
+        a.bias_offsets, a.num_bias = at(bias_offsets, B + 1, torch.int32, "bias_offsets"), n
+        if n:
+            _vec(bias_values, n, torch.float32, "bias_values")
+            a.bias_tokens = at(bias_tokens, n, torch.int32, "bias_tokens")
+            a.bias_values = at(bias_values, n, torch.float32, "bias_values")
+    if mask is not None:
+        if (not mask.is_cuda or mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[1] < (V + 31) // 32 or
+                (mask.shape[1] > 1 and mask.stride(1) != 1)):
+            raise ValueError("mask must be an int32 CUDA matrix [M, >= (vocab + 31) // 32] with unit column stride")
+        _same_device(dev, mask)
+        if mask_index is None and mask.shape[0] < R:
+            raise ValueError("without mask_index every row needs a row of mask")
+        a.mask, a.num_masks = _at(mask), mask.shape[0]
+        a.mask_ld = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
+        a.mask_index = at(mask_index, R, torch.int32, "mask_index")
+    _flag(error_flag, dev)
+    if out is not None:
+        odt, _, old = _logits(out, V)
+        if odt != dtype or out.shape[0] != R or out.device != dev:
+            raise ValueError("out must be a matrix [R, >= vocab] of the logits' type and device")
+        a.out, a.out_ld = _at(out), old
+    on = _on(dev, stream)
+    with on as s:
+        if out is None:
+            out = torch.empty((R, V), dtype=logits.dtype, device=dev)
+            a.out, a.out_ld = _at(out), V
+        on.keep(logits, row_offsets, draft_tokens, parents, history, history_len, prompt_len, repetition, frequency,
+                presence, bias_offsets, bias_tokens, bias_values, mask, mask_index, out, error_flag)
+        _check(lib().vsv_adjust_logits(ctypes.byref(a), _at(error_flag), s))
+    return out[:, :V] if out.shape[1] > V else out
+
+
+def plan_pages(block_table, held, length, row_offsets, free_pages, free_count, page_size, num_rows, stream=None):
+    """Pages and slots for rows to be stored (vsv_plan_pages).
+
+    Request i has `length[i]` tokens stored in its first `held[i]` pages of
+    block_table [B, W] and row_offsets[i + 1] - row_offsets[i] rows to store.
+    block_table and free_pages (a stack of `free_count[0]` page ids) are
+    updated in place; everything is int32. `num_rows` is the most rows there
+    may be (the offsets' own end is known to the device alone). Returns a
+    dict of device tensors: slot [num_rows] int64 and position [num_rows] (-1
+    for rows of no request), held, length and free_count behind the call, and
+    error_flag (FLAG_PAGES: the pool ran out, and the requests it could not
+    serve are as they were)."""
+    B, R, dev = row_offsets.numel() - 1, int(num_rows), row_offsets.device
+    _vec(row_offsets, B + 1, torch.int32, "row_offsets")
+    _vec(held, B, torch.int32, "held")
+    _vec(length, B, torch.int32, "length")
+    _vec(free_pages, free_pages.numel(), torch.int32, "free_pages")
+    _vec(free_count, 1, torch.int32, "free_count")
+    if (not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or
+            block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be an int32 CUDA matrix [B, W] with unit column stride")
+    if R < 0:
+        raise ValueError("num_rows must not be negative")
+    _same_device(dev, block_table, held, length, free_pages, free_count)
+    W = block_table.shape[1]
+    on = _on(dev, stream)
+    with on as s:
+        out = dict(slot=torch.empty(R, dtype=torch.int64, device=dev),
+                   position=torch.empty(R, dtype=torch.int32, device=dev),
+                   held=torch.empty(B, dtype=torch.int32, device=dev),
+                   length=torch.empty(B, dtype=torch.int32, device=dev),
+                   free_count=torch.empty(1, dtype=torch.int32, device=dev),
+                   error_flag=_new_flag(dev, s))
+        on.keep(block_table, held, length, row_offsets, free_pages, free_count)
+        _check(lib().vsv_plan_pages(_at(block_table), block_table.stride(0) if B > 1 else max(W, 1), W, _at(held),
+                                    _at(length), _at(row_offsets), B, R, _at(free_pages), free_pages.numel(),
+                                    _at(free_count), int(page_size), _at(out["slot"]), _at(out["position"]),
+                                    _at(out["held"]), _at(out["length"]), _at(out["free_count"]),
+                                    _at(out["error_flag"]), s))
+    return out
 
 
 def _alloc_outputs(B, K, G, dev, with_drafts):

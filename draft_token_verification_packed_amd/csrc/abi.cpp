@@ -6,8 +6,10 @@
 
 #include <atomic>
 
+#include "adjust.hpp"
 #include "allocate.hpp"
 #include "kernels.hpp"
+#include "pages.hpp"
 #include "probabilistic.hpp"
 #include "rows.hpp"
 
@@ -185,6 +187,17 @@ vsv_status vsv_verify_greedy_relaxed(const vsv_batch* batch, const vsv_relax* re
   return vsv::launch_verify_greedy(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 
+vsv_status vsv_verify_greedy_tree(const vsv_batch* batch, const int32_t* parents, const vsv_outputs* out,
+                                  int32_t* out_rows, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  VerifyArgs a;
+  bool empty = false;
+  const vsv_status st = prepare(batch, out, workspace, workspace_bytes, 0, &a, &empty);
+  if (st != VSV_OK || empty) return st;
+  a.parents = parents;
+  a.out_rows = out_rows;
+  return vsv::launch_verify_greedy_tree(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
 vsv_status vsv_verify_sampled(const vsv_batch* batch, const float* temperature, const int32_t* top_k,
                               const float* top_p, const float* min_p, uint64_t seed, uint64_t offset,
                               const vsv_outputs* out, void* workspace, size_t workspace_bytes,
@@ -360,6 +373,84 @@ vsv_status vsv_allocate_verify(const float* confidence, const int32_t* draft_tok
   return vsv::launch_allocate(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 
+vsv_status vsv_adjust_logits(const vsv_adjust* d, int32_t* error_flag, hipStream_t stream) {
+  if (!d || d->num_requests < 0 || d->num_rows < 0) return VSV_EINVAL;
+  if (d->num_requests == 0 || d->num_rows == 0) return VSV_OK;
+  if (!rows_ok(d->logits, d->dtype, d->vocab, d->ld, d->num_rows)) return VSV_EINVAL;
+  if (!rows_ok(d->out, d->dtype, d->vocab, d->out_ld, d->num_rows)) return VSV_EINVAL;
+  if (d->out == d->logits) {
+    if (d->out_ld != d->ld) return VSV_EINVAL;
+  } else {
+    const size_t e = elem_size(d->dtype);
+    const uintptr_t x = reinterpret_cast<uintptr_t>(d->logits), y = reinterpret_cast<uintptr_t>(d->out);
+    const uintptr_t xe = x + (static_cast<uintptr_t>(d->num_rows - 1) * d->ld + d->vocab) * e;
+    const uintptr_t ye = y + (static_cast<uintptr_t>(d->num_rows - 1) * d->out_ld + d->vocab) * e;
+    if (x < ye && y < xe) return VSV_EINVAL;
+  }
+  if (!d->row_offsets || (d->num_rows > d->num_requests && !d->draft_tokens)) return VSV_EINVAL;
+  if (d->history &&
+      (!d->history_len || d->history_width < 0 || d->history_ld < d->history_width ||
+       d->history_ld > (INT64_MAX / 4) / d->num_requests))
+    return VSV_EINVAL;
+  if (d->num_bias < 0 || (d->bias_offsets && d->num_bias > 0 && (!d->bias_tokens || !d->bias_values))) return VSV_EINVAL;
+  if (d->mask && (d->num_masks < 0 || d->mask_ld < (static_cast<int64_t>(d->vocab) + 31) / 32 ||
+                  (d->num_masks > 0 && d->mask_ld > (INT64_MAX / 4) / d->num_masks) ||
+                  (!d->mask_index && d->num_masks < d->num_rows)))
+    return VSV_EINVAL;
+  vsv::AdjustArgs a{};
+  a.x = d->logits;
+  a.y = d->out;
+  a.ld = d->ld;
+  a.out_ld = d->out_ld;
+  a.V = d->vocab;
+  a.B = d->num_requests;
+  a.R = d->num_rows;
+  a.dtype = d->dtype;
+  a.offsets = d->row_offsets;
+  a.drafts = d->draft_tokens;
+  a.parents = d->parents;
+  a.history = d->history_width > 0 ? d->history : nullptr;
+  a.hist_ld = d->history_ld;
+  a.hist_width = d->history_width;
+  a.prompt_len = d->prompt_len;
+  a.history_len = d->history_len;
+  a.repetition = d->repetition;
+  a.frequency = d->frequency;
+  a.presence = d->presence;
+  a.bias_offsets = d->num_bias > 0 ? d->bias_offsets : nullptr;
+  a.bias_tokens = d->bias_tokens;
+  a.bias_values = d->bias_values;
+  a.bias_count = d->num_bias;
+  a.mask = d->mask;
+  a.mask_ld = d->mask_ld;
+  a.mask_rows = d->num_masks;
+  a.mask_index = d->mask_index;
+  a.error_flag = error_flag;
+  a.cus = device_cus();
+  return vsv::launch_adjust(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
+vsv_status vsv_plan_pages(int32_t* block_table, int64_t table_ld, int32_t table_width, const int32_t* held,
+                          const int32_t* length, const int32_t* row_offsets, int32_t num_requests, int32_t num_rows,
+                          int32_t* free_pages, int32_t pool_size, const int32_t* free_count, int32_t page_size,
+                          int64_t* slot, int32_t* position, int32_t* new_held, int32_t* new_length,
+                          int32_t* new_free_count, int32_t* error_flag, hipStream_t stream) {
+  const int32_t B = num_requests, R = num_rows;
+  if (B < 0 || B > vsv::kMaxPlanRequests || R < 0 || page_size < 1 || pool_size < 1) return VSV_EINVAL;
+  if (!row_offsets || !free_pages || !free_count || !new_free_count || (R > 0 && !slot)) return VSV_EINVAL;
+  if (B > 0) {
+    if (!block_table || !held || !length || !new_held || !new_length) return VSV_EINVAL;
+    if (table_width < 1 || table_ld < table_width || table_ld > (INT64_MAX / 4) / B) return VSV_EINVAL;
+    if (static_cast<int64_t>(B) * table_width > INT32_MAX) return VSV_EINVAL;
+    if (new_held == held || new_length == length) return VSV_EINVAL;
+  }
+  if (new_free_count == free_count || !aligned(slot, 8)) return VSV_EINVAL;
+  const vsv::PagesArgs a{block_table, table_ld, table_width, B, R, page_size, held, length, row_offsets,
+                         free_pages, pool_size, free_count, slot, position, new_held, new_length, new_free_count,
+                         error_flag};
+  return vsv::launch_pages(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
 const char* vsv_status_string(vsv_status status) {
   switch (status) {
     case VSV_OK: return "ok";
@@ -378,6 +469,6 @@ vsv_status vsv_test_withhold_row_word(int32_t row) {
   return VSV_OK;
 }
 
-int32_t vsv_version(void) { return 104; }
+int32_t vsv_version(void) { return 105; }
 
 }  // extern "C"

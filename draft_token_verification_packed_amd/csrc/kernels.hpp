@@ -119,6 +119,9 @@ struct VerifyArgs {
   // sampled: the queue hands out the sampled requests' rows first (each
   // workgroup derives the order at its start, row_queue.hpp)
   int32_t ordered;
+  // tree verification only
+  const int32_t* parents;   // [R], or NULL: chains
+  int32_t* out_rows;        // [R] or NULL
 };
 
 struct ConfidenceArgs {
@@ -194,6 +197,7 @@ constexpr int32_t kMaxVocab = 0x3FFFFFFF;
 constexpr int64_t kMaxRowBytes = 0x7FFFFFF0;
 
 hipError_t launch_verify_greedy(const VerifyArgs& a, hipStream_t s);
+hipError_t launch_verify_greedy_tree(const VerifyArgs& a, hipStream_t s);
 hipError_t launch_verify_sampled(const VerifyArgs& a, hipStream_t s);
 hipError_t launch_confidence(const ConfidenceArgs& a, hipStream_t s);
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);

@@ -4,6 +4,7 @@
 // the row's word (emitted token, accept bit); the launch's last workgroup
 // runs the per-request scan (verify_common.hpp). No atomics on global
 // memory.
+#include "tree_scan.hpp"
 #include "verify_common.hpp"
 
 namespace vsv {
@@ -19,10 +20,14 @@ namespace vsv {
 // part, dispatched after them (so its wait always ends), gathers them
 // across one wave, merges them with its own, decides the row and hands its
 // word to the scan run by the launch's last workgroup.
-template <typename E, int NT, int U, bool kRelaxed>
+//
+// Trees (kTree) differ in the scan alone: a row's word is its arg-max, and
+// acceptance, which needs the parent's arg-max, is decided there (tree_tail).
+template <typename E, int NT, int U, bool kRelaxed, bool kTree = false>
 __global__ __launch_bounds__(NT) void verify_greedy_rows_kernel(VerifyArgs a) {
+  static_assert(!(kRelaxed && kTree), "trees are accepted strictly");
   __shared__ LeanScratch<NT> scr;
-  __shared__ TailScratch tail;
+  __shared__ std::conditional_t<kTree, TreeScratch<NT>, TailScratch> tail;
   __shared__ int s_prot[VSV_MAX_PROTECTED];
   static_assert(VSV_MAX_PROTECTED % NT == 0 || NT % VSV_MAX_PROTECTED == 0, "protected ids per thread");
   constexpr int kProtPer = VSV_MAX_PROTECTED >= NT ? VSV_MAX_PROTECTED / NT : 1;
@@ -56,7 +61,7 @@ __global__ __launch_bounds__(NT) void verify_greedy_rows_kernel(VerifyArgs a) {
 #pragma unroll
   for (int k = 0; k < kProtPer; ++k) prot_reg[k] = -1;
   auto hook = [&]() {
-    if (last) {
+    if (last && !kTree) {
       if (!kRelaxed) m = load_meta(a, r, owner);
       if (a.relax_var) {
         if (!kRelaxed && m.draft >= 0 && m.draft < a.V) xm = Elem<E>::at(row, m.draft);
@@ -119,14 +124,19 @@ __global__ __launch_bounds__(NT) void verify_greedy_rows_kernel(VerifyArgs a) {
       }
       const bool ok = a.relax_var ? relaxed_ok(a, m, token, red.best, xm, red.rank, prot, gen)
                                   : (kRelaxed ? (red.rank < a.relaxed_k) : (m.draft == token));
-      const uint32_t word = row_word(a, m, token, ok, bits);
+      const uint32_t word = kTree ? static_cast<uint32_t>(token) : row_word(a, m, token, ok, bits);
       if (bits) set_flag(a, bits);
       if (a.row_token) a.row_token[r] = token;
       if (a.row_lse) a.row_lse[r] = lse;
       if (r != a.withheld_row) store_agent64(a.ws_row + r, tagged(tag, word));
     }
   }
-  if (blockIdx.x == gridDim.x - 1) words_tail<NT>(a, tag, tail);
+  if (blockIdx.x == gridDim.x - 1) {
+    if constexpr (kTree)
+      tree_tail<NT>(a, tag, tail);
+    else
+      words_tail<NT>(a, tag, tail);
+  }
 }
 
 // Parts per row: about one part per kPartBytes of the row or, for batches
@@ -164,12 +174,12 @@ inline int row_parts(const VerifyArgs& a, int64_t row_bytes) {
   return P;
 }
 
-template <typename E, bool kRelaxed>
+template <typename E, bool kRelaxed, bool kTree = false>
 static hipError_t launch_greedy_t(VerifyArgs a, hipStream_t s) {
   a.parts = row_parts(a, static_cast<int64_t>(a.V) * static_cast<int64_t>(sizeof(E)));
   const int64_t grid = static_cast<int64_t>(a.R) * a.parts;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  verify_greedy_rows_kernel<E, kRowThreads, kUnrollRows, kRelaxed>
+  verify_greedy_rows_kernel<E, kRowThreads, kUnrollRows, kRelaxed, kTree>
       <<<dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), 0, s>>>(a);
   return hipGetLastError();
 }
@@ -178,6 +188,10 @@ hipError_t launch_verify_greedy(const VerifyArgs& a, hipStream_t s) {
   if (a.dtype == VSV_BF16)
     return a.relaxed_k > 1 ? launch_greedy_t<uint16_t, true>(a, s) : launch_greedy_t<uint16_t, false>(a, s);
   return a.relaxed_k > 1 ? launch_greedy_t<float, true>(a, s) : launch_greedy_t<float, false>(a, s);
+}
+
+hipError_t launch_verify_greedy_tree(const VerifyArgs& a, hipStream_t s) {
+  return a.dtype == VSV_BF16 ? launch_greedy_t<uint16_t, false, true>(a, s) : launch_greedy_t<float, false, true>(a, s);
 }
 
 // ---------------------------------------------------------------- workspace

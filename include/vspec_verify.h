@@ -68,6 +68,8 @@ typedef enum { VSV_F32 = 0, VSV_BF16 = 1 } vsv_dtype;
 #define VSV_FLAG_STALLED 16 /* a row's result did not reach the batch scan within the scan's    */
                             /* bounded wait (rows of one launch could not all be resident;   */
                             /* not expected on a dedicated GPU); outputs are unspecified     */
+#define VSV_FLAG_PAGES 32  /* the pool of free pages is empty, or a block table names a page     */
+                           /* that the cache does not have                                       */
 
 typedef struct {
   const void* logits;          /* [num_rows, ld] vocab-wide target logits             */
@@ -166,6 +168,32 @@ typedef struct {
 vsv_status vsv_verify_greedy_relaxed(const vsv_batch* batch, const vsv_relax* relax,
                                      const vsv_outputs* out, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream);
+
+/* Greedy verification of trees of drafts. A request's rows are the nodes of
+ * a tree: its first row is the root (the last token already emitted), every
+ * later row a drafted token, and parents[r] the row its draft follows,
+ * counted from the request's first row (0 <= parents[r] < r - off[i]; the
+ * root's own entry is not read). Row off[i] + j + 1 carries draft j of
+ * request i, at off[i] - i + j in draft_tokens as in every batch: a chain is
+ * the tree whose row j has the parent j - 1, and parents = NULL stands for
+ * chains throughout. From the root, the walk moves to the lowest row whose
+ * parent is the current row and whose draft is the current row's arg-max, as
+ * long as there is one (vllm-hust-vspec 0.13.0 README, "Scope of support":
+ * EAGLE tree verification; acceptance is strict).
+ * Outputs as vsv_verify_greedy, with accepted_len the drafts on the path and
+ * next_token the arg-max of its last row, and
+ *   out_rows [num_rows] or NULL: at out_offsets[i] the accepted_len[i] + 1
+ *                       rows of request i's path, root first: the rows whose
+ *                       keys and values belong into the cache, at the
+ *                       positions that vsv_plan_pages gives for row_offsets =
+ *                       out_offsets
+ * A request may have at most VSV_MAX_TREE_ROWS rows. VSV_FLAG_LAYOUT: layout
+ * as above, more rows, or a parent that is no earlier row of the request (the
+ * row is then on no path). Workspace: vsv_workspace_bytes(B, R, 0).
+ * Errors: as vsv_verify_greedy. */
+#define VSV_MAX_TREE_ROWS 64
+vsv_status vsv_verify_greedy_tree(const vsv_batch* batch, const int32_t* parents, const vsv_outputs* out,
+                                  int32_t* out_rows, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Greedy verification that allocates nothing, for callers that cannot
  * allocate device memory or pass a workspace: code under HIP graph capture,
@@ -404,6 +432,97 @@ vsv_status vsv_allocate_verify(const float* confidence, const int32_t* draft_tok
                                int32_t* verify_len, int32_t* row_offsets, int32_t* row_owner,
                                int32_t* row_source, int32_t* packed_drafts, float* prefix,
                                hipStream_t stream);
+
+/* Penalties, biases and grammar masks on packed rows of logits, before they
+ * are verified or drawn from. Row r of request i stands behind a path of
+ * drafts (in a chain the drafts before it; with `parents`, those from the
+ * root to its node, its own included; draft tokens as in vsv_batch). With c
+ * the occurrences of a token in the request's output and on that path, and
+ * "seen" if it occurs there or in the prompt:
+ *   y = seen ? (x > 0 ? x / repetition[i] : x * repetition[i]) : x
+ *   y = y - frequency[i] * c - (c > 0 ? presence[i] : 0)
+ *   y = y + bias of the token (the last entry that names it)
+ *   y = -inf where the row's mask has a 0 bit
+ * in float32, rounded once. A mask may leave a row nothing (all -inf). */
+typedef struct {
+  const void* logits;           /* [num_rows, ld]                                       */
+  void* out;                    /* [num_rows, out_ld], or the logits themselves with    */
+                                /* out_ld == ld; no other overlap                       */
+  int32_t dtype;                /* vsv_dtype                                            */
+  int32_t vocab;                /* as in vsv_batch                                      */
+  int64_t ld, out_ld;           /* columns beyond vocab are left as they are            */
+  int32_t num_requests;         /* B >= 0                                               */
+  int32_t num_rows;             /* R >= 0                                               */
+  const int32_t* row_offsets;   /* [B + 1], not falling, within 0 .. R: requests        */
+                                /* without rows come last, and rows at or beyond        */
+                                /* off[B] are left as they are                          */
+  const int32_t* draft_tokens;  /* [R - B], NULL when R <= B                            */
+  const int32_t* parents;       /* [R] as in vsv_verify_greedy_tree (at most            */
+                                /* VSV_MAX_TREE_ROWS rows a request), NULL: chains of   */
+                                /* any length                                           */
+  const int32_t* history;       /* [B, history_ld] tokens: the prompt, then the output; */
+                                /* NULL: none                                           */
+  int64_t history_ld;
+  int32_t history_width;        /* entries of a row that may be read                    */
+  const int32_t* prompt_len;    /* [B] tokens of the prompt, or NULL: 0                 */
+  const int32_t* history_len;   /* [B] tokens of both (required with history)           */
+  const float* repetition;      /* [B] positive and finite, or NULL: 1                  */
+  const float* frequency;       /* [B] finite, or NULL: 0                               */
+  const float* presence;        /* [B] finite, or NULL: 0                               */
+  const int32_t* bias_offsets;  /* [B + 1], or NULL: no biases                          */
+  const int32_t* bias_tokens;   /* [num_bias]                                           */
+  const float* bias_values;     /* [num_bias] finite or -inf                            */
+  int32_t num_bias;
+  const uint32_t* mask;         /* [num_masks, mask_ld] words, bit v % 32 of word       */
+                                /* v / 32 allows token v; NULL: none                    */
+  int64_t mask_ld;              /* >= (vocab + 31) / 32                                 */
+  int32_t num_masks;
+  const int32_t* mask_index;    /* [R] row of `mask`, negative: the row is not masked;  */
+                                /* NULL: row r's mask is row r                          */
+} vsv_adjust;
+
+/* VSV_FLAG_TOKEN: a token of a history, path or bias outside the vocabulary
+ * (it counts nowhere); VSV_FLAG_PARAMS: a penalty or bias outside its range
+ * (counts as off); VSV_FLAG_LAYOUT: offsets, lengths, parents or mask rows
+ * outside theirs (a request with bad offsets is left as it is). Bits of
+ * requests without any row are not looked at.
+ * Errors: VSV_EINVAL (NULL struct, logits, out or row_offsets; draft_tokens
+ * NULL with R > B, history without history_len, bias_offsets without tokens
+ * and values when num_bias > 0; sizes, strides, alignment or dtype; an
+ * overlapping out), VSV_EHIP. */
+vsv_status vsv_adjust_logits(const vsv_adjust* a, int32_t* error_flag, hipStream_t stream);
+
+/* Block tables and slots of rows to store, from lengths that only the device
+ * knows. Request i has length[i] tokens in a cache of pages of page_size
+ * tokens and row_offsets[i + 1] - row_offsets[i] rows to store behind them
+ * (out_offsets of a verify call, or the rows of a prompt; none for a request
+ * that waits). It needs p = ceil((length[i] + rows) / page_size) pages and
+ * holds held[i]. Free pages are a stack, free_pages[0 .. free_count - 1]:
+ * first, in request order, every request that holds more than it needs puts
+ * its pages p .. held - 1 on it (a request that has ended: length 0 and no
+ * rows); then, in request order, those that need more take theirs from its
+ * top. A request that the stack cannot serve any more, and every later one that
+ * needs pages, is left as it is (VSV_FLAG_PAGES; slots -1).
+ *   block_table [B, table_ld]  read, and written at the pages taken; entries
+ *                       that are given back keep their values
+ *   free_pages [pool_size]  read, and written above free_count
+ *   slot [num_rows]     page * page_size + position % page_size of every
+ *                       row, -1 for rows at or beyond row_offsets[B]
+ *   position [num_rows] or NULL: position of the row in its request, or -1
+ *   new_held, new_length [B], new_free_count [1]  the state behind the call;
+ *                       none may overlap an input, so that a call that is
+ *                       repeated on the same inputs gives the same results
+ * VSV_FLAG_LAYOUT: offsets that fall or leave 0 .. R, a negative length, a
+ * held or needed count beyond table_width (the request is left as it is), a
+ * count beyond pool_size, or a negative page.
+ * Errors: VSV_EINVAL (B outside 0 .. 8192, num_rows < 0, page_size < 1, table_width or
+ * pool_size < 1, B * table_width beyond 2^31 - 1, table_ld < table_width, NULL pointers),
+ * VSV_EHIP. B = 0 writes slots, positions and the count alone. */
+vsv_status vsv_plan_pages(int32_t* block_table, int64_t table_ld, int32_t table_width, const int32_t* held,
+                          const int32_t* length, const int32_t* row_offsets, int32_t num_requests, int32_t num_rows,
+                          int32_t* free_pages, int32_t pool_size, const int32_t* free_count, int32_t page_size,
+                          int64_t* slot, int32_t* position, int32_t* new_held, int32_t* new_length,
+                          int32_t* new_free_count, int32_t* error_flag, hipStream_t stream);
 
 /* Goodput step selection: the step count of the next decode batch from
  * completed verification results (xLLM docs, "Adaptive speculative

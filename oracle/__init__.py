@@ -6,6 +6,7 @@ imports nothing from it.
 """
 from .philox import philox4x32_10, row_uniform
 from .rows import distill_row, draw_row, top_row
+from .tree import adjust_row, path_of, plan_pages, tree_attention, verify_greedy_tree
 from .verify import (BF16, F32, PreconditionError, bf16_bits_to_f64,
                      draft_confidence, filtered_support, greedy_token,
                      logsumexp, rank_of, rank_order, relaxed_accepts, row_f64,

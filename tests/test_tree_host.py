@@ -1,0 +1,98 @@
+"""Refusals of the tree operators: a status, or an exception in the binding,
+before anything is enqueued. Needs no GPU."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import draft_token_verification_packed_amd as vsv
+from tests.test_abi_host import _batch, _outs
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(vsv.LIB_PATH):
+        pytest.skip("library not built (run the package build first)")
+    return vsv.lib()
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(logits=None), 1), (dict(dtype=7), 1), (dict(vocab=0), 1), (dict(ld=1000), 1), (dict(num_rows=3), 1),
+    (dict(row_offsets=None), 1), (dict(row_owner=None), 1), (dict(draft_tokens=None), 1), (dict(logits=0x10001), 1),
+])
+def test_verify_tree_refusals(L, bad, status):
+    b, o = _batch(**bad), _outs()
+    assert L.vsv_verify_greedy_tree(ctypes.byref(b), P(8), ctypes.byref(o), P(8), P(0x100000), 1 << 20, None) == status
+
+
+def test_verify_tree_other_refusals(L):
+    b = _batch()
+    for o in (_outs(accepted_len=None), _outs(out_tokens=None)):
+        assert L.vsv_verify_greedy_tree(ctypes.byref(b), P(8), ctypes.byref(o), None, P(0x100000), 1 << 20, None) == 1
+    o = _outs()
+    assert L.vsv_verify_greedy_tree(None, P(8), ctypes.byref(o), None, P(0x100000), 1 << 20, None) == 1
+    assert L.vsv_verify_greedy_tree(ctypes.byref(b), P(8), ctypes.byref(o), None, None, 1 << 20, None) == 3
+    assert L.vsv_verify_greedy_tree(ctypes.byref(b), P(8), ctypes.byref(o), None, P(0x100000), 64, None) == 3
+    e = _batch(num_requests=0, num_rows=0)
+    assert L.vsv_verify_greedy_tree(ctypes.byref(e), None, ctypes.byref(o), None, None, 0, None) == 0
+
+
+def _adjust(L, **kw):
+    a = dict(logits=0x100000, out=0x200000, dtype=1, vocab=1000, ld=1000, out_ld=1000, num_requests=4, num_rows=20,
+             row_offsets=8, draft_tokens=8, history=8, history_ld=16, history_width=16, history_len=8, bias_offsets=8,
+             bias_tokens=8, bias_values=8, num_bias=3, mask=8, mask_ld=32, num_masks=20)
+    a.update(kw)
+    return L.vsv_adjust_logits(ctypes.byref(vsv.Adjust(**a)), None, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(logits=None), dict(out=None), dict(logits=0x100001), dict(out=0x200001), dict(dtype=0, out=0x200002),
+    dict(dtype=3), dict(vocab=0), dict(ld=999), dict(out_ld=999), dict(ld=1 << 62), dict(out_ld=1 << 62),
+    dict(vocab=1 << 30, ld=1 << 30, out_ld=1 << 30), dict(num_requests=-1), dict(num_rows=-1), dict(row_offsets=None),
+    dict(draft_tokens=None), dict(history_len=None), dict(history_width=-1), dict(history_ld=15),
+    dict(history_ld=1 << 62), dict(num_bias=-1), dict(bias_tokens=None), dict(bias_values=None), dict(mask_ld=31),
+    dict(num_masks=-1), dict(num_masks=19), dict(mask_ld=1 << 62),
+    # outputs that overlap the logits without being them
+    dict(out=0x100002), dict(out=0x100000 + 39998), dict(out=0x100000 - 39998), dict(out=0x100000, out_ld=1001),
+])
+def test_adjust_refusals(L, bad):
+    assert _adjust(L, **bad) == 1
+
+
+def test_adjust_noops_and_null(L):
+    assert _adjust(L, num_requests=0, logits=None) == 0
+    assert _adjust(L, num_rows=0, logits=None) == 0
+    assert L.vsv_adjust_logits(None, None, None) == 1
+
+
+def _pages(L, **kw):
+    a = dict(table=0x1000, ld=8, width=8, held=0x2000, length=0x3000, offsets=0x4000, B=4, R=10, free=0x5000, pool=50,
+             count=0x6000, page=16, slot=0x7000, position=0x8000, new_held=0x9000, new_length=0xa000, new_count=0xb000)
+    a.update(kw)
+    p = lambda k: P(a[k]) if a[k] else None
+    return L.vsv_plan_pages(p("table"), a["ld"], a["width"], p("held"), p("length"), p("offsets"), a["B"], a["R"],
+                            p("free"), a["pool"], p("count"), a["page"], p("slot"), p("position"), p("new_held"),
+                            p("new_length"), p("new_count"), None, None)
+
+
+@pytest.mark.parametrize("bad", [dict([(k, None)]) for k in ("table", "held", "length", "offsets", "free", "count", "slot",
+                                                            "new_held", "new_length", "new_count")] + [
+    dict(B=-1), dict(B=8193), dict(R=-1), dict(page=0), dict(pool=0), dict(width=0), dict(ld=7), dict(ld=1 << 62),
+    dict(B=8000, width=300000, ld=300000), dict(new_held=0x2000), dict(new_length=0x3000), dict(new_count=0x6000),
+    dict(slot=0x7004)])
+def test_pages_refusals(L, bad):
+    assert _pages(L, **bad) == 1
+
+
+def test_binding_refusals():
+    cpu = torch.zeros(4, 16)
+    i = lambda n: torch.zeros(n, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        vsv.verify_greedy_tree(cpu, i(2), i(4), i(3), i(4))
+    with pytest.raises(ValueError):
+        vsv.adjust_logits(cpu, i(2), i(3))
+    with pytest.raises(ValueError):
+        vsv.plan_pages(i(4).view(1, 4), i(1), i(1), i(2), i(9), i(1), 16, 4)
