@@ -20,6 +20,7 @@ Entry points mirror the C ABI in include/vspec_verify.h:
     distill_loss_grad(student_logits, teacher_ids, teacher_logits, row_weight=None, teacher_lse=None, temperature=1.0)
     distill_forward / distill_backward: the two halves of distill_loss
     allocate_verify(confidence, draft_tokens, num_requests, num_drafts, row_budget)
+    tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, parents=None, scale=None)
     adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None, ...)
     plan_pages(block_table, held, length, row_offsets, free_pages, free_count, page_size, num_rows)
     Goodput(max_steps, window_size=20, update_interval=5, switch_min_gain=0.05)
@@ -82,6 +83,17 @@ class Distill(ctypes.Structure):
                 ("temperature", ctypes.c_float)]
 
 
+class Attention(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "k_cache", "v_cache", "out", "lse")] +
+                [(n, ctypes.c_int64) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head", "out_row",
+                                               "out_head", "cache_page", "cache_token", "cache_head")] +
+                [(n, ctypes.c_int32) for n in ("dtype", "head_dim", "num_heads", "num_kv_heads", "num_requests",
+                                               "num_rows")] +
+                [(n, ctypes.c_void_p) for n in ("row_offsets", "parents", "length", "block_table")] +
+                [("table_ld", ctypes.c_int64), ("table_width", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                 ("page_size", ctypes.c_int32), ("scale", ctypes.c_float)])
+
+
 class Adjust(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32),
                 ("vocab", ctypes.c_int32), ("ld", ctypes.c_int64), ("out_ld", ctypes.c_int64),
@@ -101,7 +113,8 @@ MAX_TOP = 256
 DISTILL_STATE = 5
 
 SYMBOLS = ("vsv_workspace_bytes", "vsv_workspace_init", "vsv_verify_greedy", "vsv_verify_greedy_relaxed",
-           "vsv_verify_greedy_static", "vsv_verify_greedy_tree", "vsv_adjust_logits", "vsv_plan_pages",
+           "vsv_verify_greedy_static", "vsv_verify_greedy_tree", "vsv_tree_attention_workspace_bytes", "vsv_tree_attention",
+           "vsv_adjust_logits", "vsv_plan_pages",
            "vsv_verify_sampled",
            "vsv_verify_probabilistic", "vsv_draft_confidence", "vsv_sample_workspace_bytes", "vsv_sample_rows",
            "vsv_top_workspace_bytes", "vsv_top_logits",
@@ -147,6 +160,10 @@ def lib():
     L.vsv_verify_greedy_static.restype = ctypes.c_int
     L.vsv_verify_greedy_tree.argtypes = [ctypes.POINTER(Batch), vp, ctypes.POINTER(Outputs), vp, vp, sz, vp]
     L.vsv_verify_greedy_tree.restype = ctypes.c_int
+    L.vsv_tree_attention_workspace_bytes.argtypes = [ctypes.POINTER(Attention)]
+    L.vsv_tree_attention_workspace_bytes.restype = sz
+    L.vsv_tree_attention.argtypes = [ctypes.POINTER(Attention), vp, vp, sz, vp]
+    L.vsv_tree_attention.restype = ctypes.c_int
     L.vsv_adjust_logits.argtypes = [ctypes.POINTER(Adjust), vp, vp]
     L.vsv_adjust_logits.restype = ctypes.c_int
     L.vsv_plan_pages.argtypes = [vp, i64, i32, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
@@ -738,6 +755,68 @@ def verify_greedy_tree(logits, row_offsets, row_owner, draft_tokens, parents, vo
                                             _at(ws), ws.numel(), s))
     out["out_rows"] = rows
     return out
+
+
+def _heads(t, shape, dtype, device, name):
+    if (not t.is_cuda or t.dtype != dtype or t.device != device or tuple(t.shape) != shape or
+            (t.numel() and t.stride(-1) != 1)):
+        raise ValueError("%s must be a %s tensor %s on %s with unit last stride" % (name, dtype, list(shape), device))
+    return t
+
+
+def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, parents=None, scale=None, out=None,
+                   return_lse=False, error_flag=None, stream=None):
+    """Attention of packed draft rows over a paged cache (vsv_tree_attention).
+
+    `q` [R, H, D], and the rows' own `k` and `v` [R, KV, D], may be slices of
+    one projection; `k_cache` and `v_cache` [pages, page_size, KV, D] have the
+    same strides. Row r of request i sees length[i] cached tokens (pages
+    block_table[i]), the rows on its path from the root (`parents` as in
+    verify_greedy_tree, None: chains) and itself. All matrices are bfloat16 or
+    all float32, D is 64, 128 or (bfloat16) 256, and pointers and strides are
+    multiples of 16 bytes. `scale` is D ** -0.5 by default. Returns out
+    [R, H, D] (`out` if given; rows of no request are left as they are), and
+    with return_lse also the scores' log-sum-exp [R, H]. Rows get no gradient."""
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q and k must be [rows, heads, dim], the caches [pages, page_size, heads, dim]")
+    dtype, dev = _dtype_code(q), q.device
+    R, H, D = q.shape
+    KV, (pages, page) = k.shape[1], k_cache.shape[:2]
+    B = row_offsets.numel() - 1
+    for t, shape, name in ((q, (R, H, D), "q"), (k, (R, KV, D), "k"), (v, (R, KV, D), "v"),
+                           (k_cache, (pages, page, KV, D), "k_cache"), (v_cache, (pages, page, KV, D), "v_cache")):
+        _heads(t, shape, q.dtype, dev, name)
+    if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, k_cache, v_cache)):
+        raise NotImplementedError("tree_attention has no backward pass")
+    if k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same strides")
+    _vec(row_offsets, B + 1, torch.int32, "row_offsets")
+    _vec(length, B, torch.int32, "length")
+    if parents is not None:
+        _vec(parents, R, torch.int32, "parents")
+    if (not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or
+            block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be an int32 CUDA matrix [B, W] with unit column stride")
+    _same_device(dev, row_offsets, length, parents, block_table)
+    _flag(error_flag, dev)
+    if out is not None:
+        _heads(out, (R, H, D), q.dtype, dev, "out")
+    on = _on(dev, stream)
+    with on as s:
+        if out is None:
+            out = torch.empty((R, H, D), dtype=q.dtype, device=dev)
+        lse = torch.empty((R, H), dtype=torch.float32, device=dev) if return_lse else None
+        W = block_table.shape[1]
+        a = Attention(_at(q), _at(k), _at(v), _at(k_cache), _at(v_cache), _at(out), _at(lse),
+                      *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2], *k_cache.stride()[:3],
+                      dtype, D, H, KV, B, R, _at(row_offsets), _at(parents), _at(length), _at(block_table),
+                      block_table.stride(0) if B > 1 else max(W, 1), W, pages, page,
+                      D ** -0.5 if scale is None else float(scale))
+        n = lib().vsv_tree_attention_workspace_bytes(ctypes.byref(a))
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        on.keep(q, k, v, row_offsets, k_cache, v_cache, block_table, length, parents, out, error_flag)
+        _check(lib().vsv_tree_attention(ctypes.byref(a), _at(error_flag), _at(ws), n, s))
+    return (out, lse) if return_lse else out
 
 
 def _adjust_vec(t, n, dtype, name, device):

@@ -8,6 +8,7 @@
 
 #include "adjust.hpp"
 #include "allocate.hpp"
+#include "attention.hpp"
 #include "kernels.hpp"
 #include "pages.hpp"
 #include "probabilistic.hpp"
@@ -135,6 +136,28 @@ vsv_status distill_scratch(vsv::DistillArgs* a, void* ws, size_t bytes) {
 
 bool distill_grad_ok(const vsv::DistillArgs& a, const void* grad, int64_t grad_ld) {
   return grad && aligned(grad, elem_size(a.x.dtype)) && grad_ld >= a.x.V && grad_ld <= (INT64_MAX / 4) / a.x.N;
+}
+
+// Checks of an attention's sizes and types, and its launch args without pointers.
+bool prepare_attention(const vsv_attention* d, vsv::AttentionArgs* a) {
+  if (!dtype_ok(d->dtype)) return false;
+  if (d->head_dim != 64 && d->head_dim != 128 && !(d->head_dim == 256 && d->dtype == VSV_BF16)) return false;
+  if (d->num_kv_heads < 1 || d->num_heads < d->num_kv_heads || d->num_heads % d->num_kv_heads) return false;
+  if (d->num_heads > 65536 || d->num_requests < 1 || d->num_requests > VSV_MAX_TREE_REQUESTS || d->num_rows < 1) return false;
+  if (d->table_width < 1 || d->num_pages < 1 || d->page_size < 1 || (d->page_size & (d->page_size - 1))) return false;
+  *a = vsv::AttentionArgs{};
+  a->B = d->num_requests;
+  a->R = d->num_rows;
+  a->H = d->num_heads;
+  a->KV = d->num_kv_heads;
+  a->D = d->head_dim;
+  a->dtype = d->dtype;
+  a->table_width = d->table_width;
+  a->num_pages = d->num_pages;
+  while ((1 << a->page_shift) < d->page_size) ++a->page_shift;
+  a->cus = device_cus();
+  return (static_cast<int64_t>(d->table_width) << a->page_shift) <= INT32_MAX - 1024 &&
+         vsv::attention_tiles(*a) <= INT32_MAX;
 }
 
 }  // namespace
@@ -371,6 +394,63 @@ vsv_status vsv_allocate_verify(const float* confidence, const int32_t* draft_tok
   vsv::AllocArgs a{confidence, draft_tokens, B, K, G, verify_len, row_offsets, row_owner, row_source,
                    G > B ? packed_drafts : nullptr, prefix};
   return vsv::launch_allocate(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
+}
+
+size_t vsv_tree_attention_workspace_bytes(const vsv_attention* d) {
+  vsv::AttentionArgs a;
+  return d && prepare_attention(d, &a) ? vsv::attention_workspace(a) : 0;
+}
+
+vsv_status vsv_tree_attention(const vsv_attention* d, int32_t* error_flag, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  if (!d || d->num_requests < 0 || d->num_rows < 0) return VSV_EINVAL;
+  if (d->num_requests == 0 || d->num_rows == 0) return VSV_OK;
+  vsv::AttentionArgs a;
+  if (!prepare_attention(d, &a)) return VSV_EINVAL;
+  if (!d->q || !d->k || !d->v || !d->k_cache || !d->v_cache || !d->out) return VSV_EINVAL;
+  if (!d->row_offsets || !d->length || !d->block_table) return VSV_EINVAL;
+  for (const void* p : {d->q, d->k, d->v, d->k_cache, d->v_cache, static_cast<const void*>(d->out)})
+    if (!aligned(p, 16)) return VSV_EINVAL;
+  // every stride keeps the 16-byte loads aligned and the last element
+  // addressable in 64 bits
+  const int64_t unit = 16 / static_cast<int64_t>(elem_size(d->dtype));
+  const int64_t strides[][2] = {{d->q_row, d->num_rows},       {d->q_head, d->num_heads},   {d->k_row, d->num_rows},
+                                {d->k_head, d->num_kv_heads},  {d->v_row, d->num_rows},     {d->v_head, d->num_kv_heads},
+                                {d->out_row, d->num_rows},     {d->out_head, d->num_heads}, {d->cache_page, d->num_pages},
+                                {d->cache_token, d->page_size}, {d->cache_head, d->num_kv_heads}};
+  for (const auto& s : strides)
+    if (s[0] < 0 || s[0] % unit || s[0] > (INT64_MAX / 16) / s[1]) return VSV_EINVAL;
+  if (d->table_ld < d->table_width || d->table_ld > (INT64_MAX / 4) / d->num_requests) return VSV_EINVAL;
+  if (!(d->scale > 0.f) || !(d->scale < INFINITY)) return VSV_EINVAL;
+  a.scale = static_cast<float>(1.44269504088896340736 * static_cast<double>(d->scale));
+  if (!(a.scale > 0.f) || !(a.scale < INFINITY)) return VSV_EINVAL;
+  if (!workspace || !aligned(workspace, vsv::kWsAlign) || workspace_bytes < vsv::attention_workspace(a)) return VSV_EWORKSPACE;
+  a.q = d->q;
+  a.k = d->k;
+  a.v = d->v;
+  a.k_cache = d->k_cache;
+  a.v_cache = d->v_cache;
+  a.out = d->out;
+  a.lse = d->lse;
+  a.q_row = d->q_row;
+  a.q_head = d->q_head;
+  a.k_row = d->k_row;
+  a.k_head = d->k_head;
+  a.v_row = d->v_row;
+  a.v_head = d->v_head;
+  a.o_row = d->out_row;
+  a.o_head = d->out_head;
+  a.c_page = d->cache_page;
+  a.c_token = d->cache_token;
+  a.c_head = d->cache_head;
+  a.table = d->block_table;
+  a.table_ld = d->table_ld;
+  a.length = d->length;
+  a.offsets = d->row_offsets;
+  a.parents = d->parents;
+  a.error_flag = error_flag;
+  a.work = workspace;
+  return vsv::launch_attention(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
 }
 
 vsv_status vsv_adjust_logits(const vsv_adjust* d, int32_t* error_flag, hipStream_t stream) {

@@ -1,0 +1,752 @@
+// Attention of packed draft rows over a paged cache (gfx950, MFMA).
+//
+// Row r of request i (a node of its tree of drafts) sees the request's
+// length[i] cached tokens, the rows on its path from the root, and itself:
+//   o[r, h] = sum_t p_t v_t,  p = softmax over the seen t of scale q[r, h] . k_t
+// The rows' own keys and values come packed beside q, not from the cache:
+// which of them belong into the cache is known only once the drafts are
+// verified, so no rejected draft ever takes a slot there.
+//
+// The M = rows * G queries that share a key head (G = H / KV) are one matrix,
+// so a key head's tokens are read once for all of them. Scores are computed
+// transposed, S^T = K Q^T: a lane then holds one query (column) and 4 tokens
+// (rows) per 16 x 16 tile, which is how O^T = V^T P^T takes P^T as its second
+// factor, so P never leaves the registers, and the running maximum, the sum
+// and the rescaling of O^T are per-lane scalars. The order of the tokens
+// inside a product is free: lane group g's 8 tokens are 4 g .. 4 g + 3 of
+// each half of a 32-token slice, and V^T is read from LDS in the same order
+// (bfloat16 through the transposing LDS read).
+//
+// Work: a tile is WK * 32 tokens of one (request, key head, block of MT
+// queries), an item the tiles of one such triple. The tiles of the whole
+// batch form one list, cut into equal spans, one per workgroup, whatever the
+// requests' lengths: each workgroup finds its span with a scan over the requests.
+// An item inside one span is finished there; the pieces of an item that
+// spans several go to scratch (reference, weight, sum) and a second kernel
+// joins them. WQ waves share a slice and split the queries; the WK slices of a tile go
+// to different waves, joined through LDS at the end of an item. With few
+// queries (WQ = 1) waves share nothing and meet no barrier in the loop.
+#include <type_traits>
+
+#include "attention.hpp"
+#include "tree.hpp"
+#include "vspec_verify.h"
+
+namespace vsv {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kSlice = 32;     // tokens a wave takes at a time
+constexpr int kThreads = 256;  // four waves: WQ * WK
+
+// One 16 x 16 product over 32 of the inner dimension: lane l holds 8 inner
+// elements of row (column) l % 16, the same 8 in both factors.
+template <typename E> struct Frag;
+template <> struct Frag<uint16_t> {
+  using T = bf16x8;
+  __device__ static __forceinline__ f32x4 mma(T a, T b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  __device__ static __forceinline__ T zero() { return T{}; }
+  __device__ static __forceinline__ T load(const uint16_t* p) { return *reinterpret_cast<const T*>(p); }
+  // P is rounded to bfloat16 for the product with V (half a step, 2^-9 of
+  // each weight); the weights' sum is taken before the rounding
+  __device__ static __forceinline__ T pack(const float* p) {
+    T r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = static_cast<__bf16>(p[e]);
+    return r;
+  }
+};
+template <> struct Frag<float> {
+  using T = f32x8;
+  // eight products over 4: product e takes element e of every lane group
+  __device__ static __forceinline__ f32x4 mma(T a, T b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+  __device__ static __forceinline__ T zero() { return T{}; }
+  __device__ static __forceinline__ T load(const float* p) {
+    const f32x4 lo = reinterpret_cast<const f32x4*>(p)[0], hi = reinterpret_cast<const f32x4*>(p)[1];
+    return T{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  }
+  __device__ static __forceinline__ T pack(const float* p) {
+    return T{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+  }
+};
+
+// Shape of an instantiation.
+template <typename E, int D, int QT, int WQ, int WK>
+struct Shape {
+  static_assert(WQ * WK * kWave == kThreads, "four waves");
+  static constexpr int kMT = 16 * QT * WQ;           // queries of an item
+  static constexpr int kTile = WK * kSlice;          // tokens of a tile
+  static constexpr int kRowBytes = D * static_cast<int>(sizeof(E));
+  static constexpr int kChunks = kRowBytes / 16;     // 16-byte chunks of a token's row
+  static constexpr int kSliceBytes = kSlice * kRowBytes;
+  static constexpr int kLoads = kSliceBytes / 16 / (kWave * WQ);   // chunks a lane stages of K (and of V)
+  static constexpr int kOut = 64;                    // columns of O joined at a time
+  static constexpr int kOutStride = kOut + 4;
+};
+
+template <typename E, int D, int QT, int WQ, int WK>
+struct AttnScratch {
+  using S = Shape<E, D, QT, WQ, WK>;
+  union {
+    struct {
+      uint32_t k[WK][S::kSliceBytes / 4];
+      uint32_t v[WK][S::kSliceBytes / 4];
+    } tile;
+    float join[WK][S::kMT][S::kOutStride];
+  };
+  float ml[WK][S::kMT][2];
+  float fin[S::kMT][2];
+  uint64_t path[VSV_MAX_TREE_ROWS];
+  int64_t scan[kThreads / kWave];
+  int64_t base;
+  int request;
+  int odd;   // a value among the rows' own is not finite
+};
+
+// Where chunk c of token row r lies in its slice. Rows are 128 bytes or more
+// apart, so lanes that read one column of many rows would meet in the same
+// banks: the chunks of a row are permuted by an exclusive or. Keys are read
+// 16 rows at a time, a chunk each; values 8 rows of two chunks (bfloat16,
+// transposed) or 4 rows, four apart, of four chunks (float32).
+template <int C>
+__device__ __forceinline__ int swizzle_k(int r) {
+  return C == 8 ? (r >> 1) & 7 : r & 15;
+}
+template <typename E, int C>
+__device__ __forceinline__ int swizzle_v(int r) {
+  if (sizeof(E) == 4) return 4 * ((r >> 2) & 3);
+  return C == 8 ? 2 * ((r >> 1) & 3) : 2 * (r & 7);
+}
+
+__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* scratch, int64_t& total) {
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int64_t incl = wave_scan_incl(v);
+  lds_barrier();
+  if (lane == kWave - 1) scratch[w] = incl;
+  lds_barrier();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int k = 0; k < kThreads / kWave; ++k) {
+    const int64_t s = scratch[k];
+    before += k < w ? s : 0;
+    total += s;
+  }
+  return before + incl - v;
+}
+
+struct Request {
+  int r0, n, len, tiles, blocks;   // rows, context, tiles of an item, blocks of queries
+};
+
+template <typename S>
+__device__ __forceinline__ Request request_of(const AttentionArgs& a, int i, bool& bad) {
+  const int r0 = a.offsets[i], r1 = a.offsets[i + 1], len = a.length[i];
+  const int64_t room = static_cast<int64_t>(a.table_width) << a.page_shift;
+  bad = r0 < 0 || r1 < r0 || r1 > a.R || r1 - r0 > VSV_MAX_TREE_ROWS || len < 0 || len > room;
+  Request q{r0, r1 - r0, len, 0, 0};
+  if (bad) q.n = 0;
+  if (q.n > 0) {
+    q.tiles = static_cast<int>((static_cast<int64_t>(len) + q.n + S::kTile - 1) / S::kTile);
+    q.blocks = (q.n * a.G + S::kMT - 1) / S::kMT;
+  }
+  return q;
+}
+
+// Start of a worker's span in a list of `units`; no more workers than units,
+// so that every span holds something.
+__device__ __forceinline__ int64_t span_start(int64_t units, int w, int workers) {
+  return units * w / workers;
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t two, std::integral_constant<int, 2>) {
+  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool not_finite(uint32_t one, std::integral_constant<int, 4>) {
+  return (one & 0x7F800000u) == 0x7F800000u;
+}
+
+// LDS written by this wave and read by its other lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <typename E, int D, int QT, int WQ, int WK>
+__global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
+  using S = Shape<E, D, QT, WQ, WK>;
+  using F = Frag<E>;
+  constexpr int C = S::kChunks;
+  constexpr int KC = D / 32;    // inner steps of K Q^T
+  constexpr int DT = D / 16;    // row blocks of O^T
+  __shared__ AttnScratch<E, D, QT, WQ, WK> s;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int wq = wave % WQ, wk = wave / WQ;
+  const int col = lane & 15, grp = lane >> 4;
+  const int w = blockIdx.x;
+  int bits = 0;
+
+  // ---- this worker's span
+  int64_t units = 0;
+  for (int base = 0; base < a.B; base += kThreads) {
+    const int i = base + tid;
+    int64_t mine = 0;
+    if (i < a.B) {
+      bool bad;
+      const Request q = request_of<S>(a, i, bad);
+      if (bad) bits |= VSV_FLAG_LAYOUT;
+      mine = static_cast<int64_t>(a.KV) * q.blocks * q.tiles;
+    }
+    int64_t total;
+    block_scan64(mine, s.scan, total);
+    units += total;
+  }
+  if (tid == 0) a.piece[4 * w] = -1;
+  if (w == 0 && bits && a.error_flag) atomicOr(a.error_flag, bits);
+  bits = 0;
+  const int workers = static_cast<int>(min(static_cast<int64_t>(a.workers), units));
+  if (w >= workers) return;
+  const int64_t u0 = span_start(units, w, workers), u1 = span_start(units, w + 1, workers);
+  int64_t seen = 0;
+  for (int base = 0; base < a.B; base += kThreads) {
+    const int i = base + tid;
+    int64_t mine = 0;
+    if (i < a.B) {
+      bool bad;
+      const Request q = request_of<S>(a, i, bad);
+      mine = static_cast<int64_t>(a.KV) * q.blocks * q.tiles;
+    }
+    int64_t total;
+    const int64_t before = seen + block_scan64(mine, s.scan, total);
+    if (before <= u0 && u0 < before + mine) {
+      s.request = i;
+      s.base = before;
+    }
+    seen += total;
+    if (seen > u0) break;
+  }
+  lds_barrier();
+  int i = s.request;
+  int64_t base = s.base;
+
+  // ---- the items of the span
+  for (int64_t u = u0; u < u1;) {
+    bool bad;
+    const Request rq = request_of<S>(a, i, bad);
+    const int64_t size = static_cast<int64_t>(a.KV) * rq.blocks * rq.tiles;
+    if (u >= base + size) {
+      base += size;
+      ++i;
+      continue;
+    }
+    const uint32_t rel = static_cast<uint32_t>(u - base);
+    const int item = static_cast<int>(rel / static_cast<uint32_t>(rq.tiles));
+    const int t0 = static_cast<int>(rel) - item * rq.tiles;
+    const int h = item / rq.blocks, mt = item - h * rq.blocks;
+    const int t1 = static_cast<int>(min(static_cast<int64_t>(rq.tiles), t0 + (u1 - u)));
+    u += t1 - t0;
+
+    const int r0 = rq.r0, n = rq.n, len = rq.len, end = len + n;
+    const int M = min(n * a.G - mt * S::kMT, S::kMT);   // queries of this block
+
+    // the rows' paths
+    if (wave == 0) {
+      const int up = a.parents && lane < n ? a.parents[r0 + lane] : 0;
+      bool off_tree;
+      s.path[lane] = tree_paths(lane, n, up, a.parents == nullptr, off_tree);
+      if (off_tree) bits |= VSV_FLAG_LAYOUT;
+      if (lane == 0) s.odd = 0;
+    }
+    lds_barrier();
+
+    // ---- queries
+    typename F::T qf[QT][KC];
+    uint64_t path[QT];
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      const int m = (wq * QT + qt) * 16 + col;
+      const bool live = m < M;
+      const int at = mt * S::kMT + (live ? m : 0);
+      const int j = at / a.G, hq = h * a.G + (at - j * a.G);
+      const E* p = static_cast<const E*>(a.q) + (r0 + j) * a.q_row + hq * a.q_head + grp * 8;
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc) qf[qt][kc] = live ? F::load(p + kc * 32) : F::zero();
+      path[qt] = live ? s.path[j] : 0;
+    }
+
+    f32x4 acc[DT][QT];
+    float mref[QT], mc[QT], l[QT];   // reference, times the scale (0 while there is none), weights so far
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      mref[qt] = -INFINITY;
+      mc[qt] = 0.f;
+      l[qt] = 0.f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) acc[dt][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // ---- staging: chunk c of the slice is chunk c % C of its token c / C
+    u32x4 ks[S::kLoads], vs[S::kLoads];
+    const char* kc_base = static_cast<const char*>(a.k_cache) + h * a.c_head * static_cast<int64_t>(sizeof(E));
+    const char* vc_base = static_cast<const char*>(a.v_cache) + h * a.c_head * static_cast<int64_t>(sizeof(E));
+    const int32_t* row_table = a.table + static_cast<int64_t>(i) * a.table_ld;
+    const int page_mask = (1 << a.page_shift) - 1;
+    const int slot0 = wq * kWave + lane;   // this lane's first chunk
+    // lane x of the wave looks up the page of token x of the slice
+    auto look_up = [&](int t) -> int {
+      const int x = t * S::kTile + wk * kSlice + (lane & (kSlice - 1));
+      int id = 0;
+      if (x < len) {
+        id = row_table[x >> a.page_shift];
+        if (id < 0 || id >= a.num_pages) {
+          bits |= VSV_FLAG_PAGES;
+          id = 0;
+        }
+      }
+      return id;
+    };
+    auto fetch = [&](int t, int ids) {
+#pragma unroll
+      for (int k = 0; k < S::kLoads; ++k) {
+        const int c = slot0 + k * kWave * WQ;
+        const int row = c / C, chunk = c % C;
+        const int x = t * S::kTile + wk * kSlice + row;
+        const int id = __shfl(ids, row);
+        ks[k] = vs[k] = u32x4{0, 0, 0, 0};
+        if (x < len) {
+          const int64_t at = (id * a.c_page + (x & page_mask) * a.c_token) * static_cast<int64_t>(sizeof(E)) + chunk * 16;
+          ks[k] = *reinterpret_cast<const u32x4*>(kc_base + at);
+          vs[k] = *reinterpret_cast<const u32x4*>(vc_base + at);
+        } else if (x < end) {
+          const int64_t r = r0 + (x - len);
+          ks[k] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.k) +
+                                                  (r * a.k_row + h * a.k_head) * static_cast<int64_t>(sizeof(E)) + chunk * 16);
+          vs[k] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.v) +
+                                                  (r * a.v_row + h * a.v_head) * static_cast<int64_t>(sizeof(E)) + chunk * 16);
+        }
+      }
+    };
+    char* kl = reinterpret_cast<char*>(s.tile.k[wk]);
+    char* vl = reinterpret_cast<char*>(s.tile.v[wk]);
+    auto put = [&](int t) {
+#pragma unroll
+      for (int k = 0; k < S::kLoads; ++k) {
+        const int c = slot0 + k * kWave * WQ;
+        const int row = c / C, chunk = c % C;
+        // a value that is not finite would reach rows that do not see it
+        // through a weight of 0: it is taken out here and added behind
+        if (t * S::kTile + wk * kSlice + row >= len) {
+          bool odd = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) odd |= not_finite(vs[k][e], std::integral_constant<int, sizeof(E)>());
+          if (odd) {
+            s.odd = 1;
+            if (sizeof(E) == 2) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((vs[k][e] & 0x7F80u) == 0x7F80u) vs[k][e] &= 0xFFFF0000u;
+                if ((vs[k][e] & 0x7F800000u) == 0x7F800000u) vs[k][e] &= 0xFFFFu;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((vs[k][e] & 0x7F800000u) == 0x7F800000u) vs[k][e] = 0;
+            }
+          }
+        }
+        *reinterpret_cast<u32x4*>(kl + (row * C + (chunk ^ swizzle_k<C>(row))) * 16) = ks[k];
+        *reinterpret_cast<u32x4*>(vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16) = vs[k];
+      }
+    };
+    auto sync = [&]() {
+      if (WQ > 1)
+        lds_barrier();
+      else
+        wave_sync();
+    };
+
+    int ids = look_up(t0);
+    fetch(t0, ids);
+    ids = t0 + 1 < t1 ? look_up(t0 + 1) : 0;
+    for (int t = t0; t < t1; ++t) {
+      sync();   // the slice has been read
+      put(t);
+      sync();
+      if (t + 1 < t1) {
+        fetch(t + 1, ids);
+        if (t + 2 < t1) ids = look_up(t + 2);
+      }
+      const int x0 = t * S::kTile + wk * kSlice;
+      if (x0 >= end) continue;   // the wave's slice lies behind the last token (no barrier below)
+
+      // S^T of two halves of 16 tokens
+      f32x4 sc[2][QT];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) sc[hf][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int row = hf * 16 + col;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+          typename F::T kf;
+          if constexpr (sizeof(E) == 2) {
+            kf = *reinterpret_cast<const bf16x8*>(kl + (row * C + ((kc * 4 + grp) ^ swizzle_k<C>(row))) * 16);
+          } else {
+            const int c0 = kc * 8 + grp * 2, z = swizzle_k<C>(row);
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(kl + (row * C + (c0 ^ z)) * 16);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(kl + (row * C + ((c0 + 1) ^ z)) * 16);
+            kf = f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          }
+#pragma unroll
+          for (int qt = 0; qt < QT; ++qt) sc[hf][qt] = F::mma(kf, qf[qt][kc], sc[hf][qt]);
+        }
+      }
+      // tokens from the tree on: only the row's path is seen
+      if (x0 + kSlice > len) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = x0 + hf * 16 + grp * 4 + e - len;
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) {
+              const bool sees = at < 0 || (at < n && (path[qt] >> (at & 63) & 1));
+              sc[hf][qt][e] = sees ? sc[hf][qt][e] : -INFINITY;
+            }
+          }
+      }
+      // The reference moves only where a score passes it by more than kSlack
+      // in log2: weights stay below 2^kSlack, and most tiles skip the
+      // reduction across lanes and the rescaling.
+      constexpr float kSlack = 8.f;
+      typename F::T pf[QT];
+      bool move = false;
+      float top[QT];
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) {
+        float b = sc[0][qt][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) b = fmaxf(b, sc[e >> 2][qt][e & 3]);
+        top[qt] = b;
+        move |= b * a.scale > mref[qt] * a.scale + kSlack;   // false while both are -inf
+      }
+      if (__builtin_amdgcn_ballot_w64(move)) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+          float b = fmaxf(top[qt], mref[qt]);
+          b = fmaxf(b, __shfl_xor(b, 16));
+          b = fmaxf(b, __shfl_xor(b, 32));
+          const float f = b == mref[qt] ? 1.f : fast_exp2((mref[qt] - b) * a.scale);
+          mref[qt] = b;
+          mc[qt] = b == -INFINITY ? 0.f : b * a.scale;
+          l[qt] *= f;
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) acc[dt][qt] *= f;
+        }
+      }
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = fast_exp2(fmaf(sc[e >> 2][qt][e & 3], a.scale, -mc[qt]));
+          l[qt] += p[e];
+        }
+        pf[qt] = F::pack(p);
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        typename F::T vf;
+        if constexpr (sizeof(E) == 2) {
+          s16x4 half[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int row = hf * 16 + grp * 4 + (col >> 2);
+            const int chunk = dt * 2 + ((col & 3) >> 1);
+            const char* p = vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16 + (col & 1) * 8;
+            half[hf] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(const_cast<char*>(p)));
+          }
+          vf = __builtin_bit_cast(bf16x8, s16x8{half[0][0], half[0][1], half[0][2], half[0][3], half[1][0], half[1][1],
+                                                half[1][2], half[1][3]});
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int row = (e >> 2) * 16 + grp * 4 + (e & 3);
+            const int chunk = dt * 4 + (col >> 2);
+            vf[e] = *reinterpret_cast<const float*>(vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16 + (col & 3) * 4);
+          }
+        }
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) acc[dt][qt] = F::mma(vf, pf[qt], acc[dt][qt]);
+      }
+      if (x0 + kSlice > len && s.odd) {
+        for (int x = max(x0, len); x < min(x0 + kSlice, end); ++x) {
+          const E* p = static_cast<const E*>(a.v) + static_cast<int64_t>(r0 + x - len) * a.v_row + h * a.v_head;
+          for (int dt = 0; dt < DT; ++dt)
+            for (int e = 0; e < 4; ++e) {
+              const float f = Elem<E>::at(p, dt * 16 + grp * 4 + e);
+              if (!(fabsf(f) < INFINITY)) {
+#pragma unroll
+                for (int d2 = 0; d2 < DT; ++d2)
+#pragma unroll
+                  for (int e2 = 0; e2 < 4; ++e2)
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt)
+                      if (d2 == dt && e2 == e && (path[qt] >> (x - len) & 1)) acc[d2][qt][e2] += f;
+              }
+            }
+        }
+      }
+    }
+
+    // ---- join the slices, then the item's result or piece
+    const bool whole = t0 == 0 && t1 == rq.tiles;
+    const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      l[qt] += __shfl_xor(l[qt], 16);
+      l[qt] += __shfl_xor(l[qt], 32);
+      if (grp == 0) {
+        const int q = (wq * QT + qt) * 16 + col;
+        s.ml[wk][q][0] = mref[qt];
+        s.ml[wk][q][1] = l[qt];
+      }
+    }
+    lds_barrier();
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      const int q = (wq * QT + qt) * 16 + col;
+      float m = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < WK; ++k) m = fmaxf(m, s.ml[k][q][0]);
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        const float mk = s.ml[k][q][0];
+        sum += mk == -INFINITY ? s.ml[k][q][1] : s.ml[k][q][1] * fast_exp2((mk - m) * a.scale);
+      }
+      const float f = mref[qt] == -INFINITY ? 1.f : fast_exp2((mref[qt] - m) * a.scale);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) acc[dt][qt] *= f;
+      if (grp == 0 && wk == 0) {
+        s.fin[q][0] = m * a.scale;
+        s.fin[q][1] = sum;
+      }
+    }
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += S::kOut) {
+      lds_barrier();   // tiles, or the columns before, have been read
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+        for (int dt = 0; dt < S::kOut / 16; ++dt)
+          *reinterpret_cast<f32x4*>(&s.join[wk][(wq * QT + qt) * 16 + col][dt * 16 + grp * 4]) = acc[d0 / 16 + dt][qt];
+      lds_barrier();
+      constexpr int kQuads = S::kOut / 4;
+      for (int c = tid; c < M * kQuads; c += kThreads) {
+        const int q = c / kQuads, d = (c % kQuads) * 4;
+        f32x4 o = *reinterpret_cast<const f32x4*>(&s.join[0][q][d]);
+#pragma unroll
+        for (int k = 1; k < WK; ++k) o += *reinterpret_cast<const f32x4*>(&s.join[k][q][d]);
+        if (whole) {
+          const float sum = s.fin[q][1];
+          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN stays one
+          const int at = mt * S::kMT + q, j = at / a.G, hq = h * a.G + (at - j * a.G);
+          E* p = static_cast<E*>(a.out) + (r0 + j) * a.o_row + hq * a.o_head + d0 + d;
+          if constexpr (sizeof(E) == 2) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            bf16x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = static_cast<__bf16>(o[e] * inv);
+            *reinterpret_cast<bf16x4*>(p) = y;
+          } else {
+            *reinterpret_cast<f32x4*>(p) = o * inv;
+          }
+        } else {
+          *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(slot) * S::kMT + q) * D + d0 + d) = o;
+        }
+      }
+    }
+    if (whole) {
+      if (a.lse)
+        for (int q = tid; q < M; q += kThreads) {
+          const int at = mt * S::kMT + q, j = at / a.G, hq = h * a.G + (at - j * a.G);
+          a.lse[static_cast<int64_t>(r0 + j) * a.H + hq] = 0.69314718f * (s.fin[q][0] + __log2f(s.fin[q][1]));
+        }
+    } else {
+      for (int q = tid; q < M; q += kThreads) {
+        a.part_ml[(static_cast<int64_t>(slot) * S::kMT + q) * 2] = s.fin[q][0];
+        a.part_ml[(static_cast<int64_t>(slot) * S::kMT + q) * 2 + 1] = s.fin[q][1];
+      }
+      if (t0 == 0 && tid == 0) {
+        // the worker whose span holds the item's last tile
+        const int64_t last = u - 1 + (rq.tiles - t1);
+        int w1 = static_cast<int>(((last + 1) * workers - 1) / units);
+        while (span_start(units, w1 + 1, workers) <= last) ++w1;
+        while (span_start(units, w1, workers) > last) --w1;
+        a.piece[4 * w] = i;
+        a.piece[4 * w + 1] = h;
+        a.piece[4 * w + 2] = mt;
+        a.piece[4 * w + 3] = w1;
+      }
+    }
+    lds_barrier();   // paths and joined columns are free again
+  }
+  if (bits && a.error_flag) atomicOr(a.error_flag, bits);
+}
+
+// Joins the pieces of the items that no worker finished: a wave per query.
+constexpr int kJoinQueries = kThreads / kWave;
+
+template <typename E, int D, int MT>
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int w = static_cast<int>(blockIdx.x) / (MT / kJoinQueries);
+  const int q = static_cast<int>(blockIdx.x) % (MT / kJoinQueries) * kJoinQueries + static_cast<int>(threadIdx.x) / kWave;
+  const int i = a.piece[4 * w];
+  if (i < 0) return;
+  const int h = a.piece[4 * w + 1], mt = a.piece[4 * w + 2], w1 = a.piece[4 * w + 3];
+  const int r0 = a.offsets[i], n = a.offsets[i + 1] - r0;
+  const int at = mt * MT + q;
+  if (at >= n * a.G) return;
+  constexpr int N = D / kWave;
+  float o[N] = {};
+  float m = -INFINITY, sum = 0.f;
+  auto slot_of = [&](int x) { return static_cast<int64_t>(x == w ? 2 * w + 1 : 2 * x); };
+  for (int x0 = w; x0 <= w1; x0 += kWave) {
+    float mk = -INFINITY, lk = 0.f;
+    if (x0 + lane <= w1) {
+      const float* ml = a.part_ml + (slot_of(x0 + lane) * MT + q) * 2;
+      mk = ml[0];
+      lk = ml[1];
+    }
+    const float top = fmaxf(m, wave_all(mk, MaxOp()));
+    const float old = m == -INFINITY ? 1.f : fast_exp2(m - top);
+    const float f = mk == -INFINITY ? 1.f : fast_exp2(mk - top);
+    sum = sum * old + wave_all(lk * f, SumOp());
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] *= old;
+    m = top;
+    const int count = min(kWave, w1 - x0 + 1);
+    for (int x = 0; x < count; ++x) {
+      const float* p = a.part + (slot_of(x0 + x) * MT + q) * D;
+      const float fx = __shfl(f, x);
+#pragma unroll
+      for (int k = 0; k < N; ++k) o[k] += fx * p[k * kWave + lane];
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  const int j = at / a.G, hq = h * a.G + (at - j * a.G);
+  E* p = static_cast<E*>(a.out) + (r0 + j) * a.o_row + hq * a.o_head;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if constexpr (sizeof(E) == 2)
+      reinterpret_cast<__bf16*>(p)[k * kWave + lane] = static_cast<__bf16>(o[k] * inv);
+    else
+      p[k * kWave + lane] = o[k] * inv;
+  }
+  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(r0 + j) * a.H + hq] = 0.69314718f * (m + __log2f(sum));
+}
+
+// ---- launch
+
+// Blocks of queries: the smallest one that holds an average request's
+// queries of a key head, so that its keys are read once.
+struct Plan {
+  int mt, tile;
+};
+Plan plan_of(const AttentionArgs& a) {
+  const int64_t mean = (static_cast<int64_t>(a.R) + a.B - 1) / a.B;
+  const int64_t m = mean * (a.H / a.KV);
+  const bool narrow = a.dtype == VSV_F32 || a.D > 128;   // two query tiles a wave
+  if (m <= 16) return {16, 128};
+  if (m <= 32) return {32, 128};
+  if (m <= 64) return narrow ? Plan{64, 64} : Plan{64, 128};
+  if (narrow || m <= 128) return narrow ? Plan{128, 32} : Plan{128, 64};
+  return {256, 32};
+}
+int workers_of(const AttentionArgs& a) { return a.cus > 0 ? a.cus : 256; }
+
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+template <typename E, int D, int QT, int WQ, int WK>
+hipError_t launch_t(AttentionArgs a, hipStream_t s) {
+  using S = Shape<E, D, QT, WQ, WK>;
+  a.G = a.H / a.KV;
+  a.workers = workers_of(a);
+  char* p = static_cast<char*>(a.work);
+  a.piece = reinterpret_cast<int32_t*>(p);
+  p += align256(static_cast<size_t>(a.workers) * 16);
+  a.part_ml = reinterpret_cast<float*>(p);
+  p += align256(static_cast<size_t>(a.workers) * 2 * S::kMT * 8);
+  a.part = reinterpret_cast<float*>(p);
+  attention_kernel<E, D, QT, WQ, WK><<<dim3(a.workers), dim3(kThreads), 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  attention_join_kernel<E, D, S::kMT><<<dim3(a.workers * (S::kMT / kJoinQueries)), dim3(kThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename E, int D>
+hipError_t launch_d(const AttentionArgs& a, hipStream_t s) {
+  const Plan p = plan_of(a);
+  if constexpr (sizeof(E) == 4 || D > 128) {
+    switch (p.mt) {
+      case 16: return launch_t<E, D, 1, 1, 4>(a, s);
+      case 32: return launch_t<E, D, 2, 1, 4>(a, s);
+      case 64: return launch_t<E, D, 2, 2, 2>(a, s);
+    }
+    return launch_t<E, D, 2, 4, 1>(a, s);
+  } else {
+    switch (p.mt) {
+      case 16: return launch_t<E, D, 1, 1, 4>(a, s);
+      case 32: return launch_t<E, D, 2, 1, 4>(a, s);
+      case 64: return launch_t<E, D, 4, 1, 4>(a, s);
+      case 128: return launch_t<E, D, 4, 2, 2>(a, s);
+    }
+    return launch_t<E, D, 4, 4, 1>(a, s);
+  }
+}
+
+}  // namespace
+
+int64_t attention_tiles(const AttentionArgs& a) {
+  const Plan p = plan_of(a);
+  const int64_t tokens = (static_cast<int64_t>(a.table_width) << a.page_shift) + VSV_MAX_TREE_ROWS;
+  const int64_t blocks = (static_cast<int64_t>(VSV_MAX_TREE_ROWS) * (a.H / a.KV) + p.mt - 1) / p.mt;
+  const int64_t tiles = (tokens + p.tile - 1) / p.tile;
+  if (tiles > (int64_t{1} << 40) / blocks / a.KV) return INT64_MAX;
+  return tiles * blocks * a.KV;
+}
+
+size_t attention_workspace(const AttentionArgs& a) {
+  const Plan p = plan_of(a);
+  const size_t w = static_cast<size_t>(workers_of(a));
+  return align256(w * 16) + align256(w * 2 * p.mt * 8) + align256(w * 2 * p.mt * a.D * 4);
+}
+
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
+  if (a.dtype == VSV_BF16) {
+    if (a.D == 64) return launch_d<uint16_t, 64>(a, s);
+    if (a.D == 128) return launch_d<uint16_t, 128>(a, s);
+    return launch_d<uint16_t, 256>(a, s);
+  }
+  return a.D == 64 ? launch_d<float, 64>(a, s) : launch_d<float, 128>(a, s);
+}
+
+}  // namespace vsv

@@ -433,6 +433,69 @@ vsv_status vsv_allocate_verify(const float* confidence, const int32_t* draft_tok
                                int32_t* row_source, int32_t* packed_drafts, float* prefix,
                                hipStream_t stream);
 
+/* Attention of packed draft rows over a paged cache: the target's (or a draft
+ * model's) attention in the forward pass whose logits are verified. Rows are
+ * packed as in vsv_batch; row r of request i sees the request's length[i]
+ * cached tokens, the rows on its path from the root of its tree (parents as
+ * in vsv_verify_greedy_tree, NULL: chains) and itself:
+ *   out[r, h] = sum_t p_t v_t,  p = softmax over the seen t of scale q[r, h] . k_t
+ * with key head h / (num_heads / num_kv_heads). The rows' own keys and values
+ * are given beside q and need not be in the cache: those of accepted rows are
+ * stored after verification (out_rows and vsv_plan_pages), so a rejected
+ * draft never holds a slot. What a row does not see cannot reach it, infinite
+ * and NaN values included. Scores, softmax and sums are float32; with bfloat16
+ * the weights are rounded to bfloat16 for their product with the values.
+ * Serving only: there is no backward pass. */
+#define VSV_MAX_TREE_REQUESTS 65536
+typedef struct {
+  const void* q;              /* [num_rows, num_heads, head_dim]                        */
+  const void* k;              /* [num_rows, num_kv_heads, head_dim]                     */
+  const void* v;
+  const void* k_cache;        /* [num_pages, page_size, num_kv_heads, head_dim]         */
+  const void* v_cache;        /* the same strides as k_cache                            */
+  void* out;                  /* [num_rows, num_heads, head_dim], no other's memory     */
+  float* lse;                 /* [num_rows, num_heads] log-sum-exp of the seen scores   */
+                              /* (natural, scaled), or NULL                             */
+  /* strides in elements (the last dimension's is 1): of rows and heads, and   */
+  /* of the caches' pages, tokens and heads; every pointer and every stride in */
+  /* bytes is a multiple of 16                                                 */
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
+  int64_t cache_page, cache_token, cache_head;
+  int32_t dtype;              /* vsv_dtype of every matrix                              */
+  int32_t head_dim;           /* 64, 128, or 256 (bfloat16 alone)                       */
+  int32_t num_heads;          /* a multiple of num_kv_heads                             */
+  int32_t num_kv_heads;
+  int32_t num_requests;       /* 0 .. VSV_MAX_TREE_REQUESTS                             */
+  int32_t num_rows;           /* R >= 0                                                 */
+  const int32_t* row_offsets; /* [B + 1], not falling, within 0 .. R; at most           */
+                              /* VSV_MAX_TREE_ROWS rows a request, which may have none; */
+                              /* rows at or beyond off[B] are left as they are          */
+  const int32_t* parents;     /* [R] or NULL                                            */
+  const int32_t* length;      /* [B] tokens of each request in the cache, may be 0      */
+  const int32_t* block_table; /* [B, table_ld] pages of each request                    */
+  int64_t table_ld;
+  int32_t table_width;        /* pages a request may have                               */
+  int32_t num_pages;          /* of the cache                                           */
+  int32_t page_size;          /* tokens of a page, a power of two                       */
+  float scale;                /* positive and finite, times log2(e) too                 */
+} vsv_attention;
+
+/* `workspace`: scratch of vsv_tree_attention_workspace_bytes bytes (256-byte
+ * aligned; of the struct it reads sizes and types alone, 0 for an invalid one).
+ * It needs no initial value and nothing in it outlives the call; calls that
+ * may overlap in time need scratch of their own. Results do not
+ * depend on anything but the inputs and the device's number of CUs.
+ * VSV_FLAG_LAYOUT: offsets, lengths (beyond table_width pages) or row counts
+ * outside their range (the request's rows are left as they are), or a parent that is
+ * no earlier row (the row then sees the context and itself alone);
+ * VSV_FLAG_PAGES: a page outside 0 .. num_pages - 1 (page 0 is read for it).
+ * Errors: VSV_EINVAL (NULL pointers, sizes, strides, alignment, dtype, scale;
+ * table_width * page_size so large that a request's work passes 2^31 tiles of
+ * 32 tokens), VSV_EWORKSPACE, VSV_EHIP. */
+size_t vsv_tree_attention_workspace_bytes(const vsv_attention* a);
+vsv_status vsv_tree_attention(const vsv_attention* a, int32_t* error_flag, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
 /* Penalties, biases and grammar masks on packed rows of logits, before they
  * are verified or drawn from. Row r of request i stands behind a path of
  * drafts (in a chain the drafts before it; with `parents`, those from the

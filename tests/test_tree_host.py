@@ -96,3 +96,39 @@ def test_binding_refusals():
         vsv.adjust_logits(cpu, i(2), i(3))
     with pytest.raises(ValueError):
         vsv.plan_pages(i(4).view(1, 4), i(1), i(1), i(2), i(9), i(1), 16, 4)
+
+
+def _attention(L, ws=0x100000, wsn=1 << 30, **kw):
+    a = dict(q=0x1000, k=0x2000, v=0x3000, k_cache=0x4000, v_cache=0x5000, out=0x6000, q_row=1024, q_head=128, k_row=256,
+             k_head=128, v_row=256, v_head=128, out_row=1024, out_head=128, cache_page=4096, cache_token=256,
+             cache_head=128, dtype=1, head_dim=128, num_heads=8, num_kv_heads=2, num_requests=4, num_rows=20,
+             row_offsets=8, length=8, block_table=8, table_ld=16, table_width=16, num_pages=64, page_size=16, scale=0.1)
+    a.update(kw)
+    return L.vsv_tree_attention(ctypes.byref(vsv.Attention(**a)), None, P(ws) if ws else None, wsn, None)
+
+
+@pytest.mark.parametrize("bad", [dict([(k, None)]) for k in ("q", "k", "v", "k_cache", "v_cache", "out", "row_offsets",
+                                                            "length", "block_table")] +
+                         [dict([(k, 0x1008)]) for k in ("q", "k", "v", "k_cache", "v_cache", "out")] +
+                         [dict([(k, 4)]) for k in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head", "out_row",
+                                                   "out_head", "cache_page", "cache_token", "cache_head")] +
+                         [dict([(k, -8)]) for k in ("q_row", "cache_page")] + [dict([(k, 1 << 62)]) for k in ("k_row", "cache_page")] + [
+    dict(dtype=2), dict(head_dim=96), dict(dtype=0, head_dim=256), dict(num_heads=9), dict(num_kv_heads=0),
+    dict(num_heads=0), dict(num_heads=131072), dict(num_requests=-1), dict(num_requests=65537), dict(num_rows=-1), dict(table_ld=15),
+    dict(table_ld=1 << 62), dict(table_width=0), dict(num_pages=0), dict(page_size=0), dict(page_size=24),
+    dict(table_width=1 << 28, table_ld=1 << 28), dict(table_width=1 << 26, table_ld=1 << 26, num_heads=8192,
+                                                       num_kv_heads=8192), dict(scale=0.0), dict(scale=-1.0),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38)])
+def test_attention_refusals(L, bad):
+    assert _attention(L, **bad) == 1
+
+
+def test_attention_scratch_and_noops(L):
+    assert _attention(L, ws=0) == 3
+    assert _attention(L, ws=0x100080) == 3
+    assert _attention(L, wsn=1000) == 3
+    assert _attention(L, num_rows=0, q=None) == 0
+    assert _attention(L, num_requests=0, q=None) == 0
+    assert L.vsv_tree_attention(None, None, None, 0, None) == 1
+    assert L.vsv_tree_attention_workspace_bytes(None) == 0
+    assert L.vsv_tree_attention_workspace_bytes(ctypes.byref(vsv.Attention(dtype=5))) == 0
