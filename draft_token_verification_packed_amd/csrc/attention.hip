@@ -17,7 +17,7 @@
 // each half of a 32-token slice, and V^T is read from LDS in the same order
 // (bfloat16 through the transposing LDS read).
 //
-// Work: a tile is WK * 32 tokens of one (request, key head, block of MT
+// Work: a tile is WK slices of tokens of one (request, key head, block of MT
 // queries), an item the tiles of one such triple. The tiles of the whole
 // batch form one list, cut into equal spans, one per workgroup, whatever the
 // requests' lengths: each workgroup finds its span with a scan over the requests.
@@ -27,6 +27,7 @@
 // to different waves, joined through LDS at the end of an item. With few
 // queries (WQ = 1) waves share nothing and meet no barrier in the loop.
 #include <type_traits>
+#include <utility>
 
 #include "attention.hpp"
 #include "tree.hpp"
@@ -87,11 +88,24 @@ template <typename E, int D, int QT, int WQ, int WK>
 struct Shape {
   static_assert(WQ * WK * kWave == kThreads, "four waves");
   static constexpr int kMT = 16 * QT * WQ;           // queries of an item
-  static constexpr int kTile = WK * kSlice;          // tokens of a tile
+  static constexpr int kSub = WK == 1 ? 2 : 1;       // steps of a slice: fewer barriers where waves share it
+  static constexpr int kTokens = kSlice * kSub;      // tokens of a slice
+  static constexpr int kTile = WK * kTokens;         // tokens of a tile
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(E));
   static constexpr int kChunks = kRowBytes / 16;     // 16-byte chunks of a token's row
-  static constexpr int kSliceBytes = kSlice * kRowBytes;
-  static constexpr int kLoads = kSliceBytes / 16 / (kWave * WQ);   // chunks a lane stages of K (and of V)
+  static constexpr int kSliceBytes = kTokens * kRowBytes;
+  static constexpr int kLoads = kSliceBytes / 16 / (kWave * WQ);   // chunks a lane brings of K (and of V)
+  // workgroups of few queries share a CU, which hides what each does between
+  // its items; buffers: two where the LDS holds them
+  static constexpr int kGroups = QT <= 2 && WK * kSliceBytes <= 32 * 1024 ? 2 : 1;
+  static constexpr int kStages = kGroups * WK * kSliceBytes * 4 <= 128 * 1024 ? 2 : 1;
+  static_assert(kLoads <= (kChunks == 8 ? 8 : 16), "a lane of 16 for every load");
+  // The row of the slice whose place lane (grp, col) of wave wq works out.
+  __device__ static __forceinline__ int owned_row(int wq, int grp, int col) {
+    return kChunks == 8    ? wq * 8 + 2 * grp + (col & 1) + (col >> 1) * 8 * WQ
+           : kChunks == 16 ? wq * 4 + grp + col * 4 * WQ
+                           : wq * 2 + (grp >> 1) + col * 2 * WQ;
+  }
   static constexpr int kOut = 64;                    // columns of O joined at a time
   static constexpr int kOutStride = kOut + 4;
 };
@@ -101,9 +115,9 @@ struct AttnScratch {
   using S = Shape<E, D, QT, WQ, WK>;
   union {
     struct {
-      uint32_t k[WK][S::kSliceBytes / 4];
-      uint32_t v[WK][S::kSliceBytes / 4];
-    } tile;
+      uint32_t k[S::kSliceBytes / 4];
+      uint32_t v[S::kSliceBytes / 4];
+    } tile[S::kStages][WK];
     float join[WK][S::kMT][S::kOutStride];
   };
   float ml[WK][S::kMT][2];
@@ -178,6 +192,46 @@ __device__ __forceinline__ bool not_finite(uint32_t one, std::integral_constant<
   return (one & 0x7F800000u) == 0x7F800000u;
 }
 
+// A load of 16 bytes a lane straight into LDS, at `to` + 16 * lane. The
+// compiler makes every later LDS read wait for its own form of this load, the
+// reads of the other buffer included; here the wait is wait_loads() alone.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+__device__ __forceinline__ void load_to_lds(int64_t from, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(to), "v"(from)
+      : "memory");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+template <int... K, typename F>
+__device__ __forceinline__ void for_each_index(std::integer_sequence<int, K...>, F&& f) {
+  (f(std::integral_constant<int, K>()), ...);
+}
+
+// The value of lane K of the lane's group of 16; for rows of 8 chunks, of
+// lane 2 K for the group's lower half and of 2 K + 1 for its upper one.
+template <int K, int C>
+__device__ __forceinline__ int64_t group_broadcast(int64_t v) {
+  constexpr int kBroadcast = 0x150;   // DPP row_newbcast of lane 0
+  int2 h = __builtin_bit_cast(int2, v), o;
+  if constexpr (C == 8) {
+    o.x = __builtin_amdgcn_update_dpp(0, h.x, kBroadcast + 2 * K, 0xF, 0x3, false);
+    o.y = __builtin_amdgcn_update_dpp(0, h.y, kBroadcast + 2 * K, 0xF, 0x3, false);
+    o.x = __builtin_amdgcn_update_dpp(o.x, h.x, kBroadcast + 2 * K + 1, 0xF, 0xC, false);
+    o.y = __builtin_amdgcn_update_dpp(o.y, h.y, kBroadcast + 2 * K + 1, 0xF, 0xC, false);
+  } else {
+    o.x = __builtin_amdgcn_update_dpp(0, h.x, kBroadcast + K, 0xF, 0xF, false);
+    o.y = __builtin_amdgcn_update_dpp(0, h.y, kBroadcast + K, 0xF, 0xF, false);
+  }
+  return __builtin_bit_cast(int64_t, o);
+}
+
 // LDS written by this wave and read by its other lanes.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -186,7 +240,7 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 template <typename E, int D, int QT, int WQ, int WK>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void attention_kernel(AttentionArgs a) {
   using S = Shape<E, D, QT, WQ, WK>;
   using F = Frag<E>;
   constexpr int C = S::kChunks;
@@ -298,16 +352,24 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
       for (int dt = 0; dt < DT; ++dt) acc[dt][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // ---- staging: chunk c of the slice is chunk c % C of its token c / C
-    u32x4 ks[S::kLoads], vs[S::kLoads];
+    // ---- staging: chunk c of the slice is chunk c % C of its token c / C,
+    // brought by lane c % (64 WQ) of the waves that share it. Loads go to LDS
+    // without a register: a wave instruction fills 64 chunks in a row, so the
+    // permutation of a token's chunks is one of the addresses it reads.
     const char* kc_base = static_cast<const char*>(a.k_cache) + h * a.c_head * static_cast<int64_t>(sizeof(E));
     const char* vc_base = static_cast<const char*>(a.v_cache) + h * a.c_head * static_cast<int64_t>(sizeof(E));
+    const char* kr_base = static_cast<const char*>(a.k) + (r0 * a.k_row + h * a.k_head) * static_cast<int64_t>(sizeof(E));
+    const char* vr_base = static_cast<const char*>(a.v) + (r0 * a.v_row + h * a.v_head) * static_cast<int64_t>(sizeof(E));
     const int32_t* row_table = a.table + static_cast<int64_t>(i) * a.table_ld;
     const int page_mask = (1 << a.page_shift) - 1;
     const int slot0 = wq * kWave + lane;   // this lane's first chunk
-    // lane x of the wave looks up the page of token x of the slice
+    // Each lane knows the place of one token: the one that load k brings to
+    // the lane's group of 16 (the half group, for rows of 8 chunks) is that
+    // of the group's lane k (2 k, 2 k + 1), and a broadcast inside the group
+    // hands it on.
+    const int my_row = min(S::owned_row(wq, grp, col), S::kTokens - 1);
     auto look_up = [&](int t) -> int {
-      const int x = t * S::kTile + wk * kSlice + (lane & (kSlice - 1));
+      const int x = t * S::kTile + wk * S::kTokens + my_row;
       int id = 0;
       if (x < len) {
         id = row_table[x >> a.page_shift];
@@ -318,79 +380,83 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
       }
       return id;
     };
-    auto fetch = [&](int t, int ids) {
-#pragma unroll
-      for (int k = 0; k < S::kLoads; ++k) {
+    auto fetch = [&](int t, int id) {
+      const int stage = S::kStages > 1 ? (t & 1) : 0;
+      const uint32_t kd = __builtin_amdgcn_readfirstlane(lds_address(s.tile[stage][wk].k) + wq * kWave * 16);
+      const uint32_t vd = __builtin_amdgcn_readfirstlane(lds_address(s.tile[stage][wk].v) + wq * kWave * 16);
+      const int x = t * S::kTile + wk * S::kTokens + my_row;
+      const int own = min(max(x - len, 0), n - 1);   // behind the last token: any row that exists
+      int64_t kp = reinterpret_cast<int64_t>(kr_base) + own * a.k_row * static_cast<int64_t>(sizeof(E));
+      int64_t vp = reinterpret_cast<int64_t>(vr_base) + own * a.v_row * static_cast<int64_t>(sizeof(E));
+      const int64_t cached = (id * a.c_page + (x & page_mask) * a.c_token) * static_cast<int64_t>(sizeof(E));
+      kp = x < len ? reinterpret_cast<int64_t>(kc_base) + cached : kp;
+      vp = x < len ? reinterpret_cast<int64_t>(vc_base) + cached : vp;
+      for_each_index(std::make_integer_sequence<int, S::kLoads>(), [&](auto index) {
+        constexpr int k = decltype(index)::value;
         const int c = slot0 + k * kWave * WQ;
-        const int row = c / C, chunk = c % C;
-        const int x = t * S::kTile + wk * kSlice + row;
-        const int id = __shfl(ids, row);
-        ks[k] = vs[k] = u32x4{0, 0, 0, 0};
-        if (x < len) {
-          const int64_t at = (id * a.c_page + (x & page_mask) * a.c_token) * static_cast<int64_t>(sizeof(E)) + chunk * 16;
-          ks[k] = *reinterpret_cast<const u32x4*>(kc_base + at);
-          vs[k] = *reinterpret_cast<const u32x4*>(vc_base + at);
-        } else if (x < end) {
-          const int64_t r = r0 + (x - len);
-          ks[k] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.k) +
-                                                  (r * a.k_row + h * a.k_head) * static_cast<int64_t>(sizeof(E)) + chunk * 16);
-          vs[k] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.v) +
-                                                  (r * a.v_row + h * a.v_head) * static_cast<int64_t>(sizeof(E)) + chunk * 16);
-        }
-      }
+        const int row = c / C, pos = c % C;
+        load_to_lds(group_broadcast<k, C>(kp) + (pos ^ swizzle_k<C>(row)) * 16, kd + k * kWave * WQ * 16);
+        load_to_lds(group_broadcast<k, C>(vp) + (pos ^ swizzle_v<E, C>(row)) * 16, vd + k * kWave * WQ * 16);
+      });
     };
-    char* kl = reinterpret_cast<char*>(s.tile.k[wk]);
-    char* vl = reinterpret_cast<char*>(s.tile.v[wk]);
-    auto put = [&](int t) {
-#pragma unroll
+    // Values of the rows' own that are not finite would reach rows that do not see
+    // them through a weight of 0, and so would what lies behind the last
+    // token: both are 0 in the tile (the former are added at the end).
+    auto clean = [&](int t) {
+      u32x4* vl = reinterpret_cast<u32x4*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].v);
+#pragma unroll 1
       for (int k = 0; k < S::kLoads; ++k) {
         const int c = slot0 + k * kWave * WQ;
-        const int row = c / C, chunk = c % C;
-        // a value that is not finite would reach rows that do not see it
-        // through a weight of 0: it is taken out here and added behind
-        if (t * S::kTile + wk * kSlice + row >= len) {
-          bool odd = false;
+        const int x = t * S::kTile + wk * S::kTokens + c / C;
+        if (x < len) continue;
+        u32x4 v = vl[c];
+        bool odd = false;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) odd |= not_finite(vs[k][e], std::integral_constant<int, sizeof(E)>());
-          if (odd) {
-            s.odd = 1;
-            if (sizeof(E) == 2) {
+        for (int e = 0; e < 4; ++e) odd |= not_finite(v[e], std::integral_constant<int, sizeof(E)>());
+        if (!odd && x < end) continue;
+        if (x < end) s.odd = 1;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((vs[k][e] & 0x7F80u) == 0x7F80u) vs[k][e] &= 0xFFFF0000u;
-                if ((vs[k][e] & 0x7F800000u) == 0x7F800000u) vs[k][e] &= 0xFFFFu;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((vs[k][e] & 0x7F800000u) == 0x7F800000u) vs[k][e] = 0;
-            }
+        for (int e = 0; e < 4; ++e) {
+          if (sizeof(E) == 2) {
+            if ((v[e] & 0x7F80u) == 0x7F80u) v[e] &= 0xFFFF0000u;
+            if ((v[e] & 0x7F800000u) == 0x7F800000u) v[e] &= 0xFFFFu;
+          } else if ((v[e] & 0x7F800000u) == 0x7F800000u) {
+            v[e] = 0;
           }
+          if (x >= end) v[e] = 0;
         }
-        *reinterpret_cast<u32x4*>(kl + (row * C + (chunk ^ swizzle_k<C>(row))) * 16) = ks[k];
-        *reinterpret_cast<u32x4*>(vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16) = vs[k];
+        vl[c] = v;
       }
     };
-    auto sync = [&]() {
+
+    int ids = look_up(t0);
+    if (S::kStages > 1) {
+      fetch(t0, ids);
+      ids = t0 + 1 < t1 ? look_up(t0 + 1) : 0;
+    }
+    for (int t = t0; t < t1; ++t) {
+      const int x0 = t * S::kTile + wk * S::kTokens;
+      if (S::kStages == 1) {
+        if (WQ > 1 && t > t0) lds_barrier();   // the slice has been read
+        fetch(t, ids);
+        if (t + 1 < t1) ids = look_up(t + 1);
+      }
+      wait_loads();
+      if (x0 + S::kTokens > len) clean(t);
       if (WQ > 1)
         lds_barrier();
       else
         wave_sync();
-    };
-
-    int ids = look_up(t0);
-    fetch(t0, ids);
-    ids = t0 + 1 < t1 ? look_up(t0 + 1) : 0;
-    for (int t = t0; t < t1; ++t) {
-      sync();   // the slice has been read
-      put(t);
-      sync();
-      if (t + 1 < t1) {
+      if (S::kStages > 1 && t + 1 < t1) {
+        // into the other buffer, which every wave has read before the barrier
         fetch(t + 1, ids);
         if (t + 2 < t1) ids = look_up(t + 2);
       }
-      const int x0 = t * S::kTile + wk * kSlice;
-      if (x0 >= end) continue;   // the wave's slice lies behind the last token (no barrier below)
+      if (x0 >= end) continue;   // the slice lies behind the last token (no barrier below)
+      const char* kl = reinterpret_cast<const char*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].k);
+      const char* vl = reinterpret_cast<const char*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].v);
+#pragma unroll
+      for (int sub = 0; sub < S::kSub; ++sub) {
 
       // S^T of two halves of 16 tokens
       f32x4 sc[2][QT];
@@ -398,7 +464,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
       for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) sc[hf][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int row = hf * 16 + col;
+        const int row = sub * kSlice + hf * 16 + col;
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc) {
           typename F::T kf;
@@ -415,12 +481,13 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
         }
       }
       // tokens from the tree on: only the row's path is seen
-      if (x0 + kSlice > len) {
+      const int xs = x0 + sub * kSlice;
+      if (xs + kSlice > len) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int at = x0 + hf * 16 + grp * 4 + e - len;
+            const int at = xs + hf * 16 + grp * 4 + e - len;
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
               const bool sees = at < 0 || (at < n && (path[qt] >> (at & 63) & 1));
@@ -475,7 +542,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
           s16x4 half[2];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const int row = hf * 16 + grp * 4 + (col >> 2);
+            const int row = sub * kSlice + hf * 16 + grp * 4 + (col >> 2);
             const int chunk = dt * 2 + ((col & 3) >> 1);
             const char* p = vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16 + (col & 1) * 8;
             half[hf] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -486,7 +553,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int row = (e >> 2) * 16 + grp * 4 + (e & 3);
+            const int row = sub * kSlice + (e >> 2) * 16 + grp * 4 + (e & 3);
             const int chunk = dt * 4 + (col >> 2);
             vf[e] = *reinterpret_cast<const float*>(vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16 + (col & 3) * 4);
           }
@@ -494,23 +561,6 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) acc[dt][qt] = F::mma(vf, pf[qt], acc[dt][qt]);
       }
-      if (x0 + kSlice > len && s.odd) {
-        for (int x = max(x0, len); x < min(x0 + kSlice, end); ++x) {
-          const E* p = static_cast<const E*>(a.v) + static_cast<int64_t>(r0 + x - len) * a.v_row + h * a.v_head;
-          for (int dt = 0; dt < DT; ++dt)
-            for (int e = 0; e < 4; ++e) {
-              const float f = Elem<E>::at(p, dt * 16 + grp * 4 + e);
-              if (!(fabsf(f) < INFINITY)) {
-#pragma unroll
-                for (int d2 = 0; d2 < DT; ++d2)
-#pragma unroll
-                  for (int e2 = 0; e2 < 4; ++e2)
-#pragma unroll
-                    for (int qt = 0; qt < QT; ++qt)
-                      if (d2 == dt && e2 == e && (path[qt] >> (x - len) & 1)) acc[d2][qt][e2] += f;
-              }
-            }
-        }
       }
     }
 
@@ -528,6 +578,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
       }
     }
     lds_barrier();
+    const bool odd = s.odd != 0;
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
       const int q = (wq * QT + qt) * 16 + col;
@@ -563,6 +614,19 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
         f32x4 o = *reinterpret_cast<const f32x4*>(&s.join[0][q][d]);
 #pragma unroll
         for (int k = 1; k < WK; ++k) o += *reinterpret_cast<const f32x4*>(&s.join[k][q][d]);
+        if (odd) {
+          // values that are not finite, for the rows that see them
+          const uint64_t seen_rows = s.path[(mt * S::kMT + q) / a.G];
+          for (int x = max(t0 * S::kTile, len); x < min(t1 * S::kTile, end); ++x) {
+            if (!(seen_rows >> (x - len) & 1)) continue;
+            const E* p = static_cast<const E*>(a.v) + static_cast<int64_t>(r0 + x - len) * a.v_row + h * a.v_head;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f = Elem<E>::at(p, d0 + d + e);
+              if (!(fabsf(f) < INFINITY)) o[e] += f;
+            }
+          }
+        }
         if (whole) {
           const float sum = s.fin[q][1];
           const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN stays one
@@ -677,10 +741,10 @@ Plan plan_of(const AttentionArgs& a) {
   if (m <= 16) return {16, 128};
   if (m <= 32) return {32, 128};
   if (m <= 64) return narrow ? Plan{64, 64} : Plan{64, 128};
-  if (narrow || m <= 128) return narrow ? Plan{128, 32} : Plan{128, 64};
-  return {256, 32};
+  if (narrow) return {128, 64};
+  return m <= 128 ? Plan{128, 64} : Plan{256, 64};
 }
-int workers_of(const AttentionArgs& a) { return a.cus > 0 ? a.cus : 256; }
+int workers_of(const AttentionArgs& a) { return (a.cus > 0 ? a.cus : 256) * 2; }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -688,7 +752,7 @@ template <typename E, int D, int QT, int WQ, int WK>
 hipError_t launch_t(AttentionArgs a, hipStream_t s) {
   using S = Shape<E, D, QT, WQ, WK>;
   a.G = a.H / a.KV;
-  a.workers = workers_of(a);
+  a.workers = workers_of(a) / 2 * S::kGroups;
   char* p = static_cast<char*>(a.work);
   a.piece = reinterpret_cast<int32_t*>(p);
   p += align256(static_cast<size_t>(a.workers) * 16);
