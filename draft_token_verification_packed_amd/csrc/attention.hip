@@ -44,7 +44,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSlice = 32;     // tokens a wave takes at a time
-constexpr int kThreads = 256;  // four waves: WQ * WK
 
 // One 16 x 16 product over 32 of the inner dimension: lane l holds 8 inner
 // elements of row (column) l % 16, the same 8 in both factors.
@@ -86,7 +85,7 @@ template <> struct Frag<float> {
 // Shape of an instantiation.
 template <typename E, int D, int QT, int WQ, int WK>
 struct Shape {
-  static_assert(WQ * WK * kWave == kThreads, "four waves");
+  static constexpr int kThreads = WQ * WK * kWave;
   static constexpr int kMT = 16 * QT * WQ;           // queries of an item
   static constexpr int kSub = WK == 1 ? 2 : 1;       // steps of a slice: fewer barriers where waves share it
   static constexpr int kTokens = kSlice * kSub;      // tokens of a slice
@@ -95,9 +94,10 @@ struct Shape {
   static constexpr int kChunks = kRowBytes / 16;     // 16-byte chunks of a token's row
   static constexpr int kSliceBytes = kTokens * kRowBytes;
   static constexpr int kLoads = kSliceBytes / 16 / (kWave * WQ);   // chunks a lane brings of K (and of V)
-  // workgroups of few queries share a CU, which hides what each does between
-  // its items; buffers: two where the LDS holds them
-  static constexpr int kGroups = QT <= 2 && WK * kSliceBytes <= 32 * 1024 ? 2 : 1;
+  // two workgroups of four waves share a CU where the LDS holds both, which
+  // hides what each does between its items; buffers: two where it holds them
+  static constexpr int kGroups = kThreads == 256 && WK * kSliceBytes <= 32 * 1024 ? 2 : 1;
+  static constexpr int kWaves = kGroups * kThreads / 256;   // a SIMD's waves
   static constexpr int kStages = kGroups * WK * kSliceBytes * 4 <= 128 * 1024 ? 2 : 1;
   static_assert(kLoads <= (kChunks == 8 ? 8 : 16), "a lane of 16 for every load");
   // The row of the slice whose place lane (grp, col) of wave wq works out.
@@ -108,6 +108,10 @@ struct Shape {
   }
   static constexpr int kOut = 64;                    // columns of O joined at a time
   static constexpr int kOutStride = kOut + 4;
+};
+
+struct Request {
+  int r0, n, len, tiles, blocks;   // rows, context, tiles of an item, blocks of queries
 };
 
 template <typename E, int D, int QT, int WQ, int WK>
@@ -123,9 +127,10 @@ struct AttnScratch {
   float ml[WK][S::kMT][2];
   float fin[S::kMT][2];
   uint64_t path[VSV_MAX_TREE_ROWS];
-  int64_t scan[kThreads / kWave];
+  int64_t scan[S::kThreads / kWave];
   int64_t base;
   int request;
+  Request first;
   int odd;   // a value among the rows' own is not finite
 };
 
@@ -144,6 +149,14 @@ __device__ __forceinline__ int swizzle_v(int r) {
   return C == 8 ? 2 * ((r >> 1) & 3) : 2 * (r & 7);
 }
 
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  int2 h = __builtin_bit_cast(int2, v);
+  h.x = __builtin_amdgcn_readfirstlane(h.x);
+  h.y = __builtin_amdgcn_readfirstlane(h.y);
+  return __builtin_bit_cast(int64_t, h);
+}
+
+template <int NT>
 __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* scratch, int64_t& total) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const int64_t incl = wave_scan_incl(v);
@@ -153,7 +166,7 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* scratch, int
   int64_t before = 0;
   total = 0;
 #pragma unroll
-  for (int k = 0; k < kThreads / kWave; ++k) {
+  for (int k = 0; k < NT / kWave; ++k) {
     const int64_t s = scratch[k];
     before += k < w ? s : 0;
     total += s;
@@ -161,13 +174,11 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* scratch, int
   return before + incl - v;
 }
 
-struct Request {
-  int r0, n, len, tiles, blocks;   // rows, context, tiles of an item, blocks of queries
-};
-
 template <typename S>
 __device__ __forceinline__ Request request_of(const AttentionArgs& a, int i, bool& bad) {
-  const int r0 = a.offsets[i], r1 = a.offsets[i + 1], len = a.length[i];
+  // (inputs no kernel writes: uniform ones come through the scalar cache)
+  typedef const __attribute__((address_space(4))) int32_t* Constant;
+  const int r0 = ((Constant)a.offsets)[i], r1 = ((Constant)a.offsets)[i + 1], len = ((Constant)a.length)[i];
   const int64_t room = static_cast<int64_t>(a.table_width) << a.page_shift;
   bad = r0 < 0 || r1 < r0 || r1 > a.R || r1 - r0 > VSV_MAX_TREE_ROWS || len < 0 || len > room;
   Request q{r0, r1 - r0, len, 0, 0};
@@ -232,6 +243,13 @@ __device__ __forceinline__ int64_t group_broadcast(int64_t v) {
   return __builtin_bit_cast(int64_t, o);
 }
 
+__device__ __forceinline__ void store_out(uint16_t* p, f32x4 o) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<bf16x4*>(p) = bf16x4{static_cast<__bf16>(o[0]), static_cast<__bf16>(o[1]), static_cast<__bf16>(o[2]),
+                                         static_cast<__bf16>(o[3])};
+}
+__device__ __forceinline__ void store_out(float* p, f32x4 o) { *reinterpret_cast<f32x4*>(p) = o; }
+
 // LDS written by this wave and read by its other lanes.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -240,9 +258,10 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 template <typename E, int D, int QT, int WQ, int WK>
-__global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, QT, WQ, WK>::kWaves)) void attention_kernel(AttentionArgs a) {
   using S = Shape<E, D, QT, WQ, WK>;
   using F = Frag<E>;
+  constexpr int kThreads = S::kThreads;
   constexpr int C = S::kChunks;
   constexpr int KC = D / 32;    // inner steps of K Q^T
   constexpr int DT = D / 16;    // row blocks of O^T
@@ -253,57 +272,71 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
   const int w = blockIdx.x;
   int bits = 0;
 
-  // ---- this worker's span
-  int64_t units = 0;
+  // ---- this worker's span: the sum over the requests, then the request that
+  // holds the span's start (in the same pass where each has a thread)
+  int64_t units = 0, before = 0, size0 = 0;
+  Request mine0{};
   for (int base = 0; base < a.B; base += kThreads) {
     const int i = base + tid;
-    int64_t mine = 0;
+    size0 = 0;
     if (i < a.B) {
       bool bad;
-      const Request q = request_of<S>(a, i, bad);
+      mine0 = request_of<S>(a, i, bad);
       if (bad) bits |= VSV_FLAG_LAYOUT;
-      mine = static_cast<int64_t>(a.KV) * q.blocks * q.tiles;
+      size0 = static_cast<int64_t>(a.KV) * mine0.blocks * mine0.tiles;
     }
     int64_t total;
-    block_scan64(mine, s.scan, total);
+    before = units + block_scan64<kThreads>(size0, s.scan, total);
     units += total;
   }
-  if (tid == 0) a.piece[4 * w] = -1;
+  if (tid == 0) a.piece[w].x = -1;
   if (w == 0 && bits && a.error_flag) atomicOr(a.error_flag, bits);
   bits = 0;
   const int workers = static_cast<int>(min(static_cast<int64_t>(a.workers), units));
   if (w >= workers) return;
+  units = uniform64(units);
   const int64_t u0 = span_start(units, w, workers), u1 = span_start(units, w + 1, workers);
-  int64_t seen = 0;
-  for (int base = 0; base < a.B; base += kThreads) {
-    const int i = base + tid;
-    int64_t mine = 0;
-    if (i < a.B) {
-      bool bad;
-      const Request q = request_of<S>(a, i, bad);
-      mine = static_cast<int64_t>(a.KV) * q.blocks * q.tiles;
+  if (a.B > kThreads) {
+    int64_t seen = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+      const int i = base + tid;
+      size0 = 0;
+      if (i < a.B) {
+        bool bad;
+        mine0 = request_of<S>(a, i, bad);
+        size0 = static_cast<int64_t>(a.KV) * mine0.blocks * mine0.tiles;
+      }
+      int64_t total;
+      before = seen + block_scan64<kThreads>(size0, s.scan, total);
+      seen += total;
+      if (before <= u0 && u0 < before + size0) s.request = base + tid;
+      if (seen > u0) break;
     }
-    int64_t total;
-    const int64_t before = seen + block_scan64(mine, s.scan, total);
-    if (before <= u0 && u0 < before + mine) {
-      s.request = i;
-      s.base = before;
-    }
-    seen += total;
-    if (seen > u0) break;
+  } else if (before <= u0 && u0 < before + size0) {
+    s.request = tid;
+  }
+  if (before <= u0 && u0 < before + size0) {
+    s.base = before;
+    s.first = mine0;
   }
   lds_barrier();
-  int i = s.request;
-  int64_t base = s.base;
+  int i = __builtin_amdgcn_readfirstlane(s.request);
+  int64_t base = uniform64(s.base);
+  Request rq = s.first;
+  rq.r0 = __builtin_amdgcn_readfirstlane(rq.r0);
+  rq.n = __builtin_amdgcn_readfirstlane(rq.n);
+  rq.len = __builtin_amdgcn_readfirstlane(rq.len);
+  rq.tiles = __builtin_amdgcn_readfirstlane(rq.tiles);
+  rq.blocks = __builtin_amdgcn_readfirstlane(rq.blocks);
 
   // ---- the items of the span
   for (int64_t u = u0; u < u1;) {
-    bool bad;
-    const Request rq = request_of<S>(a, i, bad);
     const int64_t size = static_cast<int64_t>(a.KV) * rq.blocks * rq.tiles;
     if (u >= base + size) {
       base += size;
       ++i;
+      bool bad;
+      rq = request_of<S>(a, i, bad);
       continue;
     }
     const uint32_t rel = static_cast<uint32_t>(u - base);
@@ -315,42 +348,6 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
 
     const int r0 = rq.r0, n = rq.n, len = rq.len, end = len + n;
     const int M = min(n * a.G - mt * S::kMT, S::kMT);   // queries of this block
-
-    // the rows' paths
-    if (wave == 0) {
-      const int up = a.parents && lane < n ? a.parents[r0 + lane] : 0;
-      bool off_tree;
-      s.path[lane] = tree_paths(lane, n, up, a.parents == nullptr, off_tree);
-      if (off_tree) bits |= VSV_FLAG_LAYOUT;
-      if (lane == 0) s.odd = 0;
-    }
-    lds_barrier();
-
-    // ---- queries
-    typename F::T qf[QT][KC];
-    uint64_t path[QT];
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      const int m = (wq * QT + qt) * 16 + col;
-      const bool live = m < M;
-      const int at = mt * S::kMT + (live ? m : 0);
-      const int j = at / a.G, hq = h * a.G + (at - j * a.G);
-      const E* p = static_cast<const E*>(a.q) + (r0 + j) * a.q_row + hq * a.q_head + grp * 8;
-#pragma unroll
-      for (int kc = 0; kc < KC; ++kc) qf[qt][kc] = live ? F::load(p + kc * 32) : F::zero();
-      path[qt] = live ? s.path[j] : 0;
-    }
-
-    f32x4 acc[DT][QT];
-    float mref[QT], mc[QT], l[QT];   // reference, times the scale (0 while there is none), weights so far
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      mref[qt] = -INFINITY;
-      mc[qt] = 0.f;
-      l[qt] = 0.f;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) acc[dt][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
 
     // ---- staging: chunk c of the slice is chunk c % C of its token c / C,
     // brought by lane c % (64 WQ) of the waves that share it. Loads go to LDS
@@ -429,41 +426,65 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
       }
     };
 
+    // first loads: pages, parents, queries, then the tile that the pages tell
     int ids = look_up(t0);
+    const int up = wave == 0 && a.parents && lane < n ? a.parents[r0 + lane] : 0;
+    // ---- queries
+    typename F::T qf[QT][KC];
+    int row[QT];
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      const int m = (qt * WQ + wq) * 16 + col;
+      const bool live = m < M;
+      const int at = mt * S::kMT + (live ? m : 0);
+      const int j = at / a.G, hq = h * a.G + (at - j * a.G);
+      const E* p = static_cast<const E*>(a.q) + (r0 + j) * a.q_row + hq * a.q_head + grp * 8;
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc) qf[qt][kc] = live ? F::load(p + kc * 32) : F::zero();
+      row[qt] = live ? j : -1;
+    }
+
     if (S::kStages > 1) {
       fetch(t0, ids);
       ids = t0 + 1 < t1 ? look_up(t0 + 1) : 0;
     }
-    for (int t = t0; t < t1; ++t) {
+    if (wave == 0) {
+      bool off_tree;
+      s.path[lane] = tree_paths(lane, n, up, a.parents == nullptr, off_tree);
+      if (off_tree) bits |= VSV_FLAG_LAYOUT;
+      if (lane == 0) s.odd = 0;
+    }
+    lds_barrier();
+    uint64_t path[QT];
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) path[qt] = row[qt] >= 0 ? s.path[row[qt]] : 0;
+
+    f32x4 acc[DT][QT];
+    float mref[QT], mc[QT], l[QT];   // reference, times the scale (0 while there is none), weights so far
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      mref[qt] = -INFINITY;
+      mc[qt] = 0.f;
+      l[qt] = 0.f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) acc[dt][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // One tile of this wave's slice, for its first NQ blocks of 16 queries.
+    auto compute = [&](auto live, int t) {
+      constexpr int NQ = decltype(live)::value;
       const int x0 = t * S::kTile + wk * S::kTokens;
-      if (S::kStages == 1) {
-        if (WQ > 1 && t > t0) lds_barrier();   // the slice has been read
-        fetch(t, ids);
-        if (t + 1 < t1) ids = look_up(t + 1);
-      }
-      wait_loads();
-      if (x0 + S::kTokens > len) clean(t);
-      if (WQ > 1)
-        lds_barrier();
-      else
-        wave_sync();
-      if (S::kStages > 1 && t + 1 < t1) {
-        // into the other buffer, which every wave has read before the barrier
-        fetch(t + 1, ids);
-        if (t + 2 < t1) ids = look_up(t + 2);
-      }
-      if (x0 >= end) continue;   // the slice lies behind the last token (no barrier below)
       const char* kl = reinterpret_cast<const char*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].k);
       const char* vl = reinterpret_cast<const char*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].v);
 #pragma unroll
       for (int sub = 0; sub < S::kSub; ++sub) {
 
       // S^T of two halves of 16 tokens
-      f32x4 sc[2][QT];
+      f32x4 sc[2][NQ];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt) sc[hf][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int qt = 0; qt < NQ; ++qt) sc[hf][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
         const int row = sub * kSlice + hf * 16 + col;
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc) {
@@ -477,33 +498,34 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
             kf = f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
           }
 #pragma unroll
-          for (int qt = 0; qt < QT; ++qt) sc[hf][qt] = F::mma(kf, qf[qt][kc], sc[hf][qt]);
+          for (int qt = 0; qt < NQ; ++qt) sc[hf][qt] = F::mma(kf, qf[qt][kc], sc[hf][qt]);
         }
       }
       // tokens from the tree on: only the row's path is seen
       const int xs = x0 + sub * kSlice;
       if (xs + kSlice > len) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
+        for (int qt = 0; qt < NQ; ++qt) {
+          // bit k: the lane's query sees token k of the step
+          const int first = xs - len;   // of the rows' own
+          const uint32_t seen = first >= 0 ? (first < 64 ? static_cast<uint32_t>(path[qt] >> first) : 0u)
+                                           : (static_cast<uint32_t>(path[qt]) << -first) | ((1u << -first) - 1u);
+          const uint32_t mine = seen >> (grp * 4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = xs + hf * 16 + grp * 4 + e - len;
+          for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt) {
-              const bool sees = at < 0 || (at < n && (path[qt] >> (at & 63) & 1));
-              sc[hf][qt][e] = sees ? sc[hf][qt][e] : -INFINITY;
-            }
-          }
+            for (int e = 0; e < 4; ++e) sc[hf][qt][e] = mine & (1u << (hf * 16 + e)) ? sc[hf][qt][e] : -INFINITY;
+        }
       }
       // The reference moves only where a score passes it by more than kSlack
       // in log2: weights stay below 2^kSlack, and most tiles skip the
       // reduction across lanes and the rescaling.
       constexpr float kSlack = 8.f;
-      typename F::T pf[QT];
+      typename F::T pf[NQ];
       bool move = false;
-      float top[QT];
+      float top[NQ];
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
+      for (int qt = 0; qt < NQ; ++qt) {
         float b = sc[0][qt][0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) b = fmaxf(b, sc[e >> 2][qt][e & 3]);
@@ -512,7 +534,7 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
       }
       if (__builtin_amdgcn_ballot_w64(move)) {
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
+        for (int qt = 0; qt < NQ; ++qt) {
           float b = fmaxf(top[qt], mref[qt]);
           b = fmaxf(b, __shfl_xor(b, 16));
           b = fmaxf(b, __shfl_xor(b, 32));
@@ -525,7 +547,7 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
         }
       }
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
+      for (int qt = 0; qt < NQ; ++qt) {
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -559,9 +581,37 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
           }
         }
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt) acc[dt][qt] = F::mma(vf, pf[qt], acc[dt][qt]);
+        for (int qt = 0; qt < NQ; ++qt) acc[dt][qt] = F::mma(vf, pf[qt], acc[dt][qt]);
       }
       }
+    };
+    const int blocks = (M + 15) / 16;   // of 16 queries, dealt to the waves in turn
+    const int mine = blocks > wq ? (blocks - wq + WQ - 1) / WQ : 0;
+
+    for (int t = t0; t < t1; ++t) {
+      const int x0 = t * S::kTile + wk * S::kTokens;
+      if (S::kStages == 1) {
+        if (WQ > 1 && t > t0) lds_barrier();   // the slice has been read
+        fetch(t, ids);
+        if (t + 1 < t1) ids = look_up(t + 1);
+      }
+      wait_loads();
+      if (x0 + S::kTokens > len) clean(t);
+      if (WQ > 1)
+        lds_barrier();
+      else
+        wave_sync();
+      if (S::kStages > 1 && t + 1 < t1) {
+        // into the other buffer, which every wave has read before the barrier
+        fetch(t + 1, ids);
+        if (t + 2 < t1) ids = look_up(t + 2);
+      }
+      // a slice behind the last token, or no query (no barrier below)
+      if (x0 >= end || mine == 0) continue;
+      if (WQ > 1 && QT == 2 && mine == 1)
+        compute(std::integral_constant<int, 1>(), t);
+      else
+        compute(std::integral_constant<int, QT>(), t);
     }
 
     // ---- join the slices, then the item's result or piece
@@ -572,7 +622,7 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
       l[qt] += __shfl_xor(l[qt], 16);
       l[qt] += __shfl_xor(l[qt], 32);
       if (grp == 0) {
-        const int q = (wq * QT + qt) * 16 + col;
+        const int q = (qt * WQ + wq) * 16 + col;
         s.ml[wk][q][0] = mref[qt];
         s.ml[wk][q][1] = l[qt];
       }
@@ -581,7 +631,7 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
     const bool odd = s.odd != 0;
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
-      const int q = (wq * QT + qt) * 16 + col;
+      const int q = (qt * WQ + wq) * 16 + col;
       float m = -INFINITY;
 #pragma unroll
       for (int k = 0; k < WK; ++k) m = fmaxf(m, s.ml[k][q][0]);
@@ -606,7 +656,7 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
       for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
         for (int dt = 0; dt < S::kOut / 16; ++dt)
-          *reinterpret_cast<f32x4*>(&s.join[wk][(wq * QT + qt) * 16 + col][dt * 16 + grp * 4]) = acc[d0 / 16 + dt][qt];
+          *reinterpret_cast<f32x4*>(&s.join[wk][(qt * WQ + wq) * 16 + col][dt * 16 + grp * 4]) = acc[d0 / 16 + dt][qt];
       lds_barrier();
       constexpr int kQuads = S::kOut / 4;
       for (int c = tid; c < M * kQuads; c += kThreads) {
@@ -632,15 +682,7 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
           const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN stays one
           const int at = mt * S::kMT + q, j = at / a.G, hq = h * a.G + (at - j * a.G);
           E* p = static_cast<E*>(a.out) + (r0 + j) * a.o_row + hq * a.o_head + d0 + d;
-          if constexpr (sizeof(E) == 2) {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            bf16x4 y;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = static_cast<__bf16>(o[e] * inv);
-            *reinterpret_cast<bf16x4*>(p) = y;
-          } else {
-            *reinterpret_cast<f32x4*>(p) = o * inv;
-          }
+          store_out(p, o * inv);
         } else {
           *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(slot) * S::kMT + q) * D + d0 + d) = o;
         }
@@ -663,10 +705,7 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
         int w1 = static_cast<int>(((last + 1) * workers - 1) / units);
         while (span_start(units, w1 + 1, workers) <= last) ++w1;
         while (span_start(units, w1, workers) > last) --w1;
-        a.piece[4 * w] = i;
-        a.piece[4 * w + 1] = h;
-        a.piece[4 * w + 2] = mt;
-        a.piece[4 * w + 3] = w1;
+        a.piece[w] = make_int4(r0, h, mt, w1 * 512 + M);
       }
     }
     lds_barrier();   // paths and joined columns are free again
@@ -674,57 +713,95 @@ __global__ __launch_bounds__(kThreads, (Shape<E, D, QT, WQ, WK>::kGroups)) void 
   if (bits && a.error_flag) atomicOr(a.error_flag, bits);
 }
 
-// Joins the pieces of the items that no worker finished: a wave per query.
-constexpr int kJoinQueries = kThreads / kWave;
+// Joins the pieces of the items that no worker finished: a wave per query,
+// D / 4 lanes for 4 columns each and the pieces dealt to 256 / D groups of
+// them. Every workgroup lists the items that were cut, wherever they are, so
+// that few long items and many short ones keep the whole grid busy alike.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxWorkers = 1024;
+constexpr int kJoinGroups = 2048;
 
 template <typename E, int D, int MT>
-__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int w = static_cast<int>(blockIdx.x) / (MT / kJoinQueries);
-  const int q = static_cast<int>(blockIdx.x) % (MT / kJoinQueries) * kJoinQueries + static_cast<int>(threadIdx.x) / kWave;
-  const int i = a.piece[4 * w];
-  if (i < 0) return;
-  const int h = a.piece[4 * w + 1], mt = a.piece[4 * w + 2], w1 = a.piece[4 * w + 3];
-  const int r0 = a.offsets[i], n = a.offsets[i + 1] - r0;
-  const int at = mt * MT + q;
-  if (at >= n * a.G) return;
-  constexpr int N = D / kWave;
-  float o[N] = {};
-  float m = -INFINITY, sum = 0.f;
-  auto slot_of = [&](int x) { return static_cast<int64_t>(x == w ? 2 * w + 1 : 2 * x); };
-  for (int x0 = w; x0 <= w1; x0 += kWave) {
-    float mk = -INFINITY, lk = 0.f;
-    if (x0 + lane <= w1) {
-      const float* ml = a.part_ml + (slot_of(x0 + lane) * MT + q) * 2;
-      mk = ml[0];
-      lk = ml[1];
-    }
-    const float top = fmaxf(m, wave_all(mk, MaxOp()));
-    const float old = m == -INFINITY ? 1.f : fast_exp2(m - top);
-    const float f = mk == -INFINITY ? 1.f : fast_exp2(mk - top);
-    sum = sum * old + wave_all(lk * f, SumOp());
-#pragma unroll
-    for (int k = 0; k < N; ++k) o[k] *= old;
-    m = top;
-    const int count = min(kWave, w1 - x0 + 1);
-    for (int x = 0; x < count; ++x) {
-      const float* p = a.part + (slot_of(x0 + x) * MT + q) * D;
-      const float fx = __shfl(f, x);
-#pragma unroll
-      for (int k = 0; k < N; ++k) o[k] += fx * p[k * kWave + lane];
-    }
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a) {
+  constexpr int kLanes = D / 4;             // lanes of a piece
+  constexpr int kSets = kWave / kLanes;     // pieces side by side
+  constexpr int kAhead = 4;                 // rounds of pieces loaded at a time
+  __shared__ int4 cut[kMaxWorkers];   // first row, key head, block, worker * 2^20 + last worker * 2^9 + queries
+  __shared__ int scan[kJoinThreads / kWave];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  int count = 0;
+  for (int base = 0; base < a.workers; base += kJoinThreads) {
+    const int w = base + tid;
+    int4 p = make_int4(-1, 0, 0, 0);
+    if (w < a.workers) p = a.piece[w];
+    const bool here = p.x >= 0;
+    int found;
+    const int at = count + block_exclusive_scan<kJoinThreads>(here ? 1 : 0, scan, found);
+    if (here) cut[at] = make_int4(p.x, p.y, p.z, (w << 20) + p.w);
+    count += found;
   }
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  const int j = at / a.G, hq = h * a.G + (at - j * a.G);
-  E* p = static_cast<E*>(a.out) + (r0 + j) * a.o_row + hq * a.o_head;
+  lds_barrier();
+  const int set = lane / kLanes, d = lane % kLanes * 4;
+  constexpr int kWaves = kJoinThreads / kWave;
+  const int tasks = count * MT;
+  for (int task = static_cast<int>(blockIdx.x) * kWaves + tid / kWave; task < tasks;
+       task += static_cast<int>(gridDim.x) * kWaves) {
+    // queries of one item go to workgroups far apart, items side by side
+    const int q = task / count;
+    const int4 p = cut[task - q * count];
+    const int w = p.w >> 20, w1 = p.w >> 9 & 2047, M = p.w & 511, r0 = p.x, h = p.y, mt = p.z;
+    if (q >= M) continue;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, sum = 0.f;
+    for (int x0 = w; x0 <= w1; x0 += kAhead * kSets) {
+      float mk[kAhead], lk[kAhead];
+      f32x4 ok[kAhead];
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    if constexpr (sizeof(E) == 2)
-      reinterpret_cast<__bf16*>(p)[k * kWave + lane] = static_cast<__bf16>(o[k] * inv);
-    else
-      p[k * kWave + lane] = o[k] * inv;
+      for (int e = 0; e < kAhead; ++e) {
+        // the item's start lies in the second slot of worker w, the rest in
+        // the first slots of w + 1 .. w1
+        const int x = x0 + e * kSets + set;
+        mk[e] = -INFINITY;
+        lk[e] = 0.f;
+        ok[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (x <= w1) {
+          const int64_t at = static_cast<int64_t>(x == w ? 2 * w + 1 : 2 * x) * MT + q;
+          mk[e] = a.part_ml[2 * at];
+          lk[e] = a.part_ml[2 * at + 1];
+          ok[e] = *reinterpret_cast<const f32x4*>(a.part + at * D + d);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) top = fmaxf(top, mk[e]);
+      const float old = m == -INFINITY ? 1.f : fast_exp2(m - top);
+      o *= old;
+      sum *= old;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const float f = mk[e] == -INFINITY ? 1.f : fast_exp2(mk[e] - top);   // (1: weight and sums are 0)
+        o += f * ok[e];
+        sum += f * lk[e];
+      }
+      m = top;
+    }
+#pragma unroll
+    for (int step = kLanes; step < kWave; step *= 2) {
+      const float mo = __shfl_xor(m, step), so = __shfl_xor(sum, step);
+      f32x4 oo;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) oo[e] = __shfl_xor(o[e], step);
+      const float top = fmaxf(m, mo);
+      const float f = m == -INFINITY ? 1.f : fast_exp2(m - top), fo = mo == -INFINITY ? 1.f : fast_exp2(mo - top);
+      o = f * o + fo * oo;
+      sum = f * sum + fo * so;
+      m = top;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    const int at = mt * MT + q, j = at / a.G, hq = h * a.G + (at - j * a.G);
+    if (set == 0) store_out(static_cast<E*>(a.out) + (r0 + j) * a.o_row + hq * a.o_head + d, o * inv);
+    if (a.lse && lane == 0) a.lse[static_cast<int64_t>(r0 + j) * a.H + hq] = 0.69314718f * (m + __log2f(sum));
   }
-  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(r0 + j) * a.H + hq] = 0.69314718f * (m + __log2f(sum));
 }
 
 // ---- launch
@@ -737,14 +814,15 @@ struct Plan {
 Plan plan_of(const AttentionArgs& a) {
   const int64_t mean = (static_cast<int64_t>(a.R) + a.B - 1) / a.B;
   const int64_t m = mean * (a.H / a.KV);
-  const bool narrow = a.dtype == VSV_F32 || a.D > 128;   // two query tiles a wave
   if (m <= 16) return {16, 128};
   if (m <= 32) return {32, 128};
-  if (m <= 64) return narrow ? Plan{64, 64} : Plan{64, 128};
-  if (narrow) return {128, 64};
+  if (m <= 64) return {64, 64};
   return m <= 128 ? Plan{128, 64} : Plan{256, 64};
 }
-int workers_of(const AttentionArgs& a) { return (a.cus > 0 ? a.cus : 256) * 2; }
+int workers_of(const AttentionArgs& a) {
+  const int w = (a.cus > 0 ? a.cus : 256) * 2;
+  return w < kMaxWorkers ? w : kMaxWorkers;
+}
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -754,37 +832,27 @@ hipError_t launch_t(AttentionArgs a, hipStream_t s) {
   a.G = a.H / a.KV;
   a.workers = workers_of(a) / 2 * S::kGroups;
   char* p = static_cast<char*>(a.work);
-  a.piece = reinterpret_cast<int32_t*>(p);
+  a.piece = reinterpret_cast<int4*>(p);
   p += align256(static_cast<size_t>(a.workers) * 16);
   a.part_ml = reinterpret_cast<float*>(p);
   p += align256(static_cast<size_t>(a.workers) * 2 * S::kMT * 8);
   a.part = reinterpret_cast<float*>(p);
-  attention_kernel<E, D, QT, WQ, WK><<<dim3(a.workers), dim3(kThreads), 0, s>>>(a);
+  attention_kernel<E, D, QT, WQ, WK><<<dim3(a.workers), dim3(S::kThreads), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attention_join_kernel<E, D, S::kMT><<<dim3(a.workers * (S::kMT / kJoinQueries)), dim3(kThreads), 0, s>>>(a);
+  attention_join_kernel<E, D, S::kMT><<<dim3(kJoinGroups), dim3(kJoinThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename E, int D>
 hipError_t launch_d(const AttentionArgs& a, hipStream_t s) {
-  const Plan p = plan_of(a);
-  if constexpr (sizeof(E) == 4 || D > 128) {
-    switch (p.mt) {
-      case 16: return launch_t<E, D, 1, 1, 4>(a, s);
-      case 32: return launch_t<E, D, 2, 1, 4>(a, s);
-      case 64: return launch_t<E, D, 2, 2, 2>(a, s);
-    }
-    return launch_t<E, D, 2, 4, 1>(a, s);
-  } else {
-    switch (p.mt) {
-      case 16: return launch_t<E, D, 1, 1, 4>(a, s);
-      case 32: return launch_t<E, D, 2, 1, 4>(a, s);
-      case 64: return launch_t<E, D, 4, 1, 4>(a, s);
-      case 128: return launch_t<E, D, 4, 2, 2>(a, s);
-    }
-    return launch_t<E, D, 4, 4, 1>(a, s);
+  switch (plan_of(a).mt) {
+    case 16: return launch_t<E, D, 1, 1, 4>(a, s);
+    case 32: return launch_t<E, D, 2, 1, 4>(a, s);
+    case 64: return launch_t<E, D, 2, 2, 2>(a, s);
+    case 128: return launch_t<E, D, 2, 4, 1>(a, s);
   }
+  return launch_t<E, D, 2, 8, 1>(a, s);
 }
 
 }  // namespace

@@ -34,7 +34,7 @@ struct AttentionArgs {
   int32_t workers;
   float* part;              // [2 * workers][MT][D] unnormalised sums of the pieces
   float* part_ml;           // [2 * workers][MT][2] their references and weights
-  int32_t* piece;           // [workers][4] item that starts in a worker and ends in a later one
+  int4* piece;              // [workers] item that starts in a worker and ends in a later one
 };
 
 // Most tiles that one request may come to (host check).
