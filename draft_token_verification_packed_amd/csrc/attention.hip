@@ -44,6 +44,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSlice = 32;     // tokens a wave takes at a time
+constexpr int kPages = 1024;   // pages looked up at a time
 
 // One 16 x 16 product over 32 of the inner dimension: lane l holds 8 inner
 // elements of row (column) l % 16, the same 8 in both factors.
@@ -94,11 +95,14 @@ struct Shape {
   static constexpr int kChunks = kRowBytes / 16;     // 16-byte chunks of a token's row
   static constexpr int kSliceBytes = kTokens * kRowBytes;
   static constexpr int kLoads = kSliceBytes / 16 / (kWave * WQ);   // chunks a lane brings of K (and of V)
-  // two workgroups of four waves share a CU where the LDS holds both, which
-  // hides what each does between its items; buffers: two where it holds them
-  static constexpr int kGroups = kThreads == 256 && WK * kSliceBytes <= 32 * 1024 ? 2 : 1;
+  // Two workgroups of four waves share a CU where the LDS holds both, which
+  // hides what each does between its items. Waves that share nothing keep one
+  // buffer and refill its halves as they are read; the others keep a ring.
+  static constexpr int kGroups = kThreads == 256 && WK * kSliceBytes * (WQ == 1 ? 1 : 2) <= 32 * 1024 ? 2 : 1;
   static constexpr int kWaves = kGroups * kThreads / 256;   // a SIMD's waves
-  static constexpr int kStages = kGroups * WK * kSliceBytes * 4 <= 128 * 1024 ? 2 : 1;
+  static constexpr int kFit = 128 * 1024 / (kGroups * WK * kSliceBytes * 2);
+  static constexpr int kStages = WQ == 1 ? 1 : kFit > 4 ? 4 : kFit;
+  static_assert(WQ == 1 || kStages >= 2, "shared slices are brought ahead");
   static_assert(kLoads <= (kChunks == 8 ? 8 : 16), "a lane of 16 for every load");
   // The row of the slice whose place lane (grp, col) of wave wq works out.
   __device__ static __forceinline__ int owned_row(int wq, int grp, int col) {
@@ -124,6 +128,7 @@ struct AttnScratch {
     } tile[S::kStages][WK];
     float join[WK][S::kMT][S::kOutStride];
   };
+  int page[kPages];   // the pages of the tiles at hand
   float ml[WK][S::kMT][2];
   float fin[S::kMT][2];
   uint64_t path[VSV_MAX_TREE_ROWS];
@@ -218,7 +223,20 @@ __device__ __forceinline__ void load_to_lds(int64_t from, uint32_t to) {
       : "s"(to), "v"(from)
       : "memory");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+// Wait until at most N of the wave's loads are under way (they end in order),
+// and for the LDS accesses it issued.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+// The same for all of them in a form that the compiler counts: its own loads
+// (the queries) are then known to have ended, and it puts no wait of its own,
+// which would be one for the tiles under way, before their uses in the loop.
+__device__ __forceinline__ void drain() {
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+  wait_loads<0>();
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 template <int... K, typename F>
 __device__ __forceinline__ void for_each_index(std::integer_sequence<int, K...>, F&& f) {
@@ -365,42 +383,51 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
     // of the group's lane k (2 k, 2 k + 1), and a broadcast inside the group
     // hands it on.
     const int my_row = min(S::owned_row(wq, grp, col), S::kTokens - 1);
-    auto look_up = [&](int t) -> int {
-      const int x = t * S::kTile + wk * S::kTokens + my_row;
-      int id = 0;
-      if (x < len) {
-        id = row_table[x >> a.page_shift];
+    // The pages of tiles tc .. te - 1, by the whole workgroup.
+    auto look_up = [&](int tc, int te) {
+      const int p0 = tc * S::kTile >> a.page_shift;
+      const int count = ((min(te * S::kTile, len) - 1) >> a.page_shift) + 1 - p0;
+      for (int p = tid; p < count; p += kThreads) {
+        int id = row_table[p0 + p];
         if (id < 0 || id >= a.num_pages) {
           bits |= VSV_FLAG_PAGES;
           id = 0;
         }
+        s.page[p] = id;
       }
-      return id;
     };
-    auto fetch = [&](int t, int id) {
-      const int stage = S::kStages > 1 ? (t & 1) : 0;
-      const uint32_t kd = __builtin_amdgcn_readfirstlane(lds_address(s.tile[stage][wk].k) + wq * kWave * 16);
-      const uint32_t vd = __builtin_amdgcn_readfirstlane(lds_address(s.tile[stage][wk].v) + wq * kWave * 16);
+    // The place of this lane's token of tile t (keys, values).
+    auto place = [&](int t, int p0, int64_t& kp, int64_t& vp) {
       const int x = t * S::kTile + wk * S::kTokens + my_row;
       const int own = min(max(x - len, 0), n - 1);   // behind the last token: any row that exists
-      int64_t kp = reinterpret_cast<int64_t>(kr_base) + own * a.k_row * static_cast<int64_t>(sizeof(E));
-      int64_t vp = reinterpret_cast<int64_t>(vr_base) + own * a.v_row * static_cast<int64_t>(sizeof(E));
+      kp = reinterpret_cast<int64_t>(kr_base) + own * a.k_row * static_cast<int64_t>(sizeof(E));
+      vp = reinterpret_cast<int64_t>(vr_base) + own * a.v_row * static_cast<int64_t>(sizeof(E));
+      const int id = s.page[x < len ? (x >> a.page_shift) - p0 : 0];
       const int64_t cached = (id * a.c_page + (x & page_mask) * a.c_token) * static_cast<int64_t>(sizeof(E));
       kp = x < len ? reinterpret_cast<int64_t>(kc_base) + cached : kp;
       vp = x < len ? reinterpret_cast<int64_t>(vc_base) + cached : vp;
+    };
+    auto fetch_k = [&](int t, int64_t kp) {
+      const uint32_t kd = __builtin_amdgcn_readfirstlane(lds_address(s.tile[t % S::kStages][wk].k) + wq * kWave * 16);
       for_each_index(std::make_integer_sequence<int, S::kLoads>(), [&](auto index) {
         constexpr int k = decltype(index)::value;
         const int c = slot0 + k * kWave * WQ;
-        const int row = c / C, pos = c % C;
-        load_to_lds(group_broadcast<k, C>(kp) + (pos ^ swizzle_k<C>(row)) * 16, kd + k * kWave * WQ * 16);
-        load_to_lds(group_broadcast<k, C>(vp) + (pos ^ swizzle_v<E, C>(row)) * 16, vd + k * kWave * WQ * 16);
+        load_to_lds(group_broadcast<k, C>(kp) + (c % C ^ swizzle_k<C>(c / C)) * 16, kd + k * kWave * WQ * 16);
+      });
+    };
+    auto fetch_v = [&](int t, int64_t vp) {
+      const uint32_t vd = __builtin_amdgcn_readfirstlane(lds_address(s.tile[t % S::kStages][wk].v) + wq * kWave * 16);
+      for_each_index(std::make_integer_sequence<int, S::kLoads>(), [&](auto index) {
+        constexpr int k = decltype(index)::value;
+        const int c = slot0 + k * kWave * WQ;
+        load_to_lds(group_broadcast<k, C>(vp) + (c % C ^ swizzle_v<E, C>(c / C)) * 16, vd + k * kWave * WQ * 16);
       });
     };
     // Values of the rows' own that are not finite would reach rows that do not see
     // them through a weight of 0, and so would what lies behind the last
     // token: both are 0 in the tile (the former are added at the end).
     auto clean = [&](int t) {
-      u32x4* vl = reinterpret_cast<u32x4*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].v);
+      u32x4* vl = reinterpret_cast<u32x4*>(s.tile[t % S::kStages][wk].v);
 #pragma unroll 1
       for (int k = 0; k < S::kLoads; ++k) {
         const int c = slot0 + k * kWave * WQ;
@@ -426,8 +453,10 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
       }
     };
 
-    // first loads: pages, parents, queries, then the tile that the pages tell
-    int ids = look_up(t0);
+    // first loads: pages, parents, queries
+    const int tiles_per_look = ((kPages - 1) << min(a.page_shift, 16)) / S::kTile;   // one page may be cut at its start
+    int te = min(t1, t0 + tiles_per_look);
+    look_up(t0, te);
     const int up = wave == 0 && a.parents && lane < n ? a.parents[r0 + lane] : 0;
     // ---- queries
     typename F::T qf[QT][KC];
@@ -444,10 +473,6 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
       row[qt] = live ? j : -1;
     }
 
-    if (S::kStages > 1) {
-      fetch(t0, ids);
-      ids = t0 + 1 < t1 ? look_up(t0 + 1) : 0;
-    }
     if (wave == 0) {
       bool off_tree;
       s.path[lane] = tree_paths(lane, n, up, a.parents == nullptr, off_tree);
@@ -471,11 +496,12 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
     }
 
     // One tile of this wave's slice, for its first NQ blocks of 16 queries.
-    auto compute = [&](auto live, int t) {
+    // `between` runs when the keys have been read, before the values are.
+    auto compute = [&](auto live, int t, auto between) {
       constexpr int NQ = decltype(live)::value;
       const int x0 = t * S::kTile + wk * S::kTokens;
-      const char* kl = reinterpret_cast<const char*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].k);
-      const char* vl = reinterpret_cast<const char*>(s.tile[S::kStages > 1 ? (t & 1) : 0][wk].v);
+      const char* kl = reinterpret_cast<const char*>(s.tile[t % S::kStages][wk].k);
+      const char* vl = reinterpret_cast<const char*>(s.tile[t % S::kStages][wk].v);
 #pragma unroll
       for (int sub = 0; sub < S::kSub; ++sub) {
 
@@ -556,6 +582,7 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
         }
         pf[qt] = F::pack(p);
       }
+      between();
       // O^T += V^T P^T
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
@@ -588,30 +615,82 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
     const int blocks = (M + 15) / 16;   // of 16 queries, dealt to the waves in turn
     const int mine = blocks > wq ? (blocks - wq + WQ - 1) / WQ : 0;
 
-    for (int t = t0; t < t1; ++t) {
-      const int x0 = t * S::kTile + wk * S::kTokens;
-      if (S::kStages == 1) {
-        if (WQ > 1 && t > t0) lds_barrier();   // the slice has been read
-        fetch(t, ids);
-        if (t + 1 < t1) ids = look_up(t + 1);
-      }
-      wait_loads();
-      if (x0 + S::kTokens > len) clean(t);
-      if (WQ > 1)
+    for (int tc = t0; tc < t1;) {
+      if (tc > t0) {
+        lds_barrier();   // the pages before have been read
+        te = min(t1, tc + tiles_per_look);
+        look_up(tc, te);
         lds_barrier();
-      else
-        wave_sync();
-      if (S::kStages > 1 && t + 1 < t1) {
-        // into the other buffer, which every wave has read before the barrier
-        fetch(t + 1, ids);
-        if (t + 2 < t1) ids = look_up(t + 2);
       }
-      // a slice behind the last token, or no query (no barrier below)
-      if (x0 >= end || mine == 0) continue;
-      if (WQ > 1 && QT == 2 && mine == 1)
-        compute(std::integral_constant<int, 1>(), t);
-      else
-        compute(std::integral_constant<int, QT>(), t);
+      const int p0 = tc * S::kTile >> a.page_shift;
+      int64_t kp, vp;
+      if constexpr (WQ == 1) {
+        // one buffer: the next keys are under way as soon as these have been
+        // read, the next values behind the product with these
+        place(tc, p0, kp, vp);
+        drain();
+        fetch_k(tc, kp);
+        fetch_v(tc, vp);
+        for (int t = tc; t < te; ++t) {
+          const int x0 = t * S::kTile + wk * S::kTokens;
+          const bool more = t + 1 < te;
+          wait_loads<S::kLoads>();
+          if (more) place(t + 1, p0, kp, vp);
+          auto between = [&]() {
+            if (more) {
+              wait_lds();
+              fetch_k(t + 1, kp);
+              wait_loads<S::kLoads>();
+            } else {
+              wait_loads<0>();
+            }
+            if (x0 + S::kTokens > len) clean(t);
+            wave_sync();
+          };
+          if (x0 < end)
+            compute(std::integral_constant<int, QT>(), t, between);
+          else
+            between();   // the slice lies behind the last token
+          if (more) {
+            wait_lds();
+            fetch_v(t + 1, vp);
+          }
+        }
+      } else {
+        // a ring of kStages tiles, of which kStages - 1 are under way
+        constexpr int L = 2 * S::kLoads, N = S::kStages;
+        drain();
+        for (int t = tc; t < min(te, tc + N - 1); ++t) {
+          place(t, p0, kp, vp);
+          fetch_k(t, kp);
+          fetch_v(t, vp);
+        }
+        for (int t = tc; t < te; ++t) {
+          const int behind = min(te - 1 - t, N - 2);   // tiles under way behind this one
+          if (N > 3 && behind == 2)
+            wait_loads<2 * L>();
+          else if (N > 2 && behind == 1)
+            wait_loads<L>();
+          else
+            wait_loads<0>();
+          const int x0 = t * S::kTile + wk * S::kTokens;
+          if (x0 + S::kTokens > len) clean(t);
+          lds_barrier();
+          if (t + N - 1 < te) {
+            // into the buffer of tile t - 1, which every wave has read
+            place(t + N - 1, p0, kp, vp);
+            fetch_k(t + N - 1, kp);
+            fetch_v(t + N - 1, vp);
+          }
+          if (x0 >= end || mine == 0) continue;   // a slice behind the last token, or no query
+          if (QT == 2 && mine == 1)
+            compute(std::integral_constant<int, 1>(), t, [] {});
+          else
+            compute(std::integral_constant<int, QT>(), t, [] {});
+        }
+      }
+      tc = te;
+      if (tc < t1 && WQ > 1) lds_barrier();   // the ring starts anew
     }
 
     // ---- join the slices, then the item's result or piece
