@@ -23,7 +23,11 @@
 // requests' lengths: each workgroup finds its span with a scan over the requests.
 // An item inside one span is finished there; the pieces of an item that
 // spans several go to scratch (reference, weight, sum) and a second kernel
-// joins them. WQ waves share a slice and split the queries; the WK slices of a tile go
+// joins them. (Pieces handed over inside the launch, the worker of an item's
+// first tiles waiting for the others, took 27 instead of 17 us for one
+// request of 1024 tokens and 169 instead of 112 us for two long ones: three
+// trips between XCDs one after another, and one workgroup to join 32
+// pieces.) WQ waves share a slice and split the queries; the WK slices of a tile go
 // to different waves, joined through LDS at the end of an item. With few
 // queries (WQ = 1) waves share nothing and meet no barrier in the loop.
 #include <type_traits>
@@ -110,8 +114,7 @@ struct Shape {
            : kChunks == 16 ? wq * 4 + grp + col * 4 * WQ
                            : wq * 2 + (grp >> 1) + col * 2 * WQ;
   }
-  static constexpr int kOut = 64;                    // columns of O joined at a time
-  static constexpr int kOutStride = kOut + 4;
+  static constexpr int kOutStride = D + 4;           // of a joined row of O, off the banks' period
 };
 
 struct Request {
@@ -131,6 +134,8 @@ struct AttnScratch {
   int page[kPages];   // the pages of the tiles at hand
   float ml[WK][S::kMT][2];
   float fin[S::kMT][2];
+  int64_t out_at[S::kMT];  // where a query's result goes
+  int lse_at[S::kMT];
   uint64_t path[VSV_MAX_TREE_ROWS];
   int64_t scan[S::kThreads / kWave];
   int64_t base;
@@ -261,6 +266,10 @@ __device__ __forceinline__ int64_t group_broadcast(int64_t v) {
   return __builtin_bit_cast(int64_t, o);
 }
 
+// Weight of sums taken relative to m where the common reference is `top`
+// (sums without a reference are 0).
+__device__ __forceinline__ float weight_of(float m, float top) { return m == -INFINITY ? 1.f : fast_exp2(m - top); }
+
 __device__ __forceinline__ void store_out(uint16_t* p, f32x4 o) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   *reinterpret_cast<bf16x4*>(p) = bf16x4{static_cast<__bf16>(o[0]), static_cast<__bf16>(o[1]), static_cast<__bf16>(o[2]),
@@ -307,9 +316,9 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
     before = units + block_scan64<kThreads>(size0, s.scan, total);
     units += total;
   }
-  if (tid == 0) a.piece[w].x = -1;
   if (w == 0 && bits && a.error_flag) atomicOr(a.error_flag, bits);
   bits = 0;
+  if (tid == 0) a.piece[w].x = -1;
   const int workers = static_cast<int>(min(static_cast<int64_t>(a.workers), units));
   if (w >= workers) return;
   units = uniform64(units);
@@ -473,6 +482,11 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
       row[qt] = live ? j : -1;
     }
 
+    for (int q = tid; q < M; q += kThreads) {
+      const int at = mt * S::kMT + q, j = at / a.G, hq = h * a.G + (at - j * a.G);
+      s.out_at[q] = (r0 + j) * a.o_row + hq * a.o_head;
+      s.lse_at[q] = (r0 + j) * a.H + hq;
+    }
     if (wave == 0) {
       bool off_tree;
       s.path[lane] = tree_paths(lane, n, up, a.parents == nullptr, off_tree);
@@ -693,9 +707,8 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
       if (tc < t1 && WQ > 1) lds_barrier();   // the ring starts anew
     }
 
-    // ---- join the slices, then the item's result or piece
-    const bool whole = t0 == 0 && t1 == rq.tiles;
-    const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
+    // ---- join the slices of the workgroup
+    const bool first = t0 == 0, last = t1 == rq.tiles;
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
       l[qt] += __shfl_xor(l[qt], 16);
@@ -706,7 +719,7 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
         s.ml[wk][q][1] = l[qt];
       }
     }
-    lds_barrier();
+    lds_barrier();   // (and the tiles have been read)
     const bool odd = s.odd != 0;
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
@@ -721,71 +734,56 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
         sum += mk == -INFINITY ? s.ml[k][q][1] : s.ml[k][q][1] * fast_exp2((mk - m) * a.scale);
       }
       const float f = mref[qt] == -INFINITY ? 1.f : fast_exp2((mref[qt] - m) * a.scale);
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) acc[dt][qt] *= f;
       if (grp == 0 && wk == 0) {
         s.fin[q][0] = m * a.scale;
         s.fin[q][1] = sum;
       }
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(&s.join[wk][q][dt * 16 + grp * 4]) = acc[dt][qt] * f;
     }
+    lds_barrier();
+    constexpr int kQuads = D / 4;
+    // this workgroup's part of 4 columns of a query
+    auto part = [&](int q, int d) {
+      f32x4 o = *reinterpret_cast<const f32x4*>(&s.join[0][q][d]);
 #pragma unroll
-    for (int d0 = 0; d0 < D; d0 += S::kOut) {
-      lds_barrier();   // tiles, or the columns before, have been read
+      for (int k = 1; k < WK; ++k) o += *reinterpret_cast<const f32x4*>(&s.join[k][q][d]);
+      if (odd) {
+        // values that are not finite, for the rows that see them
+        const uint64_t seen_rows = s.path[(mt * S::kMT + q) / a.G];
+        for (int x = max(t0 * S::kTile, len); x < min(t1 * S::kTile, end); ++x) {
+          if (!(seen_rows >> (x - len) & 1)) continue;
+          const E* p = static_cast<const E*>(a.v) + static_cast<int64_t>(r0 + x - len) * a.v_row + h * a.v_head;
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-        for (int dt = 0; dt < S::kOut / 16; ++dt)
-          *reinterpret_cast<f32x4*>(&s.join[wk][(qt * WQ + wq) * 16 + col][dt * 16 + grp * 4]) = acc[d0 / 16 + dt][qt];
-      lds_barrier();
-      constexpr int kQuads = S::kOut / 4;
-      for (int c = tid; c < M * kQuads; c += kThreads) {
-        const int q = c / kQuads, d = (c % kQuads) * 4;
-        f32x4 o = *reinterpret_cast<const f32x4*>(&s.join[0][q][d]);
-#pragma unroll
-        for (int k = 1; k < WK; ++k) o += *reinterpret_cast<const f32x4*>(&s.join[k][q][d]);
-        if (odd) {
-          // values that are not finite, for the rows that see them
-          const uint64_t seen_rows = s.path[(mt * S::kMT + q) / a.G];
-          for (int x = max(t0 * S::kTile, len); x < min(t1 * S::kTile, end); ++x) {
-            if (!(seen_rows >> (x - len) & 1)) continue;
-            const E* p = static_cast<const E*>(a.v) + static_cast<int64_t>(r0 + x - len) * a.v_row + h * a.v_head;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float f = Elem<E>::at(p, d0 + d + e);
-              if (!(fabsf(f) < INFINITY)) o[e] += f;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float f = Elem<E>::at(p, d + e);
+            if (!(fabsf(f) < INFINITY)) o[e] += f;
           }
         }
-        if (whole) {
-          const float sum = s.fin[q][1];
-          const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN stays one
-          const int at = mt * S::kMT + q, j = at / a.G, hq = h * a.G + (at - j * a.G);
-          E* p = static_cast<E*>(a.out) + (r0 + j) * a.o_row + hq * a.o_head + d0 + d;
-          store_out(p, o * inv);
-        } else {
-          *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(slot) * S::kMT + q) * D + d0 + d) = o;
-        }
+      }
+      return o;
+    };
+    const int64_t at = static_cast<int64_t>(first ? 2 * w + 1 : 2 * w) * S::kMT;   // of a piece
+    for (int c = tid; c < M * kQuads; c += kThreads) {
+      const int q = c / kQuads, d = c % kQuads * 4;
+      const f32x4 o = part(q, d);
+      if (first && last) {
+        const float m = s.fin[q][0], sum = s.fin[q][1];
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // a NaN stays one
+        store_out(static_cast<E*>(a.out) + s.out_at[q] + d, o * inv);
+        if (d == 0 && a.lse) a.lse[s.lse_at[q]] = 0.69314718f * (m + __log2f(sum));
+      } else {
+        *reinterpret_cast<f32x4*>(a.part + (at + q) * D + d) = o;
+        if (d == 0) a.part_ml[at + q] = make_float2(s.fin[q][0], s.fin[q][1]);
       }
     }
-    if (whole) {
-      if (a.lse)
-        for (int q = tid; q < M; q += kThreads) {
-          const int at = mt * S::kMT + q, j = at / a.G, hq = h * a.G + (at - j * a.G);
-          a.lse[static_cast<int64_t>(r0 + j) * a.H + hq] = 0.69314718f * (s.fin[q][0] + __log2f(s.fin[q][1]));
-        }
-    } else {
-      for (int q = tid; q < M; q += kThreads) {
-        a.part_ml[(static_cast<int64_t>(slot) * S::kMT + q) * 2] = s.fin[q][0];
-        a.part_ml[(static_cast<int64_t>(slot) * S::kMT + q) * 2 + 1] = s.fin[q][1];
-      }
-      if (t0 == 0 && tid == 0) {
-        // the worker whose span holds the item's last tile
-        const int64_t last = u - 1 + (rq.tiles - t1);
-        int w1 = static_cast<int>(((last + 1) * workers - 1) / units);
-        while (span_start(units, w1 + 1, workers) <= last) ++w1;
-        while (span_start(units, w1, workers) > last) --w1;
-        a.piece[w] = make_int4(r0, h, mt, w1 * 512 + M);
-      }
+    if (first && !last && tid == 0) {
+      // the worker whose span holds the item's last tile
+      const int64_t end_unit = u - 1 + (rq.tiles - t1);
+      int x = static_cast<int>(((end_unit + 1) * workers - 1) / units);
+      while (span_start(units, x + 1, workers) <= end_unit) ++x;
+      while (span_start(units, x, workers) > end_unit) --x;
+      a.piece[w] = make_int4(r0, h, mt, x * 512 + M);
     }
     lds_barrier();   // paths and joined columns are free again
   }
@@ -845,20 +843,21 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
         ok[e] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (x <= w1) {
           const int64_t at = static_cast<int64_t>(x == w ? 2 * w + 1 : 2 * x) * MT + q;
-          mk[e] = a.part_ml[2 * at];
-          lk[e] = a.part_ml[2 * at + 1];
+          const float2 ml = a.part_ml[at];
+          mk[e] = ml.x;
+          lk[e] = ml.y;
           ok[e] = *reinterpret_cast<const f32x4*>(a.part + at * D + d);
         }
       }
       float top = m;
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) top = fmaxf(top, mk[e]);
-      const float old = m == -INFINITY ? 1.f : fast_exp2(m - top);
+      const float old = weight_of(m, top);
       o *= old;
       sum *= old;
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
-        const float f = mk[e] == -INFINITY ? 1.f : fast_exp2(mk[e] - top);   // (1: weight and sums are 0)
+        const float f = weight_of(mk[e], top);
         o += f * ok[e];
         sum += f * lk[e];
       }
@@ -871,7 +870,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 #pragma unroll
       for (int e = 0; e < 4; ++e) oo[e] = __shfl_xor(o[e], step);
       const float top = fmaxf(m, mo);
-      const float f = m == -INFINITY ? 1.f : fast_exp2(m - top), fo = mo == -INFINITY ? 1.f : fast_exp2(mo - top);
+      const float f = weight_of(m, top), fo = weight_of(mo, top);
       o = f * o + fo * oo;
       sum = f * sum + fo * so;
       m = top;
@@ -896,7 +895,8 @@ Plan plan_of(const AttentionArgs& a) {
   if (m <= 16) return {16, 128};
   if (m <= 32) return {32, 128};
   if (m <= 64) return {64, 64};
-  return m <= 128 ? Plan{128, 64} : Plan{256, 64};
+  // (a row of 256 columns leaves no LDS to join 256 queries in)
+  return m <= 128 || a.D > 128 ? Plan{128, 64} : Plan{256, 64};
 }
 int workers_of(const AttentionArgs& a) {
   const int w = (a.cus > 0 ? a.cus : 256) * 2;
@@ -913,7 +913,7 @@ hipError_t launch_t(AttentionArgs a, hipStream_t s) {
   char* p = static_cast<char*>(a.work);
   a.piece = reinterpret_cast<int4*>(p);
   p += align256(static_cast<size_t>(a.workers) * 16);
-  a.part_ml = reinterpret_cast<float*>(p);
+  a.part_ml = reinterpret_cast<float2*>(p);
   p += align256(static_cast<size_t>(a.workers) * 2 * S::kMT * 8);
   a.part = reinterpret_cast<float*>(p);
   attention_kernel<E, D, QT, WQ, WK><<<dim3(a.workers), dim3(S::kThreads), 0, s>>>(a);
@@ -925,13 +925,14 @@ hipError_t launch_t(AttentionArgs a, hipStream_t s) {
 
 template <typename E, int D>
 hipError_t launch_d(const AttentionArgs& a, hipStream_t s) {
-  switch (plan_of(a).mt) {
-    case 16: return launch_t<E, D, 1, 1, 4>(a, s);
-    case 32: return launch_t<E, D, 2, 1, 4>(a, s);
-    case 64: return launch_t<E, D, 2, 2, 2>(a, s);
-    case 128: return launch_t<E, D, 2, 4, 1>(a, s);
+  const int mt = plan_of(a).mt;
+  if (mt == 16) return launch_t<E, D, 1, 1, 4>(a, s);
+  if (mt == 32) return launch_t<E, D, 2, 1, 4>(a, s);
+  if (mt == 64) return launch_t<E, D, 2, 2, 2>(a, s);
+  if constexpr (D <= 128) {
+    if (mt == 256) return launch_t<E, D, 2, 8, 1>(a, s);
   }
-  return launch_t<E, D, 2, 8, 1>(a, s);
+  return launch_t<E, D, 2, 4, 1>(a, s);
 }
 
 }  // namespace

@@ -32,9 +32,9 @@ struct AttentionArgs {
   // set at launch
   int32_t G;                // query heads per key head
   int32_t workers;
-  float* part;              // [2 * workers][MT][D] unnormalised sums of the pieces
-  float* part_ml;           // [2 * workers][MT][2] their references and weights
   int4* piece;              // [workers] item that starts in a worker and ends in a later one
+  float2* part_ml;          // [2 * workers][MT] references and weights of the pieces
+  float* part;              // [2 * workers][MT][D] unnormalised sums
 };
 
 // Most tiles that one request may come to (host check).
