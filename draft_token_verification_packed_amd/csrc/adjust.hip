@@ -73,6 +73,8 @@ __device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float(stat
 __device__ __forceinline__ void narrow(float f, float* p) { *p = f; }
 __device__ __forceinline__ void narrow(float f, uint16_t* p) { *p = static_cast<uint16_t>(to_bf16(f)); }
 
+constexpr int kRows = 8;   // rows of a request a workgroup takes at a time
+
 template <int SL>
 struct AdjustScratch {
   uint32_t count[SL];       // 2 * occurrences in output and path, + 1 if in the prompt
@@ -101,10 +103,10 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
     return;
   }
   const int n = o1 - o0;
-  // this workgroup's rows of the request
-  const int j0 = static_cast<int>(static_cast<int64_t>(n) * group / a.groups);
-  const int j1 = static_cast<int>(static_cast<int64_t>(n) * (group + 1) / a.groups);
-  if (j0 == j1) return;
+  // this workgroup's rows of the request: every groups-th block of kRows
+  const int j0 = group * kRows;
+  if (j0 >= n) return;
+  auto row_after = [&](int j) { return (j + 1) % kRows ? j + 1 : j + 1 + (a.groups - 1) * kRows; };
 
   float rho = a.repetition ? a.repetition[i] : 1.f;
   float freq = a.frequency ? a.frequency[i] : 0.f;
@@ -160,15 +162,22 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
       prompt = max(0, min(prompt, end));
     }
     const int* __restrict__ h = a.history + static_cast<int64_t>(i) * a.hist_ld;
+    // four tokens a load, kU loads under way
     constexpr int kU = 4;
-    for (int k = tid; k < end; k += NT * kU) {
-      int tok[kU];
+    const int quads = end >> 2;
+    for (int k = tid; k < quads; k += NT * kU) {
+      u32x4 tok[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) tok[u] = k + u * NT < end ? h[k + u * NT] : 0;
+      for (int u = 0; u < kU; ++u) tok[u] = reinterpret_cast<const u32x4_4*>(h)[min(k + u * NT, quads - 1)];
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (k + u * NT < end) add(tok[u], k + u * NT < prompt ? 1u : 2u);
+      for (int u = 0; u < kU; ++u) {
+        const int at = (k + u * NT) * 4;
+        if (at >= end - 3) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add(static_cast<int>(tok[u][e]), at + e < prompt ? 1u : 2u);
+      }
     }
+    for (int k = quads * 4 + tid; k < end; k += NT) add(h[k], k < prompt ? 1u : 2u);
   }
   if (biased) {
     for (int k = b0 + tid; k < b1; k += NT) {
@@ -229,13 +238,28 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
   const E* xs = static_cast<const E*>(a.x) + v0;
   E* ys = static_cast<E*>(a.y) + v0;
   const uint8_t* touched = reinterpret_cast<const uint8_t*>(s.touched);
+  // a row's logits and the bytes of its mask, one row ahead of its use
   Vec8<E> buf[kPer];
+  uint32_t allow_buf[kPer];
+  const uint8_t* mask_buf = nullptr;
   auto load_row = [&](int j) {
     const E* row = xs + static_cast<int64_t>(o0 + j) * a.ld;
+    mask_buf = nullptr;
+    if (a.mask) {
+      const int m = a.mask_index ? a.mask_index[o0 + j] : o0 + j;
+      if (m >= a.mask_rows)
+        bits |= VSV_FLAG_LAYOUT;
+      else if (m >= 0)
+        mask_buf = reinterpret_cast<const uint8_t*>(a.mask + static_cast<int64_t>(m) * a.mask_ld) + (v0 >> 3);
+    }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int q = (k * NT + tid) * 8;
-      if (q + 8 <= vn) buf[k].load(row + q);
+      allow_buf[k] = 0xFFu;
+      if (q + 8 <= vn) {
+        if (!kInPlace) buf[k].load(row + q);
+        if (mask_buf) allow_buf[k] = mask_buf[q >> 3];
+      }
     }
   };
   // Counts of row j's path, from those of row `from` (-1: none).
@@ -259,51 +283,46 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
       }
     }
   };
-  if (!kInPlace) load_row(j0);
-  for (int j = j0; j < j1; ++j) {
-    move_path(j == j0 ? -1 : j - 1, j);
-    const uint32_t* mask = nullptr;
-    if (a.mask) {
-      const int m = a.mask_index ? a.mask_index[o0 + j] : o0 + j;
-      if (m >= a.mask_rows)
-        bits |= VSV_FLAG_LAYOUT;
-      else if (m >= 0)
-        mask = a.mask + static_cast<int64_t>(m) * a.mask_ld + (v0 >> 5);
-    }
+  load_row(j0);
+  for (int j = j0, from = -1; j < n; from = j, j = row_after(j)) {
+    move_path(from, j);
     lds_barrier();
     const E* row = xs + static_cast<int64_t>(o0 + j) * a.ld;
     E* out = ys + static_cast<int64_t>(o0 + j) * a.out_ld;
     Vec8<E> cur[kPer];
+    uint32_t allow[kPer];
+    const uint8_t* mask = mask_buf;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) cur[k] = buf[k];
-    if (!kInPlace && j + 1 < j1) load_row(j + 1);
+    for (int k = 0; k < kPer; ++k) {
+      cur[k] = buf[k];
+      allow[k] = allow_buf[k];
+    }
+    if (row_after(j) < n) load_row(row_after(j));
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int q = (k * NT + tid) * 8;
       if (q + 8 <= vn) {
-        uint32_t hit = touched[q >> 3];
-        const uint32_t allow = mask ? (mask[q >> 5] >> (q & 31)) & 0xFFu : 0xFFu;
-        hit &= allow;
+        const uint32_t hit = touched[q >> 3] & allow[k];
         if (kInPlace) {
-          if (hit == 0 && allow == 0xFFu) continue;
-          if (allow) cur[k].load(row + q);
+          if (hit == 0 && allow[k] == 0xFFu) continue;
+          if (allow[k]) cur[k].load(row + q);
         }
         if (hit) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (hit >> e & 1u) cur[k].put(e, fix(cur[k].get(e), q + e));
         }
-        if (allow != 0xFFu) {
+        if (allow[k] != 0xFFu) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (!(allow >> e & 1u)) cur[k].put(e, -INFINITY);
+            if (!(allow[k] >> e & 1u)) cur[k].put(e, -INFINITY);
         }
         cur[k].store(out + q);
       } else {
         for (int e = q; e < vn && e < q + 8; ++e) {
           float x = widen(row[e]);
           if (touched[e >> 3] >> (e & 7) & 1) x = fix(x, e);
-          if (mask && !(mask[e >> 5] >> (e & 31) & 1u)) x = -INFINITY;
+          if (mask && !(mask[e >> 3] >> (e & 7) & 1)) x = -INFINITY;
           narrow(x, out + e);
         }
       }
@@ -316,13 +335,11 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
 template <typename E, int NT, int SL>
 hipError_t launch_t(AdjustArgs a, hipStream_t s) {
   a.slices = (a.V + SL - 1) / SL;
-  // rows of a request are shared out where there is little else to do
+  // a request's rows in blocks of kRows to as many workgroups as twice the
+  // mean request fills (longer ones go round)
   const int64_t base = static_cast<int64_t>(a.B) * a.slices;
-  const int64_t want = 2 * static_cast<int64_t>(a.cus > 0 ? a.cus : 256);
-  int64_t groups = base > 0 ? want / base : 1;
   const int64_t mean = (a.R + a.B - 1) / a.B;
-  if (groups > mean) groups = mean;
-  a.groups = static_cast<int32_t>(groups < 1 ? 1 : groups);
+  a.groups = mean <= kRows ? 1 : static_cast<int32_t>((2 * mean + kRows - 1) / kRows);
   const int64_t grid = base * a.groups;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (a.x == a.y)
@@ -334,9 +351,13 @@ hipError_t launch_t(AdjustArgs a, hipStream_t s) {
 
 template <typename E>
 hipError_t launch_e(const AdjustArgs& a, hipStream_t s) {
+#ifdef VSV_SL
+  return launch_t<E, VSV_NT, VSV_SL>(a, s);
+#else
   const int64_t large = static_cast<int64_t>(a.B) * ((a.V + 8191) / 8192);
   return large >= 2 * static_cast<int64_t>(a.cus > 0 ? a.cus : 256) ? launch_t<E, 512, 8192>(a, s)
                                                                      : launch_t<E, 256, 2048>(a, s);
+#endif
 }
 
 }  // namespace
