@@ -731,37 +731,77 @@ def distill_loss(student_logits, teacher_ids, teacher_logits, teacher_lse=None, 
     return _DistillLoss.apply(student_logits, teacher_ids, teacher_logits, teacher_lse, float(temperature), error_flag)
 
 
+def _in(t, n, dtype, device, name):
+    """Address of an input vector (None: 0), checked like _vec and to lie on `device`."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != device or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        _vec(t, n, dtype, name)
+        _same_device(device, t)
+    return t.data_ptr()
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.device
+
+
+def _matrix(t, rows, width, device, name):
+    """(address, row stride) of an int32 matrix of unit column stride."""
+    if (t.dtype is not torch.int32 or t.device != device or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < width or
+            (t.shape[1] > 1 and t.stride(1) != 1)):
+        raise ValueError("%s must be an int32 matrix [%d, >= %d] on %s with unit column stride" %
+                         (name, rows, width, device))
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.shape[1], 1)
+
+
 def verify_greedy_tree(logits, row_offsets, row_owner, draft_tokens, parents, vocab=None, ws=None, stream=None):
     """Greedy verification of trees of drafts (vsv_verify_greedy_tree).
 
     `parents` (int32 [R], a row's parent counted from its request's first
     row; the roots' entries are not read) or None for chains. At most
-    MAX_TREE_ROWS rows a request. Returns verify_greedy's dict with out_rows
-    [R]: the rows of every accepted path at out_offsets, -1 behind them."""
-    dev = logits.device
-    if not logits.is_cuda or not row_offsets.is_cuda or row_offsets.dim() != 1 or row_offsets.numel() < 1:
-        raise ValueError("logits and row_offsets must be CUDA tensors, row_offsets a vector of B + 1")
-    _same_device(dev, row_offsets, row_owner, draft_tokens, parents)
-    if parents is not None:
-        _vec(parents, logits.shape[0], torch.int32, "parents")
+    MAX_TREE_ROWS rows a request. Returns verify_greedy's dict (without
+    slow_rows) with out_rows [R]: the rows of every accepted path at
+    out_offsets, -1 behind them."""
+    dev = _cuda(logits, "logits")
+    dtype, V, ld = _logits(logits, vocab)
+    R, B, i32 = logits.shape[0], row_offsets.numel() - 1, torch.int32
+    if B < 0:
+        raise ValueError("row_offsets must be a vector of B + 1")
+    batch = Batch(logits.data_ptr(), dtype, V, ld, B, R, _in(row_offsets, B + 1, i32, dev, "row_offsets"),
+                  _in(row_owner, R, i32, dev, "row_owner"),
+                  _in(draft_tokens, R - B, i32, dev, "draft_tokens") if R > B else None)
+    par = _in(parents, R, i32, dev, "parents")
     on = _on(dev, stream)
     with on as s:
-        st = torch.cuda.current_stream(dev)
-        batch, outs, out, B, R = _prepare(logits, row_offsets, row_owner, draft_tokens, vocab, st)
-        rows = torch.full((max(R, 1),), -1, dtype=torch.int32, device=dev)
-        ws = workspace(B, R, False, dev, st) if ws is None else ws
+        if ws is None and torch.cuda.is_current_stream_capturing():
+            # a graph's own, so that it shares none with another one
+            ws = torch.empty(lib().vsv_workspace_bytes(B, R, 0), dtype=torch.uint8, device=dev)
+            _check(lib().vsv_workspace_init(ws.data_ptr(), ws.numel(), s))
+        elif ws is None:
+            ws = _ws_cache.get((dev.index, s))
+            if ws is None or ws.numel() < lib().vsv_workspace_bytes(B, R, 0):
+                ws = workspace(B, R, False, dev, on.other if on.other is not None else torch.cuda.current_stream(dev))
+        words = torch.empty(3 * B + 1 + 4 * R, dtype=i32, device=dev)
+        acc, nxt, offs, toks, rows, tok, lse = torch.split_with_sizes(words, (B, B, B + 1, R, R, R, R))
+        flag = _new_flag(dev, s)
+        base = words.data_ptr()
+        r0 = base + 4 * (3 * B + 1)
+        outs = Outputs(base, base + 4 * B, base + 8 * B, r0, r0 + 8 * R, r0 + 12 * R, flag.data_ptr(), None)
         on.keep(logits, row_offsets, row_owner, draft_tokens, parents, ws)
-        _check(lib().vsv_verify_greedy_tree(ctypes.byref(batch), _at(parents), ctypes.byref(outs), _at(rows),
-                                            _at(ws), ws.numel(), s))
-    out["out_rows"] = rows
-    return out
+        _check(lib().vsv_verify_greedy_tree(ctypes.byref(batch), par, ctypes.byref(outs), r0 + 4 * R, ws.data_ptr(),
+                                            ws.numel(), s))
+    return dict(accepted_len=acc, next_token=nxt, out_offsets=offs, out_tokens=toks, out_rows=rows, row_token=tok,
+                row_lse=lse.view(torch.float32), error_flag=flag)
 
 
 def _heads(t, shape, dtype, device, name):
-    if (not t.is_cuda or t.dtype != dtype or t.device != device or tuple(t.shape) != shape or
-            (t.numel() and t.stride(-1) != 1)):
+    """Strides of a tensor of `shape` with unit last stride."""
+    st = t.stride()
+    if t.dtype is not dtype or t.device != device or t.shape != shape or (st[-1] != 1 and t.numel()):
         raise ValueError("%s must be a %s tensor %s on %s with unit last stride" % (name, dtype, list(shape), device))
-    return t
+    return st
 
 
 def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, parents=None, scale=None, out=None,
@@ -779,51 +819,40 @@ def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, 
     with return_lse also the scores' log-sum-exp [R, H]. Rows get no gradient."""
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q and k must be [rows, heads, dim], the caches [pages, page_size, heads, dim]")
-    dtype, dev = _dtype_code(q), q.device
+    dtype, dev, i32 = _dtype_code(q), _cuda(q, "q"), torch.int32
     R, H, D = q.shape
     KV, (pages, page) = k.shape[1], k_cache.shape[:2]
-    B = row_offsets.numel() - 1
-    for t, shape, name in ((q, (R, H, D), "q"), (k, (R, KV, D), "k"), (v, (R, KV, D), "v"),
-                           (k_cache, (pages, page, KV, D), "k_cache"), (v_cache, (pages, page, KV, D), "v_cache")):
-        _heads(t, shape, q.dtype, dev, name)
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, k_cache, v_cache)):
-        raise NotImplementedError("tree_attention has no backward pass")
-    if k_cache.stride() != v_cache.stride():
+    B, W = row_offsets.numel() - 1, block_table.shape[-1]
+    qs, ks, vs = (_heads(t, s, q.dtype, dev, n) for t, s, n in ((q, (R, H, D), "q"), (k, (R, KV, D), "k"), (v, (R, KV, D), "v")))
+    cs = _heads(k_cache, (pages, page, KV, D), q.dtype, dev, "k_cache")
+    if _heads(v_cache, (pages, page, KV, D), q.dtype, dev, "v_cache") != cs:
         raise ValueError("k_cache and v_cache must have the same strides")
-    _vec(row_offsets, B + 1, torch.int32, "row_offsets")
-    _vec(length, B, torch.int32, "length")
-    if parents is not None:
-        _vec(parents, R, torch.int32, "parents")
-    if (not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or
-            block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-        raise ValueError("block_table must be an int32 CUDA matrix [B, W] with unit column stride")
-    _same_device(dev, row_offsets, length, parents, block_table)
-    _flag(error_flag, dev)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or k_cache.requires_grad or
+                                    v_cache.requires_grad):
+        raise NotImplementedError("tree_attention has no backward pass")
+    off = _in(row_offsets, B + 1, i32, dev, "row_offsets")
+    lens = _in(length, B, i32, dev, "length")
+    par = _in(parents, R, i32, dev, "parents")
+    err = _in(error_flag, 1, i32, dev, "error_flag")
+    table, table_ld = _matrix(block_table, B, 0, dev, "block_table")
     if out is not None:
-        _heads(out, (R, H, D), q.dtype, dev, "out")
+        os_ = _heads(out, (R, H, D), q.dtype, dev, "out")
     on = _on(dev, stream)
     with on as s:
         if out is None:
             out = torch.empty((R, H, D), dtype=q.dtype, device=dev)
+            os_ = (H * D, D, 1)
         lse = torch.empty((R, H), dtype=torch.float32, device=dev) if return_lse else None
-        W = block_table.shape[1]
-        a = Attention(_at(q), _at(k), _at(v), _at(k_cache), _at(v_cache), _at(out), _at(lse),
-                      *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2], *k_cache.stride()[:3],
-                      dtype, D, H, KV, B, R, _at(row_offsets), _at(parents), _at(length), _at(block_table),
-                      block_table.stride(0) if B > 1 else max(W, 1), W, pages, page,
+        a = Attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+                      _at(lse), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], cs[0], cs[1], cs[2],
+                      dtype, D, H, KV, B, R, off, par, lens, table, table_ld, W, pages, page,
                       D ** -0.5 if scale is None else float(scale))
-        n = lib().vsv_tree_attention_workspace_bytes(ctypes.byref(a))
+        ref = ctypes.byref(a)
+        n = lib().vsv_tree_attention_workspace_bytes(ref)
         ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         on.keep(q, k, v, row_offsets, k_cache, v_cache, block_table, length, parents, out, error_flag)
-        _check(lib().vsv_tree_attention(ctypes.byref(a), _at(error_flag), _at(ws), n, s))
+        _check(lib().vsv_tree_attention(ref, err, _at(ws), n, s))
     return (out, lse) if return_lse else out
-
-
-def _adjust_vec(t, n, dtype, name, device):
-    if t is not None:
-        _vec(t, n, dtype, name)
-        _same_device(device, t)
-    return _at(t)
 
 
 def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None, history_len=None, prompt_len=None,
@@ -845,58 +874,56 @@ def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None,
     themselves, of which only the touched elements then move; rows of no
     request are left as they are in it."""
     dtype, V, ld = _logits(logits, vocab)
-    R, dev = logits.shape[0], logits.device
+    R, dev, i32, f32 = logits.shape[0], logits.device, torch.int32, torch.float32
     B = row_offsets.numel() - 1
-    at = lambda t, n, dt, name: _adjust_vec(t, n, dt, name, dev)
-    a = Adjust(logits=_at(logits), dtype=dtype, vocab=V, ld=ld, num_requests=B, num_rows=R)
-    a.row_offsets = at(row_offsets, B + 1, torch.int32, "row_offsets")
+    off = _in(row_offsets, B + 1, i32, dev, "row_offsets")
+    drafts = None
     if R > B:
-        _vec(draft_tokens, R - B, torch.int32, "draft_tokens")
-        a.draft_tokens = at(draft_tokens, R - B, torch.int32, "draft_tokens")
-    a.parents = at(parents, R, torch.int32, "parents")
+        if draft_tokens is None:
+            raise ValueError("draft_tokens: %d rows carry drafts" % (R - B))
+        drafts = _in(draft_tokens, R - B, i32, dev, "draft_tokens")
+    par = _in(parents, R, i32, dev, "parents")
+    hist, hist_ld, width, prompt, used = None, 0, 0, None, None
     if history is not None:
-        if (not history.is_cuda or history.dtype != torch.int32 or history.dim() != 2 or history.shape[0] != B or
-                (history.shape[1] > 1 and history.stride(1) != 1) or history_len is None):
-            raise ValueError("history must be an int32 CUDA matrix [B, H] with unit column stride, with history_len")
-        _same_device(dev, history)
-        a.history, a.history_width = _at(history), history.shape[1]
-        a.history_ld = history.stride(0) if B > 1 else max(history.shape[1], 1)
-        a.history_len = at(history_len, B, torch.int32, "history_len")
-        a.prompt_len = at(prompt_len, B, torch.int32, "prompt_len")
-    a.repetition = at(repetition, B, torch.float32, "repetition")
-    a.frequency = at(frequency, B, torch.float32, "frequency")
-    a.presence = at(presence, B, torch.float32, "presence")
+        if history_len is None:
+            raise ValueError("history needs history_len")
+        hist, hist_ld = _matrix(history, B, 0, dev, "history")
+        width = history.shape[1]
+        used = _in(history_len, B, i32, dev, "history_len")
+        prompt = _in(prompt_len, B, i32, dev, "prompt_len")
+    rep = _in(repetition, B, f32, dev, "repetition")
+    freq = _in(frequency, B, f32, dev, "frequency")
+    pres = _in(presence, B, f32, dev, "presence")
+    boff, btok, bval, n = None, None, None, 0
     if bias_offsets is not None:
+        boff = _in(bias_offsets, B + 1, i32, dev, "bias_offsets")
         n = 0 if bias_tokens is None else bias_tokens.numel()
-        a.bias_offsets, a.num_bias = at(bias_offsets, B + 1, torch.int32, "bias_offsets"), n
         if n:
-            _vec(bias_values, n, torch.float32, "bias_values")
-            a.bias_tokens = at(bias_tokens, n, torch.int32, "bias_tokens")
-            a.bias_values = at(bias_values, n, torch.float32, "bias_values")
+            if bias_values is None:
+                raise ValueError("bias_tokens need bias_values")
+            btok = _in(bias_tokens, n, i32, dev, "bias_tokens")
+            bval = _in(bias_values, n, f32, dev, "bias_values")
+    mp, mask_ld, masks, midx = None, 0, 0, None
     if mask is not None:
-        if (not mask.is_cuda or mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[1] < (V + 31) // 32 or
-                (mask.shape[1] > 1 and mask.stride(1) != 1)):
-            raise ValueError("mask must be an int32 CUDA matrix [M, >= (vocab + 31) // 32] with unit column stride")
-        _same_device(dev, mask)
-        if mask_index is None and mask.shape[0] < R:
+        masks = mask.shape[0]
+        mp, mask_ld = _matrix(mask, masks, (V + 31) // 32, dev, "mask")
+        if mask_index is None and masks < R:
             raise ValueError("without mask_index every row needs a row of mask")
-        a.mask, a.num_masks = _at(mask), mask.shape[0]
-        a.mask_ld = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
-        a.mask_index = at(mask_index, R, torch.int32, "mask_index")
-    _flag(error_flag, dev)
+        midx = _in(mask_index, R, i32, dev, "mask_index")
+    err = _in(error_flag, 1, i32, dev, "error_flag")
     if out is not None:
         odt, _, old = _logits(out, V)
         if odt != dtype or out.shape[0] != R or out.device != dev:
             raise ValueError("out must be a matrix [R, >= vocab] of the logits' type and device")
-        a.out, a.out_ld = _at(out), old
     on = _on(dev, stream)
     with on as s:
         if out is None:
-            out = torch.empty((R, V), dtype=logits.dtype, device=dev)
-            a.out, a.out_ld = _at(out), V
+            out, old = torch.empty((R, V), dtype=logits.dtype, device=dev), V
+        a = Adjust(logits.data_ptr(), out.data_ptr(), dtype, V, ld, old, B, R, off, drafts, par, hist, hist_ld, width,
+                   prompt, used, rep, freq, pres, boff, btok, bval, n, mp, mask_ld, masks, midx)
         on.keep(logits, row_offsets, draft_tokens, parents, history, history_len, prompt_len, repetition, frequency,
                 presence, bias_offsets, bias_tokens, bias_values, mask, mask_index, out, error_flag)
-        _check(lib().vsv_adjust_logits(ctypes.byref(a), _at(error_flag), s))
+        _check(lib().vsv_adjust_logits(ctypes.byref(a), err, s))
     return out[:, :V] if out.shape[1] > V else out
 
 
@@ -912,34 +939,28 @@ def plan_pages(block_table, held, length, row_offsets, free_pages, free_count, p
     for rows of no request), held, length and free_count behind the call, and
     error_flag (FLAG_PAGES: the pool ran out, and the requests it could not
     serve are as they were)."""
-    B, R, dev = row_offsets.numel() - 1, int(num_rows), row_offsets.device
-    _vec(row_offsets, B + 1, torch.int32, "row_offsets")
-    _vec(held, B, torch.int32, "held")
-    _vec(length, B, torch.int32, "length")
-    _vec(free_pages, free_pages.numel(), torch.int32, "free_pages")
-    _vec(free_count, 1, torch.int32, "free_count")
-    if (not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or
-            block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-        raise ValueError("block_table must be an int32 CUDA matrix [B, W] with unit column stride")
+    B, R, i32, dev = row_offsets.numel() - 1, int(num_rows), torch.int32, _cuda(row_offsets, "row_offsets")
+    off = _in(row_offsets, B + 1, i32, dev, "row_offsets")
+    had = _in(held, B, i32, dev, "held")
+    lens = _in(length, B, i32, dev, "length")
+    pool = free_pages.numel()
+    free = _in(free_pages, pool, i32, dev, "free_pages")
+    count = _in(free_count, 1, i32, dev, "free_count")
+    table, table_ld = _matrix(block_table, B, 0, dev, "block_table")
     if R < 0:
         raise ValueError("num_rows must not be negative")
-    _same_device(dev, block_table, held, length, free_pages, free_count)
-    W = block_table.shape[1]
     on = _on(dev, stream)
     with on as s:
-        out = dict(slot=torch.empty(R, dtype=torch.int64, device=dev),
-                   position=torch.empty(R, dtype=torch.int32, device=dev),
-                   held=torch.empty(B, dtype=torch.int32, device=dev),
-                   length=torch.empty(B, dtype=torch.int32, device=dev),
-                   free_count=torch.empty(1, dtype=torch.int32, device=dev),
-                   error_flag=_new_flag(dev, s))
+        slot = torch.empty(R, dtype=torch.int64, device=dev)
+        words = torch.empty(R + 2 * B + 1, dtype=i32, device=dev)
+        position, new_held, new_length, new_count = torch.split_with_sizes(words, (R, B, B, 1))
+        flag = _new_flag(dev, s)
+        base = words.data_ptr()
         on.keep(block_table, held, length, row_offsets, free_pages, free_count)
-        _check(lib().vsv_plan_pages(_at(block_table), block_table.stride(0) if B > 1 else max(W, 1), W, _at(held),
-                                    _at(length), _at(row_offsets), B, R, _at(free_pages), free_pages.numel(),
-                                    _at(free_count), int(page_size), _at(out["slot"]), _at(out["position"]),
-                                    _at(out["held"]), _at(out["length"]), _at(out["free_count"]),
-                                    _at(out["error_flag"]), s))
-    return out
+        _check(lib().vsv_plan_pages(table, table_ld, block_table.shape[1], had, lens, off, B, R, free, pool, count,
+                                    int(page_size), slot.data_ptr(), base, base + 4 * R, base + 4 * (R + B),
+                                    base + 4 * (R + 2 * B), flag.data_ptr(), s))
+    return dict(slot=slot, position=position, held=new_held, length=new_length, free_count=new_count, error_flag=flag)
 
 
 def _alloc_outputs(B, K, G, dev, with_drafts):

@@ -32,16 +32,31 @@ namespace {
 typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// All ones if bit k of `bits` is set, else 0.
+__device__ __forceinline__ uint32_t bit_mask(uint32_t bits, int k) {
+  return static_cast<uint32_t>(static_cast<int32_t>(bits << (31 - k)) >> 31);
+}
+
 template <typename E> struct Vec8;
 template <> struct Vec8<uint16_t> {
   u32x4 w;
   __device__ __forceinline__ void load(const uint16_t* p) { w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_2*>(p)); }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<u32x4_2*>(p) = w; }
-  __device__ __forceinline__ float get(int k) const {
-    const uint32_t v = w[k >> 1];
-    return __uint_as_float(k & 1 ? v & 0xFFFF0000u : v << 16);
+  __device__ __forceinline__ void store(uint16_t* p) const { __builtin_nontemporal_store(u32x4_2(w), reinterpret_cast<u32x4_2*>(p)); }
+  __device__ __forceinline__ void get(float* f) const { Elem<uint16_t>::decode(w, f); }
+  __device__ __forceinline__ void set(const float* f) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(f[2 * k]), static_cast<__bf16>(f[2 * k + 1])});
   }
-  __device__ __forceinline__ void put(int k, float f);
+  // -inf wherever `allow` has a 0 bit
+  __device__ __forceinline__ void mask(uint32_t allow) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t keep = (bit_mask(allow, 2 * k) & 0xFFFFu) | (bit_mask(allow, 2 * k + 1) & 0xFFFF0000u);
+      w[k] = (w[k] & keep) | (0xFF80FF80u & ~keep);
+    }
+  }
 };
 template <> struct Vec8<float> {
   u32x4 w[2];
@@ -50,43 +65,54 @@ template <> struct Vec8<float> {
     w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_4*>(p) + 1);
   }
   __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<u32x4_4*>(p)[0] = w[0];
-    reinterpret_cast<u32x4_4*>(p)[1] = w[1];
+    __builtin_nontemporal_store(u32x4_4(w[0]), reinterpret_cast<u32x4_4*>(p));
+    __builtin_nontemporal_store(u32x4_4(w[1]), reinterpret_cast<u32x4_4*>(p) + 1);
   }
-  __device__ __forceinline__ float get(int k) const { return __uint_as_float(w[k >> 2][k & 3]); }
-  __device__ __forceinline__ void put(int k, float f) { w[k >> 2][k & 3] = __float_as_uint(f); }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(w[k >> 2][k & 3]);
+  }
+  __device__ __forceinline__ void set(const float* f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k >> 2][k & 3] = __float_as_uint(f[k]);
+  }
+  __device__ __forceinline__ void mask(uint32_t allow) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t keep = bit_mask(allow, k);
+      w[k >> 2][k & 3] = (w[k >> 2][k & 3] & keep) | (0xFF800000u & ~keep);
+    }
+  }
 };
 
 // Nearest bfloat16, ties to even; a NaN stays one.
-__device__ __forceinline__ uint32_t to_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-__device__ __forceinline__ void Vec8<uint16_t>::put(int k, float f) {
-  const uint32_t h = to_bf16(f);
-  w[k >> 1] = k & 1 ? (w[k >> 1] & 0xFFFFu) | (h << 16) : (w[k >> 1] & 0xFFFF0000u) | h;
-}
+__device__ __forceinline__ uint32_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
 
 __device__ __forceinline__ float widen(float f) { return f; }
 __device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float(static_cast<uint32_t>(h) << 16); }
 __device__ __forceinline__ void narrow(float f, float* p) { *p = f; }
 __device__ __forceinline__ void narrow(float f, uint16_t* p) { *p = static_cast<uint16_t>(to_bf16(f)); }
 
-constexpr int kRows = 8;   // rows of a request a workgroup takes at a time
+// A slice of 2048 tokens: its table leaves eight workgroups a CU. 4096 (four)
+// took 60 instead of 51 us on 408 rows of 50021 fp32 logits; on 640 rows of
+// 152064 bf16 ones 2048, 4096 and 8192 are within 1 us of one another.
+constexpr int kThreads = 256;
+constexpr int kSliceTokens = 2048;
+constexpr int kMostRows = 8;         // rows of a request a workgroup takes at a time
+constexpr int kShortHistory = 4096;  // tokens
 
-template <int SL>
 struct AdjustScratch {
-  uint32_t count[SL];       // 2 * occurrences in output and path, + 1 if in the prompt
-  uint32_t bias[SL];        // the last entry's number + 1, then its value's bits
-  uint32_t touched[SL / 32];
+  uint32_t count[kSliceTokens];       // 2 * occurrences in output and path, + 1 if in the prompt
+  uint32_t bias[kSliceTokens];        // the last entry's number + 1, then its value's bits
+  uint32_t touched[kSliceTokens / 32];
   int draft[VSV_MAX_TREE_ROWS];
   uint64_t path[VSV_MAX_TREE_ROWS];
 };
 
-template <typename E, int NT, int SL, bool kInPlace>
-__global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
-  __shared__ AdjustScratch<SL> s;
+template <typename E, bool kInPlace>
+__global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs a) {
+  __shared__ AdjustScratch s;
+  constexpr int NT = kThreads, SL = kSliceTokens;
   constexpr int kPer = SL / 8 / NT;   // vectors a thread streams of a row
   static_assert(kPer * NT * 8 == SL, "whole vectors per thread");
   const int tid = threadIdx.x;
@@ -103,17 +129,19 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
     return;
   }
   const int n = o1 - o0;
-  // this workgroup's rows of the request: every groups-th block of kRows
-  const int j0 = group * kRows;
+  // this workgroup's rows of the request: every groups-th block of a.rows
+  const int j0 = group * a.rows;
   if (j0 >= n) return;
-  auto row_after = [&](int j) { return (j + 1) % kRows ? j + 1 : j + 1 + (a.groups - 1) * kRows; };
+  int block_end = j0 + a.rows;
 
   float rho = a.repetition ? a.repetition[i] : 1.f;
   float freq = a.frequency ? a.frequency[i] : 0.f;
   float pres = a.presence ? a.presence[i] : 0.f;
-  if (!(rho > 0.f) || !(rho < INFINITY) || !(fabsf(freq) < INFINITY) || !(fabsf(pres) < INFINITY)) {
+  // (the reciprocal has to be a normal number)
+  const bool rho_ok = rho >= 0x1p-126f && rho <= 0x1p126f;
+  if (!rho_ok || !(fabsf(freq) < INFINITY) || !(fabsf(pres) < INFINITY)) {
     bits |= VSV_FLAG_PARAMS;
-    if (!(rho > 0.f) || !(rho < INFINITY)) rho = 1.f;
+    if (!rho_ok) rho = 1.f;
     if (!(fabsf(freq) < INFINITY)) freq = 0.f;
     if (!(fabsf(pres) < INFINITY)) pres = 0.f;
   }
@@ -154,6 +182,13 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
       atomicAdd(&s.count[q], what);
     touch(q);
   };
+  // the draft that row r > 0 of the request carries
+  auto draft_of = [&](int r) {
+    const int dq = o0 + r - i - 1;
+    if (dq >= 0 && dq < a.R - a.B) return a.drafts[dq];
+    bits |= VSV_FLAG_LAYOUT;
+    return -1;
+  };
   if (penal && a.history) {
     int end = a.history_len[i], prompt = a.prompt_len ? a.prompt_len[i] : 0;
     if (end < 0 || end > a.hist_width || prompt < 0 || prompt > end) {
@@ -193,21 +228,13 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
       }
     }
   }
-  // the tree's paths (a chain of any length needs none)
-  if (a.parents && penal) {
-    if (tid < kWave) {
-      const int up = tid < n ? a.parents[o0 + tid] : 0;
-      const int dq = o0 + tid - i - 1;   // the row's own draft
-      int d = -1;
-      if (tid > 0 && tid < n) {
-        if (dq >= 0 && dq < a.R - a.B)
-          d = a.drafts[dq];
-        else
-          bits |= VSV_FLAG_LAYOUT;
-      }
+  // the drafts of the request's first rows, and a tree's paths
+  if (penal && tid < kWave) {
+    const int up = a.parents && tid < n ? a.parents[o0 + tid] : 0;
+    s.draft[tid] = tid > 0 && tid < n ? draft_of(tid) : -1;
+    if (a.parents) {
       bool bad;
       s.path[tid] = tree_paths(tid, n, up, false, bad);
-      s.draft[tid] = d;
       if (bad) bits |= VSV_FLAG_LAYOUT;
     }
   }
@@ -219,19 +246,17 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
     }
   }
 
-  auto fix = [&](float x, int q) {
+  // (the reciprocal costs a second rounding of 2^-24 and saves a division per
+  // touched logit)
+  const float inv_rho = 1.f / rho;
+  auto adjusted = [&](float x, uint32_t c, uint32_t b) {
     if (penal) {
-      const uint32_t c = s.count[q];
-      if (c) {
-        x = x > 0.f ? x / rho : x * rho;
-        if (c > 1u) {
-          x -= freq * static_cast<float>(c >> 1);
-          x -= pres;
-        }
-      }
+      float y = x > 0.f ? x * inv_rho : x * rho;
+      y = y - freq * static_cast<float>(c >> 1);
+      y = c > 1u ? y - pres : y;
+      x = c ? y : x;
     }
-    if (biased) x += __uint_as_float(s.bias[q]);
-    return x;
+    return biased ? x + __uint_as_float(b) : x;
   };
 
   // ---- the rows
@@ -272,19 +297,17 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
         if (tid > 0 && ((was ^ now) & bit)) add(s.draft[tid], now & bit ? 2u : ~1u);
       }
     } else {
-      // rows 1 .. j of the chain carry drafts 0 .. j - 1
-      const int first = from < 0 ? 1 : from + 1;
-      for (int r = first + tid; r <= j; r += NT) {
-        const int dq = o0 + r - i - 1;
-        if (dq >= 0 && dq < a.R - a.B)
-          add(a.drafts[dq], 2u);
-        else
-          bits |= VSV_FLAG_LAYOUT;
-      }
+      // the rows of the chain up to j
+      for (int r = max(from, 0) + 1 + tid; r <= j; r += NT) add(r < VSV_MAX_TREE_ROWS ? s.draft[r] : draft_of(r), 2u);
     }
   };
   load_row(j0);
-  for (int j = j0, from = -1; j < n; from = j, j = row_after(j)) {
+  for (int j = j0, from = -1, next; j < n; from = j, j = next) {
+    next = j + 1;
+    if (next == block_end) {
+      next += (a.groups - 1) * a.rows;
+      block_end = next + a.rows;
+    }
     move_path(from, j);
     lds_barrier();
     const E* row = xs + static_cast<int64_t>(o0 + j) * a.ld;
@@ -297,7 +320,7 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
       cur[k] = buf[k];
       allow[k] = allow_buf[k];
     }
-    if (row_after(j) < n) load_row(row_after(j));
+    if (next < n) load_row(next);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int q = (k * NT + tid) * 8;
@@ -308,20 +331,27 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
           if (allow[k]) cur[k].load(row + q);
         }
         if (hit) {
+          float f[8];
+          cur[k].get(f);
+          const u32x4* c = reinterpret_cast<const u32x4*>(s.count + q);
+          const u32x4* b = reinterpret_cast<const u32x4*>(s.bias + q);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (hit >> e & 1u) cur[k].put(e, fix(cur[k].get(e), q + e));
-        }
-        if (allow[k] != 0xFFu) {
+          for (int h = 0; h < 2; ++h) {
+            const u32x4 ch = penal ? c[h] : u32x4{0, 0, 0, 0}, bh = biased ? b[h] : u32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (!(allow[k] >> e & 1u)) cur[k].put(e, -INFINITY);
+            for (int e = 0; e < 4; ++e) {
+              const float y = adjusted(f[h * 4 + e], ch[e], bh[e]);
+              f[h * 4 + e] = hit >> (h * 4 + e) & 1u ? y : f[h * 4 + e];
+            }
+          }
+          cur[k].set(f);
         }
+        if (allow[k] != 0xFFu) cur[k].mask(allow[k]);
         cur[k].store(out + q);
       } else {
         for (int e = q; e < vn && e < q + 8; ++e) {
           float x = widen(row[e]);
-          if (touched[e >> 3] >> (e & 7) & 1) x = fix(x, e);
+          if (touched[e >> 3] >> (e & 7) & 1) x = adjusted(x, penal ? s.count[e] : 0, biased ? s.bias[e] : 0);
           if (mask && !(mask[e >> 3] >> (e & 7) & 1)) x = -INFINITY;
           narrow(x, out + e);
         }
@@ -332,38 +362,34 @@ __global__ __launch_bounds__(NT) void adjust_kernel(AdjustArgs a) {
   if (bits && a.error_flag) atomicOr(a.error_flag, bits);
 }
 
-template <typename E, int NT, int SL>
+template <typename E>
 hipError_t launch_t(AdjustArgs a, hipStream_t s) {
-  a.slices = (a.V + SL - 1) / SL;
-  // a request's rows in blocks of kRows to as many workgroups as twice the
-  // mean request fills (longer ones go round)
+  a.slices = (a.V + kSliceTokens - 1) / kSliceTokens;
+  // A request's rows go in blocks of a.rows to as many workgroups as twice the
+  // mean request fills (longer ones go round). Blocks are as long as gives
+  // each of the eight workgroups that fit a CU one, or two where histories are short
+  // and a table is soon built: 408 fp32 rows of 50021 logits take 39 us with two
+  // and 42 with one for histories of 64 tokens, 58 and 52 for 16000.
   const int64_t base = static_cast<int64_t>(a.B) * a.slices;
   const int64_t mean = (a.R + a.B - 1) / a.B;
-  a.groups = mean <= kRows ? 1 : static_cast<int32_t>((2 * mean + kRows - 1) / kRows);
+  const int64_t fit = static_cast<int64_t>(a.cus > 0 ? a.cus : 256) * 8 * (a.hist_width > kShortHistory ? 1 : 2);
+  int64_t rows = static_cast<int64_t>(a.R) * a.slices / fit;
+  rows = rows < 1 ? 1 : rows > kMostRows ? kMostRows : rows;
+  a.rows = static_cast<int32_t>(rows);
+  a.groups = mean <= rows ? 1 : static_cast<int32_t>((2 * mean + rows - 1) / rows);
   const int64_t grid = base * a.groups;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (a.x == a.y)
-    adjust_kernel<E, NT, SL, true><<<dim3(static_cast<unsigned>(grid)), dim3(NT), 0, s>>>(a);
+    adjust_kernel<E, true><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(a);
   else
-    adjust_kernel<E, NT, SL, false><<<dim3(static_cast<unsigned>(grid)), dim3(NT), 0, s>>>(a);
+    adjust_kernel<E, false><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
-}
-
-template <typename E>
-hipError_t launch_e(const AdjustArgs& a, hipStream_t s) {
-#ifdef VSV_SL
-  return launch_t<E, VSV_NT, VSV_SL>(a, s);
-#else
-  const int64_t large = static_cast<int64_t>(a.B) * ((a.V + 8191) / 8192);
-  return large >= 2 * static_cast<int64_t>(a.cus > 0 ? a.cus : 256) ? launch_t<E, 512, 8192>(a, s)
-                                                                     : launch_t<E, 256, 2048>(a, s);
-#endif
 }
 
 }  // namespace
 
 hipError_t launch_adjust(const AdjustArgs& a, hipStream_t s) {
-  return a.dtype == VSV_BF16 ? launch_e<uint16_t>(a, s) : launch_e<float>(a, s);
+  return a.dtype == VSV_BF16 ? launch_t<uint16_t>(a, s) : launch_t<float>(a, s);
 }
 
 }  // namespace vsv

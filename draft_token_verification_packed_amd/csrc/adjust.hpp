@@ -36,7 +36,7 @@ struct AdjustArgs {
   int32_t* error_flag;
   int32_t cus;
   // set at launch
-  int32_t slices, groups;       // parts of the vocabulary; row groups of a request
+  int32_t slices, rows, groups;   // parts of the vocabulary; rows of a block; blocks side by side
 };
 
 hipError_t launch_adjust(const AdjustArgs& a, hipStream_t s);

@@ -154,6 +154,10 @@ __device__ __forceinline__ void tree_tail(const VerifyArgs& a, uint32_t tag, Tre
     lds_barrier();   // the next window reuses the words and links
   }
   if (tid == 0) a.out_offsets[a.B] = carry;
+  for (int p = carry + tid; p < a.R; p += NT) {
+    a.out_tokens[p] = -1;
+    if (a.out_rows) a.out_rows[p] = -1;
+  }
   if (stalled) bits |= VSV_FLAG_STALLED;
   if (bits) set_flag(a, bits);
   end_call(a, tag);

@@ -187,6 +187,7 @@ vsv_status vsv_verify_greedy_relaxed(const vsv_batch* batch, const vsv_relax* re
  *                       keys and values belong into the cache, at the
  *                       positions that vsv_plan_pages gives for row_offsets =
  *                       out_offsets
+ * out_tokens and out_rows are -1 behind the last path.
  * A request may have at most VSV_MAX_TREE_ROWS rows. VSV_FLAG_LAYOUT: layout
  * as above, more rows, or a parent that is no earlier row of the request (the
  * row is then on no path). Workspace: vsv_workspace_bytes(B, R, 0).
@@ -529,7 +530,7 @@ typedef struct {
   int32_t history_width;        /* entries of a row that may be read                    */
   const int32_t* prompt_len;    /* [B] tokens of the prompt, or NULL: 0                 */
   const int32_t* history_len;   /* [B] tokens of both (required with history)           */
-  const float* repetition;      /* [B] positive and finite, or NULL: 1                  */
+  const float* repetition;      /* [B] 2^-126 .. 2^126, or NULL: 1                      */
   const float* frequency;       /* [B] finite, or NULL: 0                               */
   const float* presence;        /* [B] finite, or NULL: 0                               */
   const int32_t* bias_offsets;  /* [B + 1], or NULL: no biases                          */

@@ -143,8 +143,8 @@ def test_rows_match_the_definition(vsv, dtype, kind, counts, V):
 
 
 @pytest.mark.parametrize("dtype", [oracle.F32, oracle.BF16])
-def test_large_batches_take_wide_slices(vsv, dtype):
-    # enough requests for the 8192-token slices
+def test_large_batches(vsv, dtype):
+    # more rows than workgroups fit the chip
     c = _case(3, [2] * 300, 16500, dtype, "wide", 1, H=90, tokens=900)
     _check(_call(vsv, c), c)
 
