@@ -533,97 +533,30 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
     }
 
     // One tile of this wave's slice, for its first NQ blocks of 16 queries.
+    // One tile of this wave's slice, for its first NQ blocks of 16 queries.
     // `between` runs when the keys have been read, before the values are.
+    // Where waves share slices, and so meet in step at every tile, what a
+    // step reads from LDS is read a phase ahead: its values before the
+    // softmax, the next step's keys before the product with the values.
+    constexpr bool kAhead = WQ > 1 && sizeof(E) == 2 && D <= 128;
     auto compute = [&](auto live, int t, auto between) {
       constexpr int NQ = decltype(live)::value;
       const int x0 = t * S::kTile + wk * S::kTokens;
       const char* kl = reinterpret_cast<const char*>(s.tile[t % S::kStages][wk].k);
       const char* vl = reinterpret_cast<const char*>(s.tile[t % S::kStages][wk].v);
-#pragma unroll
-      for (int sub = 0; sub < S::kSub; ++sub) {
-
-      // S^T of two halves of 16 tokens
-      f32x4 sc[2][NQ];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-        for (int qt = 0; qt < NQ; ++qt) sc[hf][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int row = sub * kSlice + hf * 16 + col;
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-          typename F::T kf;
-          if constexpr (sizeof(E) == 2) {
-            kf = *reinterpret_cast<const bf16x8*>(kl + (row * C + ((kc * 4 + grp) ^ swizzle_k<C>(row))) * 16);
-          } else {
-            const int c0 = kc * 8 + grp * 2, z = swizzle_k<C>(row);
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(kl + (row * C + (c0 ^ z)) * 16);
-            const f32x4 hi = *reinterpret_cast<const f32x4*>(kl + (row * C + ((c0 + 1) ^ z)) * 16);
-            kf = f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          }
-#pragma unroll
-          for (int qt = 0; qt < NQ; ++qt) sc[hf][qt] = F::mma(kf, qf[qt][kc], sc[hf][qt]);
+      auto key = [&](int sub, int hf, int kc) -> typename F::T {
+        const int row = sub * kSlice + hf * 16 + col, z = swizzle_k<C>(row);
+        if constexpr (sizeof(E) == 2) {
+          return *reinterpret_cast<const bf16x8*>(kl + (row * C + ((kc * 4 + grp) ^ z)) * 16);
+        } else {
+          const int c0 = kc * 8 + grp * 2;
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(kl + (row * C + (c0 ^ z)) * 16);
+          const f32x4 hi = *reinterpret_cast<const f32x4*>(kl + (row * C + ((c0 + 1) ^ z)) * 16);
+          return f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         }
-      }
-      // tokens from the tree on: only the row's path is seen
-      const int xs = x0 + sub * kSlice;
-      if (xs + kSlice > len) {
-#pragma unroll
-        for (int qt = 0; qt < NQ; ++qt) {
-          // bit k: the lane's query sees token k of the step
-          const int first = xs - len;   // of the rows' own
-          const uint32_t seen = first >= 0 ? (first < 64 ? static_cast<uint32_t>(path[qt] >> first) : 0u)
-                                           : (static_cast<uint32_t>(path[qt]) << -first) | ((1u << -first) - 1u);
-          const uint32_t mine = seen >> (grp * 4);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[hf][qt][e] = mine & (1u << (hf * 16 + e)) ? sc[hf][qt][e] : -INFINITY;
-        }
-      }
-      // The reference moves only where a score passes it by more than kSlack
-      // in log2: weights stay below 2^kSlack, and most tiles skip the
-      // reduction across lanes and the rescaling.
-      constexpr float kSlack = 8.f;
-      typename F::T pf[NQ];
-      bool move = false;
-      float top[NQ];
-#pragma unroll
-      for (int qt = 0; qt < NQ; ++qt) {
-        float b = sc[0][qt][0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) b = fmaxf(b, sc[e >> 2][qt][e & 3]);
-        top[qt] = b;
-        move |= b * a.scale > mref[qt] * a.scale + kSlack;   // false while both are -inf
-      }
-      if (__builtin_amdgcn_ballot_w64(move)) {
-#pragma unroll
-        for (int qt = 0; qt < NQ; ++qt) {
-          float b = fmaxf(top[qt], mref[qt]);
-          b = fmaxf(b, __shfl_xor(b, 16));
-          b = fmaxf(b, __shfl_xor(b, 32));
-          const float f = b == mref[qt] ? 1.f : fast_exp2((mref[qt] - b) * a.scale);
-          mref[qt] = b;
-          mc[qt] = b == -INFINITY ? 0.f : b * a.scale;
-          l[qt] *= f;
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt) acc[dt][qt] *= f;
-        }
-      }
-#pragma unroll
-      for (int qt = 0; qt < NQ; ++qt) {
-        float p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = fast_exp2(fmaf(sc[e >> 2][qt][e & 3], a.scale, -mc[qt]));
-          l[qt] += p[e];
-        }
-        pf[qt] = F::pack(p);
-      }
-      between();
-      // O^T += V^T P^T
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        typename F::T vf;
+      };
+      auto value = [&](int sub, int dt) -> typename F::T {
+        typename F::T v;
         if constexpr (sizeof(E) == 2) {
           s16x4 half[2];
 #pragma unroll
@@ -634,19 +567,119 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
             half[hf] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4*)(const_cast<char*>(p)));
           }
-          vf = __builtin_bit_cast(bf16x8, s16x8{half[0][0], half[0][1], half[0][2], half[0][3], half[1][0], half[1][1],
-                                                half[1][2], half[1][3]});
+          v = __builtin_bit_cast(bf16x8, s16x8{half[0][0], half[0][1], half[0][2], half[0][3], half[1][0], half[1][1],
+                                               half[1][2], half[1][3]});
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int row = sub * kSlice + (e >> 2) * 16 + grp * 4 + (e & 3);
             const int chunk = dt * 4 + (col >> 2);
-            vf[e] = *reinterpret_cast<const float*>(vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16 + (col & 3) * 4);
+            v[e] = *reinterpret_cast<const float*>(vl + (row * C + (chunk ^ swizzle_v<E, C>(row))) * 16 + (col & 3) * 4);
+          }
+        }
+        return v;
+      };
+      typename F::T kf[kAhead ? 2 : 1][kAhead ? KC : 1], vf[kAhead ? DT : 1];
+      auto keys_ahead = [&](int sub) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int kc = 0; kc < KC; ++kc) kf[hf][kc] = key(sub, hf, kc);
+      };
+      if constexpr (kAhead) keys_ahead(0);
+#pragma unroll
+      for (int sub = 0; sub < S::kSub; ++sub) {
+        // S^T of two halves of 16 tokens
+        f32x4 sc[2][NQ];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int qt = 0; qt < NQ; ++qt) sc[hf][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kc = 0; kc < KC; ++kc) {
+            typename F::T k;
+            if constexpr (kAhead)
+              k = kf[hf][kc];
+            else
+              k = key(sub, hf, kc);
+#pragma unroll
+            for (int qt = 0; qt < NQ; ++qt) sc[hf][qt] = F::mma(k, qf[qt][kc], sc[hf][qt]);
+          }
+        }
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) vf[dt] = value(sub, dt);
+        }
+        // tokens from the tree on: only the row's path is seen
+        const int xs = x0 + sub * kSlice;
+        if (xs + kSlice > len) {
+#pragma unroll
+          for (int qt = 0; qt < NQ; ++qt) {
+            // bit k: the lane's query sees token k of the step
+            const int first = xs - len;   // of the rows' own
+            const uint32_t seen = first >= 0 ? (first < 64 ? static_cast<uint32_t>(path[qt] >> first) : 0u)
+                                             : (static_cast<uint32_t>(path[qt]) << -first) | ((1u << -first) - 1u);
+            const uint32_t mine = seen >> (grp * 4);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[hf][qt][e] = mine & (1u << (hf * 16 + e)) ? sc[hf][qt][e] : -INFINITY;
+          }
+        }
+        // The reference moves only where a score passes it by more than kSlack
+        // in log2: weights stay below 2^kSlack, and most tiles skip the
+        // reduction across lanes and the rescaling.
+        constexpr float kSlack = 8.f;
+        typename F::T pf[NQ];
+        bool move = false;
+        float top[NQ];
+#pragma unroll
+        for (int qt = 0; qt < NQ; ++qt) {
+          float b = sc[0][qt][0];
+#pragma unroll
+          for (int e = 1; e < 8; ++e) b = fmaxf(b, sc[e >> 2][qt][e & 3]);
+          top[qt] = b;
+          move |= b * a.scale > mref[qt] * a.scale + kSlack;   // false while both are -inf
+        }
+        if (__builtin_amdgcn_ballot_w64(move)) {
+#pragma unroll
+          for (int qt = 0; qt < NQ; ++qt) {
+            float b = fmaxf(top[qt], mref[qt]);
+            b = fmaxf(b, __shfl_xor(b, 16));
+            b = fmaxf(b, __shfl_xor(b, 32));
+            const float f = b == mref[qt] ? 1.f : fast_exp2((mref[qt] - b) * a.scale);
+            mref[qt] = b;
+            mc[qt] = b == -INFINITY ? 0.f : b * a.scale;
+            l[qt] *= f;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) acc[dt][qt] *= f;
           }
         }
 #pragma unroll
-        for (int qt = 0; qt < NQ; ++qt) acc[dt][qt] = F::mma(vf, pf[qt], acc[dt][qt]);
-      }
+        for (int qt = 0; qt < NQ; ++qt) {
+          float p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            p[e] = fast_exp2(fmaf(sc[e >> 2][qt][e & 3], a.scale, -mc[qt]));
+            l[qt] += p[e];
+          }
+          pf[qt] = F::pack(p);
+        }
+        between();
+        if constexpr (kAhead) {
+          if (sub + 1 < S::kSub) keys_ahead(sub + 1);
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          typename F::T v;
+          if constexpr (kAhead)
+            v = vf[dt];
+          else
+            v = value(sub, dt);
+#pragma unroll
+          for (int qt = 0; qt < NQ; ++qt) acc[dt][qt] = F::mma(v, pf[qt], acc[dt][qt]);
+        }
       }
     };
     const int blocks = (M + 15) / 16;   // of 16 queries, dealt to the waves in turn
