@@ -96,7 +96,8 @@ template <typename E, int D, int QT, int WQ, int WK>
 struct Shape {
   static constexpr int kThreads = WQ * WK * kWave;
   static constexpr int kMT = 16 * QT * WQ;           // queries of an item
-  static constexpr int kSub = WK == 1 ? 2 : 1;       // steps of a slice: fewer barriers where waves share it
+  // steps of a slice: fewer barriers where waves share it
+  static constexpr int kSub = WQ == 8 && D * static_cast<int>(sizeof(E)) <= 256 ? 4 : WK == 1 ? 2 : 1;
   static constexpr int kTokens = kSlice * kSub;      // tokens of a slice
   static constexpr int kTile = WK * kTokens;         // tokens of a tile
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(E));
@@ -532,7 +533,6 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
       for (int dt = 0; dt < DT; ++dt) acc[dt][qt] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // One tile of this wave's slice, for its first NQ blocks of 16 queries.
     // One tile of this wave's slice, for its first NQ blocks of 16 queries.
     // `between` runs when the keys have been read, before the values are.
     // Where waves share slices, and so meet in step at every tile, what a
