@@ -797,11 +797,12 @@ def verify_greedy_tree(logits, row_offsets, row_owner, draft_tokens, parents, vo
 
 
 def _heads(t, shape, dtype, device, name):
-    """Strides of a tensor of `shape` with unit last stride."""
+    """Strides of a tensor of `shape` with unit last stride (0 for a
+    dimension of one, whose stride torch leaves open)."""
     st = t.stride()
     if t.dtype is not dtype or t.device != device or t.shape != shape or (st[-1] != 1 and t.numel()):
         raise ValueError("%s must be a %s tensor %s on %s with unit last stride" % (name, dtype, list(shape), device))
-    return st
+    return st if 1 not in shape else [s if n > 1 else 0 for s, n in zip(st, shape)]
 
 
 def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, parents=None, scale=None, out=None,
@@ -841,7 +842,7 @@ def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, 
     with on as s:
         if out is None:
             out = torch.empty((R, H, D), dtype=q.dtype, device=dev)
-            os_ = (H * D, D, 1)
+            os_ = (H * D if R > 1 else 0, D if H > 1 else 0)
         lse = torch.empty((R, H), dtype=torch.float32, device=dev) if return_lse else None
         a = Attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                       _at(lse), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], cs[0], cs[1], cs[2],

@@ -420,6 +420,11 @@ vsv_status vsv_tree_attention(const vsv_attention* d, int32_t* error_flag, void*
                                 {d->cache_token, d->page_size}, {d->cache_head, d->num_kv_heads}};
   for (const auto& s : strides)
     if (s[0] < 0 || s[0] % unit || s[0] > (INT64_MAX / 16) / s[1]) return VSV_EINVAL;
+  // no two results in one place
+  const int64_t rows_of_head = (d->num_rows - 1) * d->out_row + d->head_dim;
+  const int64_t heads_of_row = (d->num_heads - 1) * d->out_head + d->head_dim;
+  if ((d->num_heads > 1 && d->out_head < d->head_dim) || (d->num_rows > 1 && d->out_row < d->head_dim)) return VSV_EINVAL;
+  if (d->num_heads > 1 && d->num_rows > 1 && d->out_row < heads_of_row && d->out_head < rows_of_head) return VSV_EINVAL;
   if (d->table_ld < d->table_width || d->table_ld > (INT64_MAX / 4) / d->num_requests) return VSV_EINVAL;
   if (!(d->scale > 0.f) || !(d->scale < INFINITY)) return VSV_EINVAL;
   a.scale = static_cast<float>(1.44269504088896340736 * static_cast<double>(d->scale));

@@ -459,7 +459,7 @@ typedef struct {
                               /* (natural, scaled), or NULL                             */
   /* strides in elements (the last dimension's is 1): of rows and heads, and   */
   /* of the caches' pages, tokens and heads; every pointer and every stride in */
-  /* bytes is a multiple of 16                                                 */
+  /* bytes is a multiple of 16, and no two rows or heads of out overlap        */
   int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
   int64_t cache_page, cache_token, cache_head;
   int32_t dtype;              /* vsv_dtype of every matrix                              */

@@ -230,3 +230,20 @@ def test_device_conditions(vsv):
     assert flag(history_len=i32(3, 41)) == vsv.FLAG_LAYOUT
     assert flag(history=np.full((2, 40), 60, dtype=np.int32), history_len=i32(3, 4), prompt_len=i32(1, 1)) == vsv.FLAG_TOKEN
     assert flag(mask_index=i32(0, 1, 5, 0, 0)) == vsv.FLAG_LAYOUT
+
+
+def test_rows_beyond_32_bits(vsv):
+    """The last of rows whose elements lie past 2^31 (2^32 bytes), in place."""
+    import torch
+    V, R = 262144, 8300
+    x = torch.zeros((R, V), dtype=torch.bfloat16, device="cuda")
+    x[-1] = 2.0
+    off = to_dev(np.array([0, R], dtype=np.int32))
+    drafts = torch.zeros(R - 1, dtype=torch.int32, device="cuda")
+    drafts[-1] = V - 1
+    y = vsv.adjust_logits(x, off, drafts, presence=torch.ones(1, device="cuda"), out=x)
+    assert y.data_ptr() == x.data_ptr()
+    want = torch.full((V,), 2.0, dtype=torch.bfloat16, device="cuda")
+    want[0] = want[-1] = 1.0
+    assert torch.equal(x[-1], want)
+    assert torch.equal(x[0], torch.zeros_like(want))

@@ -229,3 +229,33 @@ def test_device_conditions(vsv):
         assert bits == vsv.FLAG_LAYOUT
         assert torch.all(out[4:] == 9.0) and not torch.any(out[:4] == 9.0)
     assert run(par=i32(-1, 0, 0, 0, -1, 0, 2, 0, 0, 0))[0] == vsv.FLAG_LAYOUT
+
+
+def test_dimensions_of_one(vsv):
+    import torch
+    c = _case(49, [1], [30], 1, 1, 64, 16, BF16)
+    # strides of dimensions of one element may be anything
+    odd = lambda t: torch.as_strided(t, t.shape, (3, 5, 1))
+    q, k, v = [odd(to_dev(c[n])) for n in ("q", "k", "v")]
+    _check(*_call(vsv, c, q=q, k=k, v=v), c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_caches_beyond_32_bits(vsv, dtype):
+    """Pages whose elements lie past 2^32: the cache is allocated whole and
+    filled at the pages in use alone."""
+    import torch
+    page, KV, D, pages = 64, 4, 128, 2 ** 32 // (64 * 4 * 128) + 40
+    c = _case(50, [3, 5], [100, 777], 8, KV, D, page, dtype)
+    used = [(i, j) for i, n in enumerate(c["length"]) for j in range(-(-int(n) // page))]
+    kc, vc = [torch.empty((pages, page, KV, D), dtype=torch.bfloat16 if dtype == BF16 else torch.float32, device="cuda")
+              for _ in range(2)]
+    table = np.full_like(c["table"], -7)
+    small = [to_dev(c[n]) for n in ("kc", "vc")]
+    for m, (i, j) in enumerate(used):
+        table[i, j] = pages - 1 - 2 * m if m % 3 else m
+        for big, s in zip((kc, vc), small):
+            big[int(table[i, j])] = s[int(c["table"][i, j])]
+    print("cache of %d elements dtype=%d" % (kc.numel(), dtype), flush=True)
+    _check(*_call(vsv, c, kc=kc, vc=vc, table=to_dev(table)), c)
+    del kc, vc

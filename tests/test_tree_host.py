@@ -118,9 +118,16 @@ def _attention(L, ws=0x100000, wsn=1 << 30, **kw):
     dict(table_ld=1 << 62), dict(table_width=0), dict(num_pages=0), dict(page_size=0), dict(page_size=24),
     dict(table_width=1 << 28, table_ld=1 << 28), dict(table_width=1 << 26, table_ld=1 << 26, num_heads=8192,
                                                        num_kv_heads=8192), dict(scale=0.0), dict(scale=-1.0),
-    dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38)])
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38),
+    dict(out_head=64), dict(out_row=64), dict(out_row=0), dict(out_row=512), dict(out_row=128, out_head=2048)])
 def test_attention_refusals(L, bad):
     assert _attention(L, **bad) == 1
+
+
+def test_attention_heads_may_come_first(L):
+    # (refused for its scratch alone)
+    assert _attention(L, ws=0, out_row=128, out_head=20 * 128) == 3
+    assert _attention(L, ws=0, num_heads=1, num_kv_heads=1, out_row=128, out_head=0) == 3
 
 
 def test_attention_scratch_and_noops(L):
