@@ -143,7 +143,8 @@ bool prepare_attention(const vsv_attention* d, vsv::AttentionArgs* a) {
   if (!dtype_ok(d->dtype)) return false;
   if (d->head_dim != 64 && d->head_dim != 128 && !(d->head_dim == 256 && d->dtype == VSV_BF16)) return false;
   if (d->num_kv_heads < 1 || d->num_heads < d->num_kv_heads || d->num_heads % d->num_kv_heads) return false;
-  if (d->num_heads > 65536 || d->num_requests < 1 || d->num_requests > VSV_MAX_TREE_REQUESTS || d->num_rows < 1) return false;
+  if (d->num_heads > 65536 || static_cast<int64_t>(d->num_rows) * d->num_heads > INT32_MAX) return false;
+  if (d->num_requests < 1 || d->num_requests > VSV_MAX_TREE_REQUESTS || d->num_rows < 1) return false;
   if (d->table_width < 1 || d->num_pages < 1 || d->page_size < 1 || (d->page_size & (d->page_size - 1))) return false;
   *a = vsv::AttentionArgs{};
   a->B = d->num_requests;

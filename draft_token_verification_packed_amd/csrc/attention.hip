@@ -30,6 +30,15 @@
 // pieces.) WQ waves share a slice and split the queries; the WK slices of a tile go
 // to different waves, joined through LDS at the end of an item. With few
 // queries (WQ = 1) waves share nothing and meet no barrier in the loop.
+//
+// Few queries are bound by HBM, many by the matrix and vector units in turn
+// (waves that share a slice meet at every tile, so products and softmax
+// overlap in part only). On one MI355X, key heads of 128 columns, bfloat16:
+//   128 requests x 5 rows, 200-1019 tokens, 40 / 8 heads   98 us  3.4 TB/s
+//     (the loads alone 69; joining and storing 1500 items about 25)
+//   2 requests x 3-8 rows, 49-65 thousand tokens, 64 / 8  108 us  4.3 TB/s
+//   16 trees of 20-50 rows, 1-8 thousand tokens, 40 / 8   134 us  390 TFLOP/s
+//     (the loads alone 63)
 #include <type_traits>
 #include <utility>
 
@@ -64,8 +73,10 @@ template <> struct Frag<uint16_t> {
   }
   __device__ static __forceinline__ T zero() { return T{}; }
   __device__ static __forceinline__ T load(const uint16_t* p) { return *reinterpret_cast<const T*>(p); }
-  // P is rounded to bfloat16 for the product with V (half a step, 2^-9 of
-  // each weight); the weights' sum is taken before the rounding
+  // P is rounded to bfloat16 for the product with V, as the matrix unit takes
+  // both factors in one type: each weight is off by half a step, 2^-8 of it at
+  // most, at random, about what the result's own rounding costs. The weights'
+  // sum is taken before the rounding.
   __device__ static __forceinline__ T pack(const float* p) {
     T r;
 #pragma unroll
@@ -96,7 +107,8 @@ template <typename E, int D, int QT, int WQ, int WK>
 struct Shape {
   static constexpr int kThreads = WQ * WK * kWave;
   static constexpr int kMT = 16 * QT * WQ;           // queries of an item
-  // steps of a slice: fewer barriers where waves share it
+  // Steps of a slice: fewer barriers where waves share it (256 queries: four
+  // took 135 us on 16 trees, two 142, one 157).
   static constexpr int kSub = WQ == 8 && D * static_cast<int>(sizeof(E)) <= 256 ? 4 : WK == 1 ? 2 : 1;
   static constexpr int kTokens = kSlice * kSub;      // tokens of a slice
   static constexpr int kTile = WK * kTokens;         // tokens of a tile
@@ -291,7 +303,8 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 template <typename E, int D, int QT, int WQ, int WK>
-__global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, QT, WQ, WK>::kWaves)) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, QT, WQ, WK>::kWaves))
+void attention_kernel(AttentionArgs a) {
   using S = Shape<E, D, QT, WQ, WK>;
   using F = Frag<E>;
   constexpr int kThreads = S::kThreads;
@@ -536,8 +549,9 @@ __global__ __launch_bounds__((Shape<E, D, QT, WQ, WK>::kThreads), (Shape<E, D, Q
     // One tile of this wave's slice, for its first NQ blocks of 16 queries.
     // `between` runs when the keys have been read, before the values are.
     // Where waves share slices, and so meet in step at every tile, what a
-    // step reads from LDS is read a phase ahead: its values before the
-    // softmax, the next step's keys before the product with the values.
+    // step reads from LDS is read a phase ahead (its values before the
+    // softmax, the next step's keys before the product with the values): 135
+    // instead of 139 us on 16 trees.
     constexpr bool kAhead = WQ > 1 && sizeof(E) == 2 && D <= 128;
     auto compute = [&](auto live, int t, auto between) {
       constexpr int NQ = decltype(live)::value;
@@ -942,7 +956,10 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 // ---- launch
 
 // Blocks of queries: the smallest one that holds an average request's
-// queries of a key head, so that its keys are read once.
+// queries of a key head, so that its keys are read once. (16 trees of 100 to
+// 250 queries: 135 us with blocks of 256, 141 with 128, 181 with 64. Four waves
+// of 64 queries each instead of eight of 32 took 200: their sums leave the
+// vector registers.)
 struct Plan {
   int mt, tile;
 };

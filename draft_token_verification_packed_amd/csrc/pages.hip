@@ -15,8 +15,9 @@
 // own), so every workgroup works the sums out for itself, no two need to
 // meet, and a call repeated on the same inputs writes the same results.
 //
-// The call is bound by latency: three loads a request, a block scan, a load
-// and a store a row. One launch of a workgroup per kRowsPerGroup rows.
+// The call is bound by latency: four loads a request, a block scan, then a
+// search, a load and a store a row, one row a thread: 6.6 us for 128 requests
+// and 384 rows, 8.3 us for 512 and 96,000.
 #include "device.hpp"
 #include "pages.hpp"
 #include "vspec_verify.h"

@@ -491,8 +491,9 @@ typedef struct {
  * no earlier row (the row then sees the context and itself alone);
  * VSV_FLAG_PAGES: a page outside 0 .. num_pages - 1 (page 0 is read for it).
  * Errors: VSV_EINVAL (NULL pointers, sizes, strides, alignment, dtype, scale;
- * table_width * page_size so large that a request's work passes 2^31 tiles of
- * 32 tokens), VSV_EWORKSPACE, VSV_EHIP. */
+ * num_rows * num_heads beyond 2^31 - 1; table_width * page_size beyond it, or
+ * so large that a request's work could pass 2^31 tiles), VSV_EWORKSPACE,
+ * VSV_EHIP. */
 size_t vsv_tree_attention_workspace_bytes(const vsv_attention* a);
 vsv_status vsv_tree_attention(const vsv_attention* a, int32_t* error_flag, void* workspace, size_t workspace_bytes,
                               hipStream_t stream);

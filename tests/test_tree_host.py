@@ -114,7 +114,7 @@ def _attention(L, ws=0x100000, wsn=1 << 30, **kw):
                                                    "out_head", "cache_page", "cache_token", "cache_head")] +
                          [dict([(k, -8)]) for k in ("q_row", "cache_page")] + [dict([(k, 1 << 62)]) for k in ("k_row", "cache_page")] + [
     dict(dtype=2), dict(head_dim=96), dict(dtype=0, head_dim=256), dict(num_heads=9), dict(num_kv_heads=0),
-    dict(num_heads=0), dict(num_heads=131072), dict(num_requests=-1), dict(num_requests=65537), dict(num_rows=-1), dict(table_ld=15),
+    dict(num_heads=0), dict(num_heads=131072), dict(num_rows=1 << 28, num_requests=65536), dict(num_requests=-1), dict(num_requests=65537), dict(num_rows=-1), dict(table_ld=15),
     dict(table_ld=1 << 62), dict(table_width=0), dict(num_pages=0), dict(page_size=0), dict(page_size=24),
     dict(table_width=1 << 28, table_ld=1 << 28), dict(table_width=1 << 26, table_ld=1 << 26, num_heads=8192,
                                                        num_kv_heads=8192), dict(scale=0.0), dict(scale=-1.0),
