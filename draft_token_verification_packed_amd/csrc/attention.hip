@@ -35,7 +35,7 @@
 // (waves that share a slice meet at every tile, so products and softmax
 // overlap in part only). On one MI355X, key heads of 128 columns, bfloat16:
 //   128 requests x 5 rows, 200-1019 tokens, 40 / 8 heads   98 us  3.4 TB/s
-//     (the loads alone 69; joining and storing 1500 items about 25)
+//     (the loads alone 69; joining and storing 1024 items about 25)
 //   2 requests x 3-8 rows, 49-65 thousand tokens, 64 / 8  108 us  4.3 TB/s
 //   16 trees of 20-50 rows, 1-8 thousand tokens, 40 / 8   134 us  390 TFLOP/s
 //     (the loads alone 63)
