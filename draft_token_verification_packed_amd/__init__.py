@@ -873,7 +873,9 @@ def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None,
     v // 32 is set, and `mask_index` [R] names each row's (negative: none;
     None: row r has mask r). `out` may be a matrix like the logits or the logits
     themselves, of which only the touched elements then move; rows of no
-    request are left as they are in it."""
+    request are left as they are in it. Rows get no gradient."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise NotImplementedError("adjust_logits has no backward pass")
     dtype, V, ld = _logits(logits, vocab)
     R, dev, i32, f32 = logits.shape[0], logits.device, torch.int32, torch.float32
     B = row_offsets.numel() - 1

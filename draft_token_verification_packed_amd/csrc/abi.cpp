@@ -527,7 +527,8 @@ vsv_status vsv_plan_pages(int32_t* block_table, int64_t table_ld, int32_t table_
   if (B > 0) {
     if (!block_table || !held || !length || !new_held || !new_length) return VSV_EINVAL;
     if (table_width < 1 || table_ld < table_width || table_ld > (INT64_MAX / 4) / B) return VSV_EINVAL;
-    if (static_cast<int64_t>(B) * table_width > INT32_MAX) return VSV_EINVAL;
+    // every sum of pages fits 32 bits
+    if (static_cast<int64_t>(B) * table_width + pool_size > INT32_MAX) return VSV_EINVAL;
     if (new_held == held || new_length == length) return VSV_EINVAL;
   }
   if (new_free_count == free_count || !aligned(slot, 8)) return VSV_EINVAL;

@@ -78,8 +78,8 @@ __global__ __launch_bounds__(NT) void pages_kernel(PagesArgs a) {
     bits |= VSV_FLAG_LAYOUT;
     count = max(0, min(count, a.pool_size));
   }
-  // the sums: pages cannot pass 2^31 as a request holds at most `width` and
-  // B * width is bounded by the host
+  // the sums: with the stack they cannot pass 2^31, as a request holds at most
+  // `width` and the host bounds B * width + pool_size
   int takes = 0, gives = 0;
   for (int base = 0; base < B; base += NT) {
     const int i = base + t;

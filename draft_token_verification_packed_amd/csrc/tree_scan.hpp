@@ -120,8 +120,7 @@ __device__ __forceinline__ void tree_tail(const VerifyArgs& a, uint32_t tag, Tre
     }
     lds_barrier();
 
-    // the walks; a request that is not sound emits one token, its first
-    // row's if it has one
+    // the walks; a request that is not sound emits the token 0 alone
     int acc = 0, last = 0;
     if (inside) {
       last = r0 - w0;

@@ -547,7 +547,8 @@ typedef struct {
 } vsv_adjust;
 
 /* VSV_FLAG_TOKEN: a token of a history, path or bias outside the vocabulary
- * (it counts nowhere); VSV_FLAG_PARAMS: a penalty or bias outside its range
+ * (it counts nowhere; histories and paths are read for requests with a
+ * penalty in force, biases and masks always); VSV_FLAG_PARAMS: a penalty or bias outside its range
  * (counts as off); VSV_FLAG_LAYOUT: offsets, lengths, parents or mask rows
  * outside theirs (a request with bad offsets is left as it is). Bits of
  * requests without any row are not looked at.
@@ -581,7 +582,8 @@ vsv_status vsv_adjust_logits(const vsv_adjust* a, int32_t* error_flag, hipStream
  * held or needed count beyond table_width (the request is left as it is), a
  * count beyond pool_size, or a negative page.
  * Errors: VSV_EINVAL (B outside 0 .. 8192, num_rows < 0, page_size < 1, table_width or
- * pool_size < 1, B * table_width beyond 2^31 - 1, table_ld < table_width, NULL pointers),
+ * pool_size < 1, B * table_width + pool_size beyond 2^31 - 1, table_ld <
+ * table_width, NULL pointers),
  * VSV_EHIP. B = 0 writes slots, positions and the count alone. */
 vsv_status vsv_plan_pages(int32_t* block_table, int64_t table_ld, int32_t table_width, const int32_t* held,
                           const int32_t* length, const int32_t* row_offsets, int32_t num_requests, int32_t num_rows,

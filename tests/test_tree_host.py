@@ -81,7 +81,7 @@ def _pages(L, **kw):
 @pytest.mark.parametrize("bad", [dict([(k, None)]) for k in ("table", "held", "length", "offsets", "free", "count", "slot",
                                                             "new_held", "new_length", "new_count")] + [
     dict(B=-1), dict(B=8193), dict(R=-1), dict(page=0), dict(pool=0), dict(width=0), dict(ld=7), dict(ld=1 << 62),
-    dict(B=8000, width=300000, ld=300000), dict(new_held=0x2000), dict(new_length=0x3000), dict(new_count=0x6000),
+    dict(B=8000, width=300000, ld=300000), dict(B=8000, width=250000, ld=250000, pool=1 << 30), dict(new_held=0x2000), dict(new_length=0x3000), dict(new_count=0x6000),
     dict(slot=0x7004)])
 def test_pages_refusals(L, bad):
     assert _pages(L, **bad) == 1
@@ -94,6 +94,8 @@ def test_binding_refusals():
         vsv.verify_greedy_tree(cpu, i(2), i(4), i(3), i(4))
     with pytest.raises(ValueError):
         vsv.adjust_logits(cpu, i(2), i(3))
+    with pytest.raises(NotImplementedError):
+        vsv.adjust_logits(cpu.requires_grad_(), i(2), i(3))
     with pytest.raises(ValueError):
         vsv.plan_pages(i(4).view(1, 4), i(1), i(1), i(2), i(9), i(1), 16, 4)
 
