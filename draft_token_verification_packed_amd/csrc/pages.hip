@@ -69,6 +69,7 @@ template <int NT, int CAP>
 __global__ __launch_bounds__(NT) void pages_kernel(PagesArgs a) {
   __shared__ PagesScratch<CAP> s;
   const int t = threadIdx.x, B = a.B;
+  // (indexes that a step may carry past 2^31 have 64 bits)
   const int step = static_cast<int>(gridDim.x) * NT;
   const int first = static_cast<int>(blockIdx.x) * NT + t;
   int bits = 0;
@@ -119,7 +120,8 @@ __global__ __launch_bounds__(NT) void pages_kernel(PagesArgs a) {
   };
 
   // rows: the page is an old one of the request or one it takes
-  for (int r = first; r < a.R; r += step) {
+  for (int64_t row = first; row < a.R; row += step) {
+    const int r = static_cast<int>(row);
     int64_t slot = -1;
     int pos = -1;
     if (B > 0 && r < s.off[B]) {
@@ -137,17 +139,18 @@ __global__ __launch_bounds__(NT) void pages_kernel(PagesArgs a) {
         }
       }
     }
-    a.slot[r] = slot;
-    if (a.position) a.position[r] = pos;
+    a.slot[row] = slot;
+    if (a.position) a.position[row] = pos;
   }
   // the takers' new table entries
-  for (int k = first; k < takes && k < top; k += step) {
+  for (int64_t entry_of = first; entry_of < takes && entry_of < top; entry_of += step) {
+    const int k = static_cast<int>(entry_of);
     const int i = last_at_most(s.taken, B, k);
     if (served(i)) a.table[static_cast<int64_t>(i) * a.ld + a.held[i] + (k - s.taken[i])] = entry(top - 1 - k);
   }
   // the givers' pages
-  for (int g = first; g < gives; g += step)
-    if (count + g < a.pool_size) a.pool[count + g] = entry(count + g);
+  for (int64_t g = first; g < gives && count + g < a.pool_size; g += step)
+    a.pool[count + g] = entry(static_cast<int>(count + g));
   // the requests
   for (int i = first; i < B; i += step) {
     const Ask q = ask_of(a, i);
