@@ -12,7 +12,6 @@
 #include <stdlib.h>
 #include <string.h>
 #include <sys/mman.h>
-#include <ucontext.h>
 #include <unistd.h>
 
 #include <algorithm>
@@ -77,15 +76,37 @@ inline void release() {
 // ---- lanes
 enum State { kRunning, kExchange, kBarrier, kDone };
 struct Copy { const char* from; char* to; };
+// Leaves the running stack for another one (registers that a call keeps).
+extern "C" void emu_swap(void** leave, void* enter);
+asm(R"(
+.text
+.type emu_swap, @function
+emu_swap:
+  push %rbp
+  push %rbx
+  push %r12
+  push %r13
+  push %r14
+  push %r15
+  mov %rsp, (%rdi)
+  mov %rsi, %rsp
+  pop %r15
+  pop %r14
+  pop %r13
+  pop %r12
+  pop %rbx
+  pop %rbp
+  ret
+)");
 struct Lane {
-  ucontext_t context;
+  void* at = nullptr;        // its stack's top while it is not running
   State state = kDone;
   int op = 0;
   unsigned count = 0;        // exchanges so far
   std::deque<Copy> loads;    // under way
   std::vector<char> stack;
 };
-inline ucontext_t scheduler;
+inline void* scheduler = nullptr;
 inline std::vector<Lane> lanes;
 inline Lane* me = nullptr;
 inline std::function<void()>* body = nullptr;
@@ -97,7 +118,7 @@ inline std::vector<Slot> board[2];
 inline void yield(State s, int op) {
   me->state = s;
   me->op = op;
-  swapcontext(&me->context, &scheduler);
+  emu_swap(&me->at, scheduler);
 }
 // Every lane of the wave gives `v`; returns where they lie, lane 0 first.
 template <typename T>
@@ -121,7 +142,7 @@ inline void entry() {
   (*body)();
   me->state = kDone;
   if (!me->loads.empty()) fail("a load is under way where the kernel ends");
-  swapcontext(&me->context, &scheduler);
+  emu_swap(&me->at, scheduler);
 }
 
 inline bool early = false;    // loads arrive at once, or where they are waited for
@@ -135,13 +156,13 @@ inline void run_block(int threads, std::function<void()> f) {
   for (int t = 0; t < threads; ++t) {
     Lane& l = lanes[t];
     if (l.stack.empty()) l.stack.resize(256 * 1024);
-    getcontext(&l.context);
-    l.context.uc_stack.ss_sp = l.stack.data();
-    l.context.uc_stack.ss_size = l.stack.size();
-    l.context.uc_link = nullptr;
+    // six registers, entry's address, and a return address that is never used
+    void** top = reinterpret_cast<void**>((reinterpret_cast<uintptr_t>(l.stack.data() + l.stack.size()) & ~uintptr_t{15}) - 64);
+    memset(top, 0, 64);
+    top[6] = reinterpret_cast<void*>(&entry);
+    l.at = top;
     l.state = kRunning;
     l.count = 0;
-    makecontext(&l.context, entry, 0);
   }
   const int waves = threads / kWave;
   for (;;) {
@@ -154,7 +175,7 @@ inline void run_block(int threads, std::function<void()> f) {
         for (int l = 0; l < kWave; ++l) {
           me = &wave[l];
           thread.x = static_cast<unsigned>(w * kWave + l);
-          swapcontext(&scheduler, &me->context);
+          emu_swap(&scheduler, me->at);
         }
         for (int l = 1; l < kWave; ++l)
           if (wave[l].state != wave[0].state || (wave[0].state == kExchange && wave[l].op != wave[0].op)) fail("lanes part at an exchange");
