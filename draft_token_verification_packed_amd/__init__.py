@@ -103,7 +103,8 @@ class Adjust(ctypes.Structure):
                 ("history_len", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
                 ("presence", ctypes.c_void_p), ("bias_offsets", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
                 ("bias_values", ctypes.c_void_p), ("num_bias", ctypes.c_int32), ("mask", ctypes.c_void_p),
-                ("mask_ld", ctypes.c_int64), ("num_masks", ctypes.c_int32), ("mask_index", ctypes.c_void_p)]
+                ("mask_ld", ctypes.c_int64), ("num_masks", ctypes.c_int32), ("mask_index", ctypes.c_void_p),
+                ("num_drafts", ctypes.c_int32)]
 
 
 MAX_PROTECTED = 256
@@ -864,7 +865,9 @@ def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None,
     type.
 
     Row r of request i stands behind the drafts before it (with `parents`:
-    behind those on its path from the root). `history` [B, H] int32 holds each
+    behind those on its path from the root). Requests without rows come last;
+    `draft_tokens` then holds one draft less than there are rows for every
+    request that has some. `history` [B, H] int32 holds each
     request's prompt and output, `prompt_len` and `history_len` [B] how many
     tokens of it are the prompt's and how many there are; `repetition`,
     `frequency` and `presence` are float32 [B]. Biases are lists of tokens and
@@ -880,11 +883,12 @@ def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None,
     R, dev, i32, f32 = logits.shape[0], logits.device, torch.int32, torch.float32
     B = row_offsets.numel() - 1
     off = _in(row_offsets, B + 1, i32, dev, "row_offsets")
-    drafts = None
-    if R > B:
-        if draft_tokens is None:
-            raise ValueError("draft_tokens: %d rows carry drafts" % (R - B))
-        drafts = _in(draft_tokens, R - B, i32, dev, "draft_tokens")
+    # (requests without rows leave more drafts than R - B)
+    D = 0 if draft_tokens is None else draft_tokens.numel()
+    if D < R - B or (D > R > B):
+        raise ValueError("draft_tokens: %d entries, between %d and %d rows carry drafts" % (D, max(R - B, 0), R))
+    drafts = _in(draft_tokens, D, i32, dev, "draft_tokens") if D else None
+    D = min(D, R)
     par = _in(parents, R, i32, dev, "parents")
     hist, hist_ld, width, prompt, used = None, 0, 0, None, None
     if history is not None:
@@ -923,7 +927,7 @@ def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None,
         if out is None:
             out, old = torch.empty((R, V), dtype=logits.dtype, device=dev), V
         a = Adjust(logits.data_ptr(), out.data_ptr(), dtype, V, ld, old, B, R, off, drafts, par, hist, hist_ld, width,
-                   prompt, used, rep, freq, pres, boff, btok, bval, n, mp, mask_ld, masks, midx)
+                   prompt, used, rep, freq, pres, boff, btok, bval, n, mp, mask_ld, masks, midx, D)
         on.keep(logits, row_offsets, draft_tokens, parents, history, history_len, prompt_len, repetition, frequency,
                 presence, bias_offsets, bias_tokens, bias_values, mask, mask_index, out, error_flag)
         _check(lib().vsv_adjust_logits(ctypes.byref(a), err, s))

@@ -473,7 +473,10 @@ vsv_status vsv_adjust_logits(const vsv_adjust* d, int32_t* error_flag, hipStream
     const uintptr_t ye = y + (static_cast<uintptr_t>(d->num_rows - 1) * d->out_ld + d->vocab) * e;
     if (x < ye && y < xe) return VSV_EINVAL;
   }
-  if (!d->row_offsets || (d->num_rows > d->num_requests && !d->draft_tokens)) return VSV_EINVAL;
+  // (requests without rows leave more drafts than num_rows - num_requests)
+  const int64_t least = static_cast<int64_t>(d->num_rows) - d->num_requests;
+  const int64_t drafts = d->num_drafts ? d->num_drafts : least > 0 ? least : 0;
+  if (!d->row_offsets || drafts < least || drafts < 0 || drafts > d->num_rows || (drafts > 0 && !d->draft_tokens)) return VSV_EINVAL;
   if (d->history &&
       (!d->history_len || d->history_width < 0 || d->history_ld < d->history_width ||
        d->history_ld > (INT64_MAX / 4) / d->num_requests))
@@ -511,6 +514,7 @@ vsv_status vsv_adjust_logits(const vsv_adjust* d, int32_t* error_flag, hipStream
   a.mask_ld = d->mask_ld;
   a.mask_rows = d->num_masks;
   a.mask_index = d->mask_index;
+  a.num_drafts = static_cast<int32_t>(drafts);
   a.error_flag = error_flag;
   a.cus = device_cus();
   return vsv::launch_adjust(a, stream) == hipSuccess ? VSV_OK : VSV_EHIP;
@@ -556,6 +560,6 @@ vsv_status vsv_test_withhold_row_word(int32_t row) {
   return VSV_OK;
 }
 
-int32_t vsv_version(void) { return 105; }
+int32_t vsv_version(void) { return 106; }
 
 }  // extern "C"

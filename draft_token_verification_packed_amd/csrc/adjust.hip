@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs a) {
   // the draft that row r > 0 of the request carries
   auto draft_of = [&](int r) {
     const int dq = o0 + r - i - 1;
-    if (dq >= 0 && dq < a.R - a.B) return a.drafts[dq];
+    if (dq >= 0 && dq < a.num_drafts) return a.drafts[dq];
     bits |= VSV_FLAG_LAYOUT;
     return -1;
   };

@@ -15,7 +15,7 @@ struct AdjustArgs {
   int64_t ld, out_ld;
   int32_t V, B, R, dtype;
   const int32_t* offsets;   // [B + 1]
-  const int32_t* drafts;    // [R - B]
+  const int32_t* drafts;    // [num_drafts]
   const int32_t* parents;   // [R], or NULL: chains
   const int32_t* history;   // [B, hist_ld] or NULL
   int64_t hist_ld;
@@ -33,6 +33,7 @@ struct AdjustArgs {
   int64_t mask_ld;
   int32_t mask_rows;
   const int32_t* mask_index;    // [R], or NULL: row r's mask is row r
+  int32_t num_drafts;
   int32_t* error_flag;
   int32_t cus;
   // set at launch

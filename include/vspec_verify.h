@@ -521,7 +521,8 @@ typedef struct {
   const int32_t* row_offsets;   /* [B + 1], not falling, within 0 .. R: requests        */
                                 /* without rows come last, and rows at or beyond        */
                                 /* off[B] are left as they are                          */
-  const int32_t* draft_tokens;  /* [R - B], NULL when R <= B                            */
+  const int32_t* draft_tokens;  /* [num_drafts], may be NULL when R <= B and no row     */
+                                /* carries one                                          */
   const int32_t* parents;       /* [R] as in vsv_verify_greedy_tree (at most            */
                                 /* VSV_MAX_TREE_ROWS rows a request), NULL: chains of   */
                                 /* any length                                           */
@@ -544,6 +545,9 @@ typedef struct {
   int32_t num_masks;
   const int32_t* mask_index;    /* [R] row of `mask`, negative: the row is not masked;  */
                                 /* NULL: row r's mask is row r                          */
+  int32_t num_drafts;           /* entries of draft_tokens, R - B .. R: with requests   */
+                                /* that have no rows there are more drafts than R - B;  */
+                                /* 0: R - B                                             */
 } vsv_adjust;
 
 /* VSV_FLAG_TOKEN: a token of a history, path or bias outside the vocabulary

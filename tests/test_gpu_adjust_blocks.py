@@ -40,3 +40,31 @@ def test_blocks_of_several_rows(vsv, dtype, kind, counts, V, H):
     c = _case(V, counts, V, dtype, kind, 1, H=H, bias=30, tokens=300)
     print("adjust blocks %d rows V=%d H=%d dtype=%d" % (c["R"], V, H, dtype), flush=True)
     _both(vsv, c, chain=kind == "chain")
+
+
+@pytest.mark.parametrize("kind", ["chain", "wide"])
+@pytest.mark.parametrize("counts,empty", [([5, 4, 3], 2), ([2], 3), ([1, 1, 6], 9)])
+def test_requests_without_rows_leave_every_draft(vsv, kind, counts, empty):
+    """No padding rows: the batch ends with the last request that has rows,
+    and holds more drafts than rows less requests."""
+    import torch
+    c = _case(21, counts, 300, oracle.F32, kind, tokens=40)
+    c["off"] = np.concatenate((c["off"], np.full(empty, c["off"][-1], dtype=np.int32)))
+    for k in ("history", "history_len", "prompt_len", "repetition", "frequency", "presence"):
+        c[k] = np.concatenate((c[k], np.repeat(c[k][:1], empty, 0)))
+    c["bias_offsets"] = np.concatenate((c["bias_offsets"], np.repeat(c["bias_offsets"][-1:], empty)))
+    assert len(c["drafts"]) == c["R"] - len(counts) > c["R"] - len(counts) - empty
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _check(_call(vsv, c, chain=kind == "chain", error_flag=err), c)
+    assert int(err) == 0
+    for n in (c["R"] + 1, c["R"] - len(counts) - empty - 1):
+        if c["R"] > len(counts) + empty and n >= 0:
+            with pytest.raises(ValueError):
+                _call(vsv, dict(c, drafts=np.zeros(n, dtype=np.int32)))
+
+
+def test_drafts_of_single_rows_are_not_read(vsv):
+    c = _case(22, [1] * 5, 300, oracle.F32)
+    want = host(_call(vsv, c))
+    for n in (0, 3, 9):
+        assert np.array_equal(host(_call(vsv, dict(c, drafts=np.full(n, 7, dtype=np.int32)))), want, equal_nan=True)
