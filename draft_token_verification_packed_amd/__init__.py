@@ -817,7 +817,8 @@ def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, 
     verify_greedy_tree, None: chains) and itself. All matrices are bfloat16 or
     all float32, D is 64, 128 or (bfloat16) 256, and pointers and strides are
     multiples of 16 bytes. `scale` is D ** -0.5 by default. Returns out
-    [R, H, D] (`out` if given; rows of no request are left as they are), and
+    [R, H, D] (`out` if given, which shares no memory with the inputs; rows of
+    no request are left as they are), and
     with return_lse also the scores' log-sum-exp [R, H]. Rows get no gradient."""
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q and k must be [rows, heads, dim], the caches [pages, page_size, heads, dim]")

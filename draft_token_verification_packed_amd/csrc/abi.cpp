@@ -10,6 +10,7 @@
 #include "allocate.hpp"
 #include "attention.hpp"
 #include "kernels.hpp"
+#include "overlap.hpp"
 #include "pages.hpp"
 #include "probabilistic.hpp"
 #include "rows.hpp"
@@ -431,6 +432,20 @@ vsv_status vsv_tree_attention(const vsv_attention* d, int32_t* error_flag, void*
   a.scale = static_cast<float>(1.44269504088896340736 * static_cast<double>(d->scale));
   if (!(a.scale > 0.f) || !(a.scale < INFINITY)) return VSV_EINVAL;
   if (!workspace || !aligned(workspace, vsv::kWsAlign) || workspace_bytes < vsv::attention_workspace(a)) return VSV_EWORKSPACE;
+  // results go where no other workgroup still reads
+  const int64_t e = static_cast<int64_t>(elem_size(d->dtype)), row = d->head_dim * e;
+  const int64_t R = d->num_rows, H = d->num_heads, KV = d->num_kv_heads;
+  const vsv::Places out{d->out, row, {d->out_row * e, d->out_head * e, 0}, {R, H, 1}};
+  const int64_t cache_stride[3] = {d->cache_page * e, d->cache_token * e, d->cache_head * e};
+  const vsv::Places others[] = {{d->q, row, {d->q_row * e, d->q_head * e, 0}, {R, H, 1}},
+                                {d->k, row, {d->k_row * e, d->k_head * e, 0}, {R, KV, 1}},
+                                {d->v, row, {d->v_row * e, d->v_head * e, 0}, {R, KV, 1}},
+                                {d->k_cache, row, {cache_stride[0], cache_stride[1], cache_stride[2]}, {d->num_pages, d->page_size, KV}},
+                                {d->v_cache, row, {cache_stride[0], cache_stride[1], cache_stride[2]}, {d->num_pages, d->page_size, KV}},
+                                {d->lse ? d->lse : workspace, d->lse ? R * H * 4 : 1, {0, 0, 0}, {1, 1, 1}},
+                                {workspace, static_cast<int64_t>(vsv::attention_workspace(a)), {0, 0, 0}, {1, 1, 1}}};
+  for (const vsv::Places& p : others)
+    if (vsv::places_meet(out, p)) return VSV_EINVAL;
   a.q = d->q;
   a.k = d->k;
   a.v = d->v;

@@ -491,6 +491,8 @@ typedef struct {
  * no earlier row (the row then sees the context and itself alone);
  * VSV_FLAG_PAGES: a page outside 0 .. num_pages - 1 (page 0 is read for it).
  * Errors: VSV_EINVAL (NULL pointers, sizes, strides, alignment, dtype, scale;
+ * an out that shares memory with another matrix, lse or the workspace (slices
+ * of the same rows are told apart; a matrix that overlaps itself counts whole);
  * num_rows * num_heads beyond 2^31 - 1; table_width * page_size beyond it, or
  * so large that a request's work could pass 2^31 tiles), VSV_EWORKSPACE,
  * VSV_EHIP. */
