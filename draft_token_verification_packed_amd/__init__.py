@@ -32,6 +32,7 @@ import itertools
 import os
 
 import torch  # load torch's HIP runtime first so the library binds to it
+from torch.autograd import forward_ad as _fwd
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvspec_verify.so")
@@ -718,7 +719,7 @@ def distill_loss(student_logits, teacher_ids, teacher_logits, teacher_lse=None, 
     Columns at or beyond `vocab` are not part of the rows. A step
     captured into a graph needs leaves of its own (made for the capture, or
     without a live eager graph), as any torch backward pass does."""
-    if torch.autograd.forward_ad.unpack_dual(student_logits).tangent is not None:
+    if _fwd.unpack_dual(student_logits).tangent is not None:
         raise NotImplementedError("distill_loss has no forward-mode derivative")
     if vocab is not None and int(vocab) != student_logits.shape[1]:
         if not 1 <= int(vocab) <= student_logits.shape[1]:
@@ -740,6 +741,17 @@ def _in(t, n, dtype, device, name):
         _vec(t, n, dtype, name)
         _same_device(device, t)
     return t.data_ptr()
+
+
+def _no_gradient(name, *tensors):
+    """Refuses tensors that ask for a derivative (None: not given)."""
+    backward = torch.is_grad_enabled()
+    # (tangents live inside a dual level alone: the look at every tensor costs
+    # 3 us of a call's 14 to 20)
+    forward = getattr(_fwd, "_current_level", 0) >= 0
+    for t in tensors:
+        if t is not None and ((backward and t.requires_grad) or (forward and _fwd.unpack_dual(t).tangent is not None)):
+            raise NotImplementedError("%s has no derivative" % name)
 
 
 def _cuda(t, name):
@@ -819,7 +831,9 @@ def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, 
     multiples of 16 bytes. `scale` is D ** -0.5 by default. Returns out
     [R, H, D] (`out` if given, which shares no memory with the inputs; rows of
     no request are left as they are), and
-    with return_lse also the scores' log-sum-exp [R, H]. Rows get no gradient."""
+    with return_lse also the scores' log-sum-exp [R, H]. Tensors that ask for
+    a derivative, backward or forward, are refused."""
+    _no_gradient("tree_attention", q, k, v, k_cache, v_cache, out)
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q and k must be [rows, heads, dim], the caches [pages, page_size, heads, dim]")
     dtype, dev, i32 = _dtype_code(q), _cuda(q, "q"), torch.int32
@@ -830,9 +844,6 @@ def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, 
     cs = _heads(k_cache, (pages, page, KV, D), q.dtype, dev, "k_cache")
     if _heads(v_cache, (pages, page, KV, D), q.dtype, dev, "v_cache") != cs:
         raise ValueError("k_cache and v_cache must have the same strides")
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or k_cache.requires_grad or
-                                    v_cache.requires_grad):
-        raise NotImplementedError("tree_attention has no backward pass")
     off = _in(row_offsets, B + 1, i32, dev, "row_offsets")
     lens = _in(length, B, i32, dev, "length")
     par = _in(parents, R, i32, dev, "parents")
@@ -877,9 +888,9 @@ def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None,
     v // 32 is set, and `mask_index` [R] names each row's (negative: none;
     None: row r has mask r). `out` may be a matrix like the logits or the logits
     themselves, of which only the touched elements then move; rows of no
-    request are left as they are in it. Rows get no gradient."""
-    if logits.requires_grad and torch.is_grad_enabled():
-        raise NotImplementedError("adjust_logits has no backward pass")
+    request are left as they are in it. Tensors that ask for a derivative,
+    backward or forward, are refused."""
+    _no_gradient("adjust_logits", logits, repetition, frequency, presence, bias_values, out)
     dtype, V, ld = _logits(logits, vocab)
     R, dev, i32, f32 = logits.shape[0], logits.device, torch.int32, torch.float32
     B = row_offsets.numel() - 1
