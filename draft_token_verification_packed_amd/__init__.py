@@ -958,7 +958,10 @@ def plan_pages(block_table, held, length, row_offsets, free_pages, free_count, p
     for rows of no request), held, length and free_count behind the call, and
     error_flag (FLAG_PAGES: the pool ran out, and the requests it could not
     serve are as they were)."""
-    B, R, i32, dev = row_offsets.numel() - 1, int(num_rows), torch.int32, _cuda(row_offsets, "row_offsets")
+    R, page = int(num_rows), int(page_size)
+    if not 0 <= R < 2 ** 31 or not 0 <= page < 2 ** 31:      # (ctypes would take them modulo 2^32)
+        raise ValueError("num_rows and page_size must be within 0 .. 2^31 - 1")
+    B, i32, dev = row_offsets.numel() - 1, torch.int32, _cuda(row_offsets, "row_offsets")
     off = _in(row_offsets, B + 1, i32, dev, "row_offsets")
     had = _in(held, B, i32, dev, "held")
     lens = _in(length, B, i32, dev, "length")
@@ -966,8 +969,6 @@ def plan_pages(block_table, held, length, row_offsets, free_pages, free_count, p
     free = _in(free_pages, pool, i32, dev, "free_pages")
     count = _in(free_count, 1, i32, dev, "free_count")
     table, table_ld = _matrix(block_table, B, 0, dev, "block_table")
-    if R < 0:
-        raise ValueError("num_rows must not be negative")
     on = _on(dev, stream)
     with on as s:
         slot = torch.empty(R, dtype=torch.int64, device=dev)
@@ -977,7 +978,7 @@ def plan_pages(block_table, held, length, row_offsets, free_pages, free_count, p
         base = words.data_ptr()
         on.keep(block_table, held, length, row_offsets, free_pages, free_count)
         _check(lib().vsv_plan_pages(table, table_ld, block_table.shape[1], had, lens, off, B, R, free, pool, count,
-                                    int(page_size), slot.data_ptr(), base, base + 4 * R, base + 4 * (R + B),
+                                    page, slot.data_ptr(), base, base + 4 * R, base + 4 * (R + B),
                                     base + 4 * (R + 2 * B), flag.data_ptr(), s))
     return dict(slot=slot, position=position, held=new_held, length=new_length, free_count=new_count, error_flag=flag)
 
