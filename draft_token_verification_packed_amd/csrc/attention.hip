@@ -234,6 +234,8 @@ __device__ __forceinline__ bool not_finite(uint32_t one, std::integral_constant<
 // A load of 16 bytes a lane straight into LDS, at `to` + 16 * lane. The
 // compiler makes every later LDS read wait for its own form of this load, the
 // reads of the other buffer included; here the wait is wait_loads() alone.
+// (m0 is reserved: the compiler keeps no value in it, so it is not named among
+// what is written, and it writes m0 nowhere else in these kernels.)
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
 }
