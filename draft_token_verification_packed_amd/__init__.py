@@ -829,9 +829,13 @@ def tree_attention(q, k, v, row_offsets, k_cache, v_cache, block_table, length, 
     verify_greedy_tree, None: chains) and itself. All matrices are bfloat16 or
     all float32, D is 64, 128 or (bfloat16) 256, and pointers and strides are
     multiples of 16 bytes. `scale` is D ** -0.5 by default. Returns out
-    [R, H, D] (`out` if given, which shares no memory with the inputs; rows of
-    no request are left as they are), and
-    with return_lse also the scores' log-sum-exp [R, H]. Tensors that ask for
+    [R, H, D] (`out` if given, which shares no memory with the inputs), and
+    with return_lse also the scores' log-sum-exp [R, H]. Rows of no request,
+    and of requests whose offsets or lengths make no sense, are left as they
+    are in a given `out` and hold nothing of meaning in a new one. Device
+    conditions set bits in `error_flag` (int32 [1]) if given: FLAG_LAYOUT for
+    offsets, lengths or parents, FLAG_PAGES for a page that the caches do not
+    have. Tensors that ask for
     a derivative, backward or forward, are refused."""
     _no_gradient("tree_attention", q, k, v, k_cache, v_cache, out)
     if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
@@ -887,8 +891,11 @@ def adjust_logits(logits, row_offsets, draft_tokens, parents=None, history=None,
     [M, (vocab + 31) // 32] int32 allows token v where bit v % 32 of word
     v // 32 is set, and `mask_index` [R] names each row's (negative: none;
     None: row r has mask r). `out` may be a matrix like the logits or the logits
-    themselves, of which only the touched elements then move; rows of no
-    request are left as they are in it. Tensors that ask for a derivative,
+    themselves, of which only the touched elements then move. Rows of no
+    request, and of requests whose offsets make no sense, are left as they are
+    in a given `out` and hold nothing of meaning in a new one. Device
+    conditions set bits in `error_flag` (int32 [1]) if given: FLAG_LAYOUT,
+    FLAG_TOKEN and FLAG_PARAMS. Tensors that ask for a derivative,
     backward or forward, are refused."""
     _no_gradient("adjust_logits", logits, repetition, frequency, presence, bias_values, out)
     dtype, V, ld = _logits(logits, vocab)

@@ -8,17 +8,19 @@
 //   y = y - f c - p [c > 0]
 //   y = y + b
 //   y = -inf where the row's grammar mask has a 0 bit
-// in float32, rounded once to the logits' type.
+// in float32 (x / rho as x times the rounded reciprocal), rounded once to the
+// logits' type.
 //
 // A workgroup takes a slice of one request's vocabulary and holds a word per
 // token of it in LDS: twice the count, plus one if the token is in the
-// prompt. It reads the request's history once, counting the tokens inside the slice
+// prompt. It reads the request's history, counting the tokens inside the slice
 // with LDS atomics on integers (their order cannot show), and then streams
-// its slice of the request's rows one after another, moving the counts from
+// its slice of a block of the request's rows one after another, moving the counts from
 // row to row by the drafts that the paths do not share. A bit per token
 // tells the stream which 8 logits to look up at all, so the untouched rest
-// goes from load to store as it is. The history is read once per slice from
-// L2 instead of once per row, and no dense count matrix exists.
+// goes from load to store as it is. The history is read once per slice
+// and block of rows (mostly from L2) instead of once per row, and no dense
+// count matrix exists.
 // Bound by HBM: each logit read and written once. 640 rows of 152064 bf16
 // logits with histories of up to 1024 tokens, biases and half the rows masked
 // take 90 us, 4.4 TB/s (the same rows copied by this kernel 79, 5.0); 397

@@ -31,9 +31,11 @@
 // to different waves, joined through LDS at the end of an item. With few
 // queries (WQ = 1) waves share nothing and meet no barrier in the loop.
 //
-// Few queries are bound by HBM, many by the matrix and vector units in turn
-// (waves that share a slice meet at every tile, so products and softmax
-// overlap in part only). On one MI355X, key heads of 128 columns, bfloat16:
+// Few queries are bound by HBM, many by waiting: waves that share a slice
+// meet at every tile, some with two blocks of 16 queries and some with one
+// (trees: a wave waits 44 % of its time and waits to issue another 26 %;
+// matrix units are busy 53,000 of about 250,000 cycles, vector instructions
+// take 74,000). On one MI355X, key heads of 128 columns, bfloat16:
 //   128 requests x 5 rows, 200-1019 tokens, 40 / 8 heads   98 us  3.4 TB/s
 //     (the loads alone 69; joining and storing 1024 items about 25)
 //   2 requests x 3-8 rows, 49-65 thousand tokens, 64 / 8  108 us  4.3 TB/s

@@ -510,7 +510,8 @@ vsv_status vsv_tree_attention(const vsv_attention* a, int32_t* error_flag, void*
  *   y = y - frequency[i] * c - (c > 0 ? presence[i] : 0)
  *   y = y + bias of the token (the last entry that names it)
  *   y = -inf where the row's mask has a 0 bit
- * in float32, rounded once. A mask may leave a row nothing (all -inf). */
+ * in float32 (the division as a product with the rounded reciprocal), rounded
+ * once to the logits' type. A mask may leave a row nothing (all -inf). */
 typedef struct {
   const void* logits;           /* [num_rows, ld]                                       */
   void* out;                    /* [num_rows, out_ld], or the logits themselves with    */
