@@ -107,7 +107,8 @@ constexpr int kSliceTokens = 2048;
 constexpr int kMostRows = 8;         // rows of a request a workgroup takes at a time
 constexpr int kShortHistory = 4096;  // tokens
 
-struct AdjustScratch {
+// (words are read four at a time)
+struct alignas(16) AdjustScratch {
   uint32_t count[kSliceTokens];       // 2 * occurrences in output and path, + 1 if in the prompt
   uint32_t bias[kSliceTokens];        // the last entry's number + 1, then its value's bits
   uint32_t touched[kSliceTokens / 32];

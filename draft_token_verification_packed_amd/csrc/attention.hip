@@ -141,7 +141,7 @@ struct Request {
 };
 
 template <typename E, int D, int QT, int WQ, int WK>
-struct AttnScratch {
+struct alignas(16) AttnScratch {
   using S = Shape<E, D, QT, WQ, WK>;
   union {
     struct {

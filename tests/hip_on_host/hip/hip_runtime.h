@@ -233,6 +233,11 @@ inline uint32_t __float_as_uint(float v) { return __builtin_bit_cast(uint32_t, v
 inline float __log2f(float v) { return log2f(v); }
 inline uint32_t __umulhi(uint32_t a, uint32_t b) { return static_cast<uint32_t>((static_cast<uint64_t>(a) * b) >> 32); }
 template <typename T, typename U> T atomicOr(T* p, U v) { T old = *p; *p = static_cast<T>(old | v); return old; }
+template <typename T, typename U> T atomicAdd(T* p, U v) { T old = *p; *p = static_cast<T>(old + v); return old; }
+template <typename T, typename U> T atomicMax(T* p, U v) { T old = *p; if (v > old) *p = v; return old; }
+// (at any address that its type allows)
+#define __builtin_nontemporal_load(p) (*(p))
+#define __builtin_nontemporal_store(v, p) (*(p) = (v))
 template <typename T> T emu_load(T* p) { return *p; }
 #define __hip_atomic_load(p, ...) emu_load(p)
 #define __hip_atomic_store(p, v, ...) (*(p) = (v))
