@@ -144,3 +144,48 @@ def test_mixed_batches(vsv):
     c.update(off=off, par=par)
     c["dev"][0], c["dev"][3] = to_dev(off), to_dev(par)
     _check(c, *_call(vsv, c), [0, 6, 7, 8, 29, 31, 59])
+
+
+def _plain(seed, counts, lens, H, KV, D, page, dtype):
+    """A batch of given rows and lengths."""
+    import torch
+    rng = np.random.default_rng(seed)
+    c = _case(seed, dtype, D, 16, KV, len(counts), (0, 1), page)
+    off, _, par = layout(rng, counts)
+    length = np.array(lens, dtype=np.int32)
+    used = -(-length // page)
+    pages = int(used.sum()) + 2
+    ids, at = rng.permutation(pages).astype(np.int32), 0
+    table = np.full((len(counts), int(used.max()) + 1), -7, dtype=np.int32)
+    for i, n in enumerate(used):
+        table[i, :n] = ids[at:at + n]
+        at += n
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    f = lambda *s: torch.randn(*s, device="cuda", generator=g).to(getattr(torch, dtype))
+    R = int(off[-1])
+    c.update(q=f(R, H, D), k=f(R, KV, D), v=f(R, KV, D), kc=f(pages, page, KV, D), vc=f(pages, page, KV, D), off=off, par=par,
+             length=length, table=table, dev=[to_dev(a) for a in (off, table, length, par)])
+    return c
+
+
+@pytest.mark.parametrize("dtype,counts,lens,H,KV,page", [
+    ("bfloat16", [64, 3], [2000, 700], 128, 1, 16),          # one key head: 8192 queries in many blocks
+    ("float32", [20, 64], [300, 1000], 96, 1, 32),
+    ("bfloat16", [5, 2, 9], [5000, 70000, 0], 10, 2, 65536),  # pages longer than a context
+    ("float32", [1, 4], [70000, 3], 4, 2, 131072),
+])
+def test_shapes_at_the_ends(vsv, dtype, counts, lens, H, KV, page):
+    c = _plain(3, counts, lens, H, KV, 64, page, dtype)
+    print("attention ends %s %s" % (dtype, counts), flush=True)
+    _check(c, *_call(vsv, c), range(len(counts)))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_thousands_of_requests(vsv, dtype):
+    # more requests than a workgroup has threads, many of them without rows
+    rng = np.random.default_rng(4)
+    counts = rng.integers(0, 4, 9000)
+    counts[5000:7000] = 0
+    lens = rng.integers(0, 60, 9000)
+    c = _plain(5, counts, lens, 4, 2, 64, 16, dtype)
+    _check(c, *_call(vsv, c), [int(i) for i in np.flatnonzero(counts)[::211]])
