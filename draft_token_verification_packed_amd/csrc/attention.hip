@@ -983,17 +983,35 @@ int workers_of(const AttentionArgs& a) {
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
+// An instantiation, and what a call of it needs: workgroups, and where the
+// parts of its scratch lie.
+template <typename E, int D, int QT, int WQ, int WK> struct Kernel {};
+struct Scratch {
+  int workers;
+  size_t part_ml, part, bytes;
+};
 template <typename E, int D, int QT, int WQ, int WK>
-hipError_t launch_t(AttentionArgs a, hipStream_t s) {
+Scratch scratch_of(Kernel<E, D, QT, WQ, WK>, const AttentionArgs& a) {
   using S = Shape<E, D, QT, WQ, WK>;
+  Scratch c;
+  c.workers = workers_of(a) / 2 * S::kGroups;
+  const size_t pieces = static_cast<size_t>(c.workers) * 2 * S::kMT;
+  c.part_ml = align256(static_cast<size_t>(c.workers) * sizeof(int4));
+  c.part = c.part_ml + align256(pieces * sizeof(float2));
+  c.bytes = c.part + align256(pieces * D * sizeof(float));
+  return c;
+}
+
+template <typename E, int D, int QT, int WQ, int WK>
+hipError_t launch_t(Kernel<E, D, QT, WQ, WK> kernel, AttentionArgs a, hipStream_t s) {
+  using S = Shape<E, D, QT, WQ, WK>;
+  const Scratch c = scratch_of(kernel, a);
   a.G = a.H / a.KV;
-  a.workers = workers_of(a) / 2 * S::kGroups;
+  a.workers = c.workers;
   char* p = static_cast<char*>(a.work);
   a.piece = reinterpret_cast<int4*>(p);
-  p += align256(static_cast<size_t>(a.workers) * 16);
-  a.part_ml = reinterpret_cast<float2*>(p);
-  p += align256(static_cast<size_t>(a.workers) * 2 * S::kMT * 8);
-  a.part = reinterpret_cast<float*>(p);
+  a.part_ml = reinterpret_cast<float2*>(p + c.part_ml);
+  a.part = reinterpret_cast<float*>(p + c.part);
   attention_kernel<E, D, QT, WQ, WK><<<dim3(a.workers), dim3(S::kThreads), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -1001,16 +1019,26 @@ hipError_t launch_t(AttentionArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename E, int D>
-hipError_t launch_d(const AttentionArgs& a, hipStream_t s) {
+// f of the instantiation that a call takes.
+template <typename E, int D, typename F>
+auto with_blocks(const AttentionArgs& a, F f) {
   const int mt = plan_of(a).mt;
-  if (mt == 16) return launch_t<E, D, 1, 1, 4>(a, s);
-  if (mt == 32) return launch_t<E, D, 2, 1, 4>(a, s);
-  if (mt == 64) return launch_t<E, D, 2, 2, 2>(a, s);
+  if (mt == 16) return f(Kernel<E, D, 1, 1, 4>());
+  if (mt == 32) return f(Kernel<E, D, 2, 1, 4>());
+  if (mt == 64) return f(Kernel<E, D, 2, 2, 2>());
   if constexpr (D <= 128) {
-    if (mt == 256) return launch_t<E, D, 2, 8, 1>(a, s);
+    if (mt == 256) return f(Kernel<E, D, 2, 8, 1>());
   }
-  return launch_t<E, D, 2, 4, 1>(a, s);
+  return f(Kernel<E, D, 2, 4, 1>());
+}
+template <typename F>
+auto with_kernel(const AttentionArgs& a, F f) {
+  if (a.dtype == VSV_BF16) {
+    if (a.D == 64) return with_blocks<uint16_t, 64>(a, f);
+    if (a.D == 128) return with_blocks<uint16_t, 128>(a, f);
+    return with_blocks<uint16_t, 256>(a, f);
+  }
+  return a.D == 64 ? with_blocks<float, 64>(a, f) : with_blocks<float, 128>(a, f);
 }
 
 }  // namespace
@@ -1025,18 +1053,11 @@ int64_t attention_tiles(const AttentionArgs& a) {
 }
 
 size_t attention_workspace(const AttentionArgs& a) {
-  const Plan p = plan_of(a);
-  const size_t w = static_cast<size_t>(workers_of(a));
-  return align256(w * 16) + align256(w * 2 * p.mt * 8) + align256(w * 2 * p.mt * a.D * 4);
+  return with_kernel(a, [&](auto kernel) { return scratch_of(kernel, a).bytes; });
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
-  if (a.dtype == VSV_BF16) {
-    if (a.D == 64) return launch_d<uint16_t, 64>(a, s);
-    if (a.D == 128) return launch_d<uint16_t, 128>(a, s);
-    return launch_d<uint16_t, 256>(a, s);
-  }
-  return a.D == 64 ? launch_d<float, 64>(a, s) : launch_d<float, 128>(a, s);
+  return with_kernel(a, [&](auto kernel) { return launch_t(kernel, a, s); });
 }
 
 }  // namespace vsv

@@ -28,7 +28,7 @@ template <> uint16_t narrow(float f) { return __builtin_bit_cast(uint16_t, __tru
 struct Span { const char* lo; std::vector<bool> may; };   // an array's chunks of 16 bytes
 
 template <typename E>
-int batch(int D, int H, int KV, int page, int cus, int B, int rows_lo, int rows_hi, int len_lo, int len_hi, int kind, int seed) {
+int batch(int D, int H, int KV, int page, int cus, int B, int rows_lo, int rows_hi, int len_lo, int len_hi, int kind, int seed, int block) {
   std::mt19937 rng(seed);
   auto pick = [&](int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); };
   std::normal_distribution<float> normal;
@@ -140,6 +140,11 @@ int batch(int D, int H, int KV, int page, int cus, int B, int rows_lo, int rows_
       return 2;
     }
   }
+  // the scratch is the launch's workgroups' own
+  const size_t workers = emu::launches[0], pieces = workers * 2 * block;
+  auto whole = [](size_t b) { return (b + 255) / 256 * 256; };
+  if (emu::launches.size() != 8 || scratch != whole(workers * 16) + whole(pieces * 8) + whole(pieces * D * 4))
+    return printf("%zu bytes of scratch for %zu workgroups\n", scratch, workers), 7;
   if (!malformed && *flag) return printf("flags %d\n", *flag), 4;
   // against 64 bits; tolerances as in tests/test_gpu_attention.py, with the
   // sum of |q k| of each token in place of a bound for all of them
@@ -197,5 +202,5 @@ int main(int argc, char** argv) {
   std::vector<int> n;
   for (int k = 1; k < argc; ++k) n.push_back(atoi(argv[k]));
   auto f = n[0] ? batch<uint16_t> : batch<float>;
-  return f(n[1], n[2], n[3], n[4], n[5], n[6], n[7], n[8], n[9], n[10], n[11], n[12]);
+  return f(n[1], n[2], n[3], n[4], n[5], n[6], n[7], n[8], n[9], n[10], n[11], n[12], n[13]);
 }

@@ -189,9 +189,11 @@ inline void run_block(int threads, std::function<void()> f) {
   }
 }
 
+inline std::vector<unsigned> launches;   // workgroups of every launch
 template <typename K, typename A>
 void launch(K kernel, dim3 groups, dim3 threads, const A& args) {
   grid.x = groups.x;
+  launches.push_back(groups.x);
   for (unsigned k = 0; k < groups.x; ++k) {
     block.x = backward ? groups.x - 1 - k : k;
     if (only >= 0 && block.x != static_cast<unsigned>(only)) continue;

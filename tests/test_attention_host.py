@@ -1,8 +1,8 @@
 """The attention kernel's own source on the CPU (hip_on_host/), with so few
 workgroups that each one takes many tiles, items and requests: the refill of
 its buffers, cuts inside and at the borders of items, the second look-up of
-pages, and the counted waits. Every access is checked, and results are held
-against sums in 64 bits (attention_host.cpp)."""
+pages, and the counted waits. Every access is checked, the scratch has the size
+that its workgroups use, and results are held against sums in 64 bits (attention_host.cpp)."""
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -10,7 +10,7 @@ import pytest
 from tests import host_kernel
 
 # query heads a key head, rows of a request: blocks of 16, 32, 64, 128 and 256 queries
-BLOCKS = {16: (2, 2, 8), 32: (5, 4, 7), 64: (8, 4, 8), 128: (8, 9, 16), 256: (8, 15, 36)}
+BLOCKS = {16: (2, 2, 8), 32: (5, 4, 6), 64: (8, 5, 8), 128: (8, 9, 16), 256: (8, 17, 36)}
 TYPES = [(b, d) for b in (0, 1) for d in (64, 128, 256) if b or d < 256]
 KERNELS = [(b, d, m) for b, d in TYPES for m in BLOCKS if d < 256 or m < 256]
 TREE, CHAIN, RISING, MALFORMED = range(4)
@@ -26,7 +26,7 @@ def program(tmp_path_factory):
 
 def _run(program, bf16, D, block, kv, page, cus, B, lens, kind, seed):
     G, lo, hi = BLOCKS[block]
-    out = host_kernel.run(program, bf16, D, G * kv, kv, page, cus, B, lo, hi, lens[0], lens[1], kind, seed)
+    out = host_kernel.run(program, bf16, D, G * kv, kv, page, cus, B, lo, hi, lens[0], lens[1], kind, seed, block)
     assert "ok" in out
 
 
