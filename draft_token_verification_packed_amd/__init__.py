@@ -747,11 +747,11 @@ def _no_gradient(name, *tensors):
     """Refuses tensors that ask for a derivative (None: not given)."""
     # (tangents live inside a dual level alone: the look at every tensor costs
     # 3 us of a call's 14 to 20)
-    forward = getattr(_fwd, "_current_level", 0) >= 0
-    for t in tensors:
-        if t is not None and ((t.requires_grad and torch.is_grad_enabled()) or
-                              (forward and _fwd.unpack_dual(t).tangent is not None)):
-            raise NotImplementedError("%s has no derivative" % name)
+    backward, forward = torch.is_grad_enabled(), getattr(_fwd, "_current_level", 0) >= 0
+    if backward or forward:
+        for t in tensors:
+            if t is not None and ((backward and t.requires_grad) or (forward and _fwd.unpack_dual(t).tangent is not None)):
+                raise NotImplementedError("%s has no derivative" % name)
 
 
 def _cuda(t, name):
